@@ -1,6 +1,7 @@
 """GB300 (sm_103a) fused MXFP4-weight mixture-of-experts layer.
 
-Thin Python binding over the C ABI in ``include/kt_moe.h`` (library
+Thin Python binding over the C ABI in ``include/kt_moe.h`` and, for the attention
+operators in front of the layer (``attention.py``), ``include/kt_attn.h`` (library
 ``_build/libkt_moe.so``, built by ``build_ext.build``).  Every step of the
 layer runs in the library's CUDA kernels; this module only checks shapes,
 allocates outputs/workspaces with torch and passes raw device pointers and
@@ -25,6 +26,7 @@ __all__ = [
     "KTError", "lib", "route_permute", "forward", "workspace_bytes", "workspace_layout", "read_device_error",
     "grouped_gemm_f32", "Layerwise", "status_string", "check_fc_shapes", "kernel_launches", "profile_enable",
     "profile_read", "STAGES", "route_permute_noalloc", "decode", "DECODE_MAX_SLOTS", "MoeLayer",
+    "PagedKV", "qk_norm_rope", "rope_table",
 ]
 
 KT_OK = 0
@@ -112,7 +114,7 @@ def lib(build_if_missing: bool = True):
         if _lib is None:
             path = build_ext.build() if build_if_missing else build_ext.LIB_PATH
             L = ctypes.CDLL(path)
-            for name, (args, res) in _SIGNATURES.items():
+            for name, (args, res) in {**_SIGNATURES, **attention.SIGNATURES}.items():
                 fn = getattr(L, name)
                 fn.argtypes = args
                 fn.restype = res
@@ -582,3 +584,7 @@ class Layerwise:
             self.close()
         except Exception:  # noqa: BLE001 - interpreter shutdown
             pass
+
+
+from . import attention  # noqa: E402 - needs the helpers above
+from .attention import PagedKV, qk_norm_rope, rope_table  # noqa: E402

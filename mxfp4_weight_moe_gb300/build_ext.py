@@ -3,7 +3,7 @@
 Each translation unit under ``csrc/`` is compiled by nvcc in parallel
 (``-gencode arch=compute_103a,code=sm_103a``), then linked with the static
 CUDA runtime into one shared library exporting the C ABI of
-``include/kt_moe.h``.  No torch types cross that boundary.
+``include/kt_moe.h`` and ``include/kt_attn.h``.  No torch types cross that boundary.
 """
 from __future__ import annotations
 
@@ -39,7 +39,7 @@ def sources() -> list[str]:
 def _fingerprint(extra: list[str]) -> str:
     h = hashlib.sha256()
     for f in sources() + sorted(glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))) + \
-            [os.path.join(INCLUDE, "kt_moe.h")]:
+            sorted(glob.glob(os.path.join(INCLUDE, "*.h"))):
         with open(f, "rb") as fh:
             h.update(f.encode() + fh.read())
     h.update(" ".join(extra).encode())

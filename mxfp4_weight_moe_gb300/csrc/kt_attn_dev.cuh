@@ -1,0 +1,208 @@
+// kt_attn_dev.cuh -- device helpers of the paged-attention kernels: sequence
+// geometry, the even division of all sequences' work among the CTAs, page
+// look-up and the loads and matrix instructions both kernels use.
+#pragma once
+
+#include <math.h>
+
+#include "kt_attn_internal.h"
+#include "kt_common.cuh"
+
+namespace kt {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct AttnShape {
+    const int32_t* block_table;
+    long long table_stride;
+    const int32_t* cu_q;
+    const int32_t* seq_lens;
+    const float* sinks;
+    int* err;
+    int seqs, tokens, max_pages, num_pages, page_size;
+    int kv_heads, group, head_dim, window;
+    float scale_log2;   // scale * log2(e): the softmax runs on powers of two
+};
+
+inline AttnShape attn_shape(const AttnArgs& a) {
+    AttnShape s{};
+    s.block_table = a.batch.block_table;
+    s.table_stride = a.batch.table_stride;
+    s.cu_q = a.batch.cu_q;
+    s.seq_lens = a.batch.seq_lens;
+    s.sinks = a.sinks;
+    s.err = a.err;
+    s.seqs = a.batch.seqs;
+    s.tokens = a.batch.tokens;
+    s.max_pages = a.batch.max_pages;
+    s.num_pages = a.kv.num_pages;
+    s.page_size = a.kv.page_size;
+    s.kv_heads = a.kv.heads;
+    s.group = a.q.heads / a.kv.heads;
+    s.head_dim = a.kv.head_dim;
+    s.window = a.window;
+    s.scale_log2 = a.scale * kLog2e;
+    return s;
+}
+
+// 4-D map (element, slot, head, page) of the cache's keys or values; a box is
+// 64 elements x box_slots slots of one head and page in the 128-byte swizzle.
+// Elements past head_dim and pages outside the cache read as zeros.
+bool encode_kv_map(CUtensorMap* m, const kt_paged_kv& kv, bool values, int box_slots);
+
+#ifdef __CUDACC__
+// Sequence b of the step.  Nothing here goes past the step's tokens or the
+// block table, whatever the arrays hold.
+struct SeqInfo {
+    int first_token, q_len;
+    int first_pos;   // position of its first new token (negative: before the sequence)
+    int keys;        // keys that can be read
+};
+__device__ __forceinline__ SeqInfo seq_info(const AttnShape& s, int b) {
+    SeqInfo q;
+    const int t0 = min(max(s.cu_q[b], 0), s.tokens), t1 = min(max(s.cu_q[b + 1], t0), s.tokens);
+    const int len = max(s.seq_lens[b], 0);
+    q.first_token = t0;
+    q.q_len = t1 - t0;
+    q.first_pos = len - q.q_len;
+    const long long room = static_cast<long long>(s.max_pages) * s.page_size;
+    q.keys = static_cast<int>(min(static_cast<long long>(len), room));
+    if (q.keys < len && q.q_len > 0) set_error(s.err, KT_DEVERR_BAD_PAGE);
+    return q;
+}
+
+// First key that a row at position pos sees.
+__device__ __forceinline__ int window_start(int pos, int window) { return window > 0 ? max(0, pos - window + 1) : 0; }
+
+// Page of key `key`, -1 (reads as zeros, and says so in the error word) when the table has none there.
+__device__ __forceinline__ int checked_page(const AttnShape& s, const int32_t* pages, int key) {
+    const int page = pages[key / s.page_size];
+    if (page >= 0 && page < s.num_pages) return page;
+    set_error(s.err, KT_DEVERR_BAD_PAGE);
+    return -1;
+}
+
+// A CTA's run of the units of all sequences: [begin, begin + per) of `total`,
+// its first unit being unit in_seq of sequence seq.
+struct RunPlan {
+    long long total, per, begin, in_seq;
+    int seq;
+};
+
+// Deals the sequences' units (units_of(b)) in equal contiguous runs of at least
+// min_units.  All THREADS threads of the CTA call it; `shared` is theirs.
+template <int THREADS, typename UnitsOf>
+__device__ __forceinline__ RunPlan plan_run(int seqs, int min_units, UnitsOf units_of, RunPlan* shared) {
+    __shared__ long long s_warp[THREADS / 32];
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    // totals, then (once the runs' length is known) the sequence that holds this CTA's first unit
+    long long total = 0;
+    long long mine = tid < seqs ? units_of(tid) : 0;
+    const long long first_mine = mine;
+    for (int b0 = THREADS; b0 < seqs; b0 += THREADS) mine += b0 + tid < seqs ? units_of(b0 + tid) : 0;
+    long long sum = mine;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s_warp[warp] = sum;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) total += s_warp[w];
+    const long long even = (total + gridDim.x - 1) / gridDim.x;
+    const long long per = even > min_units ? even : min_units;
+    const long long begin = per * blockIdx.x;
+    if (tid == 0) *shared = RunPlan{total, per, begin, 0, seqs};
+    long long before = 0;
+    for (int b0 = 0; b0 < seqs && begin < total; b0 += THREADS) {
+        const long long n = b0 == 0 ? first_mine : (b0 + tid < seqs ? units_of(b0 + tid) : 0);
+        long long incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        __syncthreads();
+        if (lane == 31) s_warp[warp] = incl;
+        __syncthreads();
+        long long prefix = before;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) prefix += s_warp[w];
+            before += s_warp[w];
+        }
+        if (begin >= prefix + incl - n && begin < prefix + incl) {
+            shared->seq = b0 + tid;
+            shared->in_seq = begin - (prefix + incl - n);
+        }
+        if (before > begin) break;   // the same for every thread
+    }
+    __syncthreads();
+    return *shared;
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                            int w) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}],"
+        " [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// D (16 x 8, fp32) += A (16 x 16, row-major) x B (16 x 8, column-major)
+template <typename T>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma_16816<__nv_bfloat16>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+        " {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma_16816<__half>(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+        " {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 2^x; -inf gives 0, results below the normal range are flushed.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two floats rounded to T, the first in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+#endif
+
+}  // namespace kt

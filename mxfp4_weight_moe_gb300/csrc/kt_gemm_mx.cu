@@ -1378,6 +1378,10 @@ static bool encode(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int
               CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+bool encode_tiled_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw) {
+    return encode(m, dt, base, rank, dims, strides, box, sw);
+}
 
 // Largest cluster size (up to `want`) whose co-resident clusters of one CTA
 // per SM cover at least 15/16 of the SMs; asked of the driver once per device.
