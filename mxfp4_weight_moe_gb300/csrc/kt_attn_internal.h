@@ -53,6 +53,8 @@ struct AttnArgs {
 };
 size_t attn_split_workspace_bytes();
 kt_status launch_attn_split(const AttnArgs& a, cudaStream_t s);
+size_t attn_tile_workspace_bytes();
+kt_status launch_attn_tile(const AttnArgs& a, cudaStream_t s);
 
 #ifdef __CUDACC__
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }

@@ -402,7 +402,7 @@ static int split_ctas() { return sm_count() * kSplitCtasPerSm; }
 
 size_t attn_split_workspace_bytes() {
     const size_t c = static_cast<size_t>(split_ctas());
-    return align_up(c * sizeof(unsigned), 1024) + c * 2 * kSplitRows * (128 + 2) * sizeof(float);
+    return align_up(align_up(c * sizeof(unsigned), 1024) + c * 2 * kSplitRows * (128 + 2) * sizeof(float), 1024);
 }
 
 template <typename T, int DP>

@@ -1,0 +1,756 @@
+// kt_attn_tile.cu -- attention over a paged cache for chunks of new tokens, on
+// the tcgen05 tensor cores.
+//
+// An item is (sequence, cache head, 2 x 128 query rows): a group of 128 rows
+// holds 128 / group consecutive tokens under the cache head's query heads, so
+// heads that share a cache head share its key and value tiles.  Per tile of 128
+// keys and row group the CTA computes
+//   S = Q K^T            (tensor cores, fp32 in tensor memory)
+//   P = 2^(c S - c m)    (one thread per row; c = scale log2 e, m the row's reference)
+//   O += P V             (tensor cores; P is read from tensor memory, where it replaces S)
+// The two groups alternate: while one group's softmax runs, the tensor cores
+// work on the other's products.  m is the running maximum as of its last change;
+// it follows the true maximum only when that has grown by more than 2^8, so the
+// rescaling of O (by the row's own thread) is rare, and the sums stay exact in
+// fp32 (P up to 2^8 rounds with the same relative error).
+//
+// Work is dealt as in the split kernel: all items' key tiles form one line, cut
+// into equal runs; the last CTA of a cut item joins its partial sums in order.
+//
+// Warps: 0-3 softmax of group 0, 4-7 of group 1, 8 issues the MMAs, 9 the TMA loads.
+#include "kt_attn_dev.cuh"
+
+namespace kt {
+
+constexpr int kTileKeys = 128;
+constexpr int kTileThreads = 384;
+constexpr int kTileMinUnits = 2;      // least key tiles of a CTA's run
+constexpr int kPlanSeqs = 512;        // sequences planned at a time
+constexpr float kLazyLog2 = 8.0f;     // growth of the maximum (log2) that is let stand
+
+template <int DP>
+struct TileCfg {
+    static constexpr int kQBytes = 128 * DP * 2;         // one row group
+    static constexpr int kStageBytes = kTileKeys * DP * 2;   // one tile of K or V
+    static constexpr int kStages = DP == 128 ? 5 : 10;
+    static constexpr int kSmem = 2 * kQBytes + kStages * kStageBytes + 1024;
+    static constexpr uint32_t kTmemO = 256;              // S0, S1 at 0, 128; O0, O1 at 256, 256 + DP
+};
+
+struct TileParams {
+    AttnShape sh;
+    void* out;
+    long long o_token, o_head;
+    int tokens_per_group;   // 128 / group
+    int box_slots;          // slots of one load: the largest power of two that divides page_size, at most 128
+    float4* part_o;         // [CTAs][2 pieces][DP / 4][256 rows]
+    float2* part_ml;        // [CTAs][2][256]
+    unsigned* counters;     // [CTAs][2 groups]
+};
+
+struct TileItem {
+    int lo, hi, unit0, units;
+};
+__device__ __forceinline__ TileItem tile_item(const AttnShape& s, const SeqInfo& q, int tokens_per_item, int rt) {
+    TileItem it;
+    const int t0 = rt * tokens_per_item;
+    const int t1 = min(t0 + tokens_per_item, q.q_len) - 1;
+    it.hi = max(0, min(q.first_pos + t1 + 1, q.keys));
+    it.lo = window_start(q.first_pos + t0, s.window);
+    if (it.lo >= it.hi) it.lo = it.hi = 0;
+    it.unit0 = it.lo / kTileKeys;
+    it.units = max(1, (it.hi + kTileKeys - 1) / kTileKeys - it.unit0);
+    return it;
+}
+
+// Walks a CTA's run item by item; every role of the CTA walks it for itself.
+struct TileWalk {
+    int b, rt, tiles, h, uo, take;
+    long long left, first_unit;   // units of the run from here on; the item's first unit on the whole line
+    SeqInfo sq;
+    TileItem it;
+
+    __device__ __forceinline__ void load_seq(const AttnShape& s, int tpi) {
+        while (b < s.seqs) {
+            sq = seq_info(s, b);
+            tiles = (sq.q_len + tpi - 1) / tpi;
+            if (tiles > 0) return;
+            ++b;
+        }
+        left = 0;
+    }
+    // whole warp: finds the item of unit plan.in_seq of sequence plan.seq
+    __device__ __forceinline__ void start(const AttnShape& s, int tpi, const RunPlan& plan) {
+        const int lane = static_cast<int>(threadIdx.x) & 31;
+        left = min(plan.per, plan.total - plan.begin);
+        if (left <= 0) return;
+        b = plan.seq;
+        rt = h = uo = 0;
+        load_seq(s, tpi);
+        long long before = 0;
+        for (int r0 = 0; r0 < tiles; r0 += 32) {
+            const int r = r0 + lane;
+            const long long n = r < tiles ? static_cast<long long>(tile_item(s, sq, tpi, r).units) * s.kv_heads : 0;
+            long long incl = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += up;
+            }
+            const unsigned found = __ballot_sync(0xffffffffu, before + incl > plan.in_seq);
+            if (found != 0) {
+                const int src = __ffs(static_cast<int>(found)) - 1;
+                before += __shfl_sync(0xffffffffu, incl - n, src);
+                rt = r0 + src;
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        it = tile_item(s, sq, tpi, rt);
+        const long long in = plan.in_seq - before;
+        h = static_cast<int>(in / it.units);
+        uo = static_cast<int>(in - static_cast<long long>(h) * it.units);
+        first_unit = plan.begin - uo;
+        take = static_cast<int>(min(static_cast<long long>(it.units - uo), left));
+    }
+    __device__ __forceinline__ void next(const AttnShape& s, int tpi) {
+        left -= take;
+        if (left <= 0) return;
+        first_unit += it.units;   // a run that goes on has finished this item
+        uo = 0;
+        if (++h == s.kv_heads) {
+            h = 0;
+            if (++rt == tiles) {
+                rt = 0;
+                ++b;
+                load_seq(s, tpi);
+                if (left <= 0) return;
+            }
+            it = tile_item(s, sq, tpi, rt);
+        }
+        take = static_cast<int>(min(static_cast<long long>(it.units), left));
+    }
+    __device__ __forceinline__ int groups(int tpg) const { return sq.q_len - rt * 2 * tpg > tpg ? 2 : 1; }
+};
+
+// plan_run with a warp per sequence (a long chunk has many items, whose units are summed by the warp's lanes).
+__device__ __forceinline__ RunPlan plan_tiles(const AttnShape& s, int tpi, unsigned* costs, RunPlan* shared) {
+    constexpr int kWarps = kTileThreads / 32;
+    __shared__ long long s_sum[kWarps];
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    auto fill = [&](int b0) {   // costs of sequences [b0, b0 + kPlanSeqs): units / kv_heads
+        for (int b = b0 + warp; b < min(s.seqs, b0 + kPlanSeqs); b += kWarps) {
+            const SeqInfo q = seq_info(s, b);
+            const int tiles = (q.q_len + tpi - 1) / tpi;
+            unsigned n = 0;
+            for (int r = lane; r < tiles; r += 32) n += static_cast<unsigned>(tile_item(s, q, tpi, r).units);
+            n = __reduce_add_sync(0xffffffffu, n);
+            if (lane == 0) costs[b - b0] = n;
+        }
+        __syncthreads();
+    };
+    long long mine = 0;
+    for (int b0 = 0; b0 < s.seqs; b0 += kPlanSeqs) {
+        if (b0 > 0) __syncthreads();
+        fill(b0);
+        for (int i = tid; i < min(s.seqs - b0, kPlanSeqs); i += kTileThreads) mine += costs[i];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) s_sum[warp] = mine;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += s_sum[w];
+    total *= s.kv_heads;
+    const long long even = (total + gridDim.x - 1) / gridDim.x;
+    const long long per = even > kTileMinUnits ? even : kTileMinUnits;
+    const long long begin = per * blockIdx.x;
+    if (tid == 0) *shared = RunPlan{total, per, begin, 0, s.seqs};
+    __syncthreads();
+    // the sequence of unit `begin`: warp 0 scans the costs 32 at a time
+    long long before = 0;
+    for (int b0 = 0; b0 < s.seqs && begin < total; b0 += kPlanSeqs) {
+        if (s.seqs > kPlanSeqs) {
+            __syncthreads();
+            fill(b0);
+        }
+        const int count = min(s.seqs - b0, kPlanSeqs);
+        if (warp == 0) {
+            for (int i0 = 0; i0 < count && before <= begin; i0 += 32) {
+                const long long n =
+                    i0 + lane < count ? static_cast<long long>(costs[i0 + lane]) * s.kv_heads : 0;
+                long long incl = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += up;
+                }
+                const long long prefix = before + incl - n;
+                if (begin >= prefix && begin < prefix + n) {
+                    shared->seq = b0 + i0 + lane;
+                    shared->in_seq = begin - prefix;
+                }
+                before += __shfl_sync(0xffffffffu, incl, 31);
+            }
+        }
+    }
+    __syncthreads();
+    return *shared;
+}
+
+// Matrix descriptor of a value tile as the MN-major B operand (128-byte swizzle): 64-element blocks of the head
+// `lbo` bytes apart, groups of 8 keys 1024 bytes apart.
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(lbo >> 4) << 16 |
+           static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
+}
+
+// Instruction descriptor of kind::f16: fp32 accumulate, M = 128, N = n, A and B both bf16 or both fp16.
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc_f16(int n, bool b_mn_major) {
+    const uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    return (1u << 4) | (fmt << 7) | (fmt << 10) | ((b_mn_major ? 1u : 0u) << 16) |
+           (static_cast<uint32_t>(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred P1;\n\t"
+        "setp.ne.b32 P1, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, P1;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred P1;\n\t"
+        "setp.ne.b32 P1, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, P1;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st_32x32b_x32(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}],"
+        " [%2];" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// mbar_wait with one answer for the whole warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    attn_tile_kernel(const TileParams p, const __grid_constant__ CUtensorMap qmap,
+                     const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+    using Cfg = TileCfg<DP>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t s_kv_full[Cfg::kStages], s_kv_empty[Cfg::kStages];
+    __shared__ __align__(8) uint64_t s_q_full[2], s_q_empty[2], s_s_full[2], s_p_full[2], s_o_full[2], s_done;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_last[2];
+    __shared__ RunPlan s_plan;
+    const AttnShape& sh = p.sh;
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+    const int tpg = p.tokens_per_group;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t q_smem = smem_u32(smem);
+    uint8_t* kv_ptr = smem + 2 * Cfg::kQBytes;
+    const uint32_t kv_smem = smem_u32(kv_ptr);
+
+    if (tid == 0) {
+        s_abort = 0;
+        for (int i = 0; i < Cfg::kStages; ++i) {
+            mbar_init(smem_u32(&s_kv_full[i]), 1);
+            mbar_init(smem_u32(&s_kv_empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&s_q_full[i]), 1);
+            mbar_init(smem_u32(&s_q_empty[i]), 1);
+            mbar_init(smem_u32(&s_s_full[i]), 1);
+            mbar_init(smem_u32(&s_p_full[i]), 128);
+            mbar_init(smem_u32(&s_o_full[i]), 1);
+        }
+        mbar_init(smem_u32(&s_done), 1);
+        fence_mbar_init();
+        tma_prefetch_map(&qmap);
+        tma_prefetch_map(&kmap);
+        tma_prefetch_map(&vmap);
+    }
+    if (warp == 8) {
+        tc_alloc(smem_u32(&s_tmem), 512);
+        tc_relinquish();
+    }
+    if (tpg * sh.group < 128) {   // rows of no token: zeros for good (the loads do not touch them)
+        for (int i = tid; i < 2 * Cfg::kQBytes / 16; i += kTileThreads)
+            reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    const RunPlan plan = plan_tiles(sh, 2 * tpg, reinterpret_cast<unsigned*>(kv_ptr), &s_plan);
+    tc_fence_before();
+    fence_proxy_async_smem();   // the plan's and the zeros' generic writes before the first loads
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = s_tmem;
+    const int* abort_flag = &s_abort;
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        TileWalk w;
+        w.start(sh, 2 * tpg, plan);
+        if (warp == 9) {
+            // ------------------------------------------------ loads
+            uint32_t stage = 0, round = 0, item_no[2] = {0, 0};
+            const int boxes = kTileKeys / p.box_slots;
+            const int box = lane % boxes;   // of 1, 2, 4 or 8 per 64 elements (page_size is a multiple of 16)
+            bool ok = true;
+            // tile of keys [key0, key0 + 128) of K or V into the next stage
+            auto load_tile = [&](const CUtensorMap* map, int key0, const int32_t* pages) {
+                const uint32_t full = smem_u32(&s_kv_full[stage]);
+                if (round > 0) ok = ok && warp_wait(smem_u32(&s_kv_empty[stage]), (round - 1) & 1u, abort_flag);
+                if (!ok) return;
+                if (lane == 0) mbar_arrive_expect_tx(full, Cfg::kStageBytes);
+                __syncwarp();
+                if (lane < boxes * (DP / 64)) {
+                    const int x = lane / boxes;
+                    const int key = key0 + box * p.box_slots;
+                    // boxes that no row sees come from outside the cache, as zeros
+                    const int page =
+                        key < w.it.hi && key + p.box_slots > w.it.lo ? checked_page(sh, pages, key) : -1;
+                    tma_load_4d(kv_smem + stage * Cfg::kStageBytes + x * (kTileKeys * 128) + box * p.box_slots * 128,
+                                map, full, x * 64, key % sh.page_size, w.h, page);
+                }
+                __syncwarp();
+                if (++stage == Cfg::kStages) {
+                    stage = 0;
+                    ++round;
+                }
+            };
+            while (w.left > 0 && ok) {
+                const int32_t* pages = sh.block_table + w.b * sh.table_stride;
+                const int key0 = (w.it.unit0 + w.uo) * kTileKeys;
+                const int groups = w.groups(tpg);
+                for (int i = 0; i < groups && ok; ++i) {
+                    if (item_no[i] > 0)
+                        ok = warp_wait(smem_u32(&s_q_empty[i]), (item_no[i] - 1) & 1u, abort_flag);
+                    if (!ok) break;
+                    ++item_no[i];
+                    if (lane == 0) {
+                        const uint32_t bar = smem_u32(&s_q_full[i]);
+                        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(tpg * sh.group * DP * 2));
+                        for (int x = 0; x < DP; x += 64)
+                            tma_load_3d(q_smem + i * Cfg::kQBytes + (x / 64) * (128 * 128), &qmap, bar, x,
+                                        w.h * sh.group, w.sq.first_token + (w.rt * 2 + i) * tpg);
+                    }
+                    __syncwarp();
+                    if (i == 0) load_tile(&kmap, key0, pages);
+                }
+                for (int j = 0; j < w.take && ok; ++j) {
+                    load_tile(&vmap, key0 + j * kTileKeys, pages);
+                    if (ok && j + 1 < w.take) load_tile(&kmap, key0 + (j + 1) * kTileKeys, pages);
+                }
+                w.next(sh, 2 * tpg);
+            }
+            if (!ok && !*reinterpret_cast<volatile int*>(&s_abort)) {
+                if (lane == 0) {
+                    s_abort = 1;
+                    set_error(sh.err, KT_DEVERR_TIMEOUT_LOAD);
+                }
+            }
+            if (!ok) {   // loads still in flight land before the CTA ends (each wait bounded)
+                int never = 0;
+                for (uint32_t i = 0; i < Cfg::kStages; ++i) {
+                    const uint32_t r = i < stage ? round : round - 1;   // the stage's last load
+                    if (i < stage || round > 0) mbar_wait(smem_u32(&s_kv_full[i]), r & 1u, &never, 1000000);
+                }
+                for (int i = 0; i < 2; ++i)
+                    if (item_no[i] > 0) mbar_wait(smem_u32(&s_q_full[i]), (item_no[i] - 1) & 1u, &never, 1000000);
+            }
+        } else if (warp == 8) {
+            // ------------------------------------------------ MMAs (lane 0 issues)
+            constexpr uint32_t kIdescQK = idesc_f16<T>(kTileKeys, false);
+            constexpr uint32_t kIdescPV = idesc_f16<T>(DP, true);
+            uint32_t stage = 0, round = 0, item_no[2] = {0, 0}, tile_no[2] = {0, 0};
+            bool ok = true;
+            auto advance = [&]() {
+                if (++stage == Cfg::kStages) {
+                    stage = 0;
+                    ++round;
+                }
+            };
+            auto qk = [&](int i, uint32_t st) {   // S_i = Q_i K^T
+                if (lane == 0) {
+                    const uint64_t a = sdesc_k_sw128(q_smem + i * Cfg::kQBytes);
+                    const uint64_t b = sdesc_k_sw128(kv_smem + st * Cfg::kStageBytes);
+#pragma unroll
+                    for (int ks = 0; ks < DP / 16; ++ks) {
+                        const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
+                        tc_mma_ss(tmem + i * 128, a + off, b + off, kIdescQK, ks > 0 ? 1u : 0u);
+                    }
+                    tc_commit(smem_u32(&s_s_full[i]));
+                }
+            };
+            while (w.left > 0 && ok) {
+                const int groups = w.groups(tpg);
+                const int key0 = (w.it.unit0 + w.uo) * kTileKeys;
+                for (int i = 0; i < groups && ok; ++i) {
+                    ok = warp_wait(smem_u32(&s_q_full[i]), item_no[i] & 1u, abort_flag);
+                    if (ok && i == 0) ok = warp_wait(smem_u32(&s_kv_full[stage]), round & 1u, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    qk(i, stage);
+                    if (w.take == 1 && lane == 0) tc_commit(smem_u32(&s_q_empty[i]));
+                    ++item_no[i];
+                }
+                if (!ok) break;
+                if (lane == 0) tc_commit(smem_u32(&s_kv_empty[stage]));
+                advance();
+                for (int j = 0; j < w.take && ok; ++j) {
+                    const uint32_t vst = stage;
+                    ok = warp_wait(smem_u32(&s_kv_full[vst]), round & 1u, abort_flag);
+                    if (!ok) break;
+                    advance();
+                    // values past the sequence's end are whatever the page holds: zeros, for 0 x NaN is NaN
+                    const int past = w.sq.keys - (key0 + j * kTileKeys);
+                    if (past < kTileKeys && past % p.box_slots != 0 && past > 0) {
+                        const int end = (past / p.box_slots + 1) * p.box_slots;   // the rest was loaded as zeros
+                        for (int c = lane; c < (end - past) * (DP / 8); c += 32) {
+                            const int r = past + c / (DP / 8), x = c % (DP / 8);
+                            *reinterpret_cast<uint4*>(kv_ptr + vst * Cfg::kStageBytes + (x >> 3) * (kTileKeys * 128) +
+                                                      r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    const bool more = j + 1 < w.take;
+                    for (int i = 0; i < groups && ok; ++i) {
+                        ok = warp_wait(smem_u32(&s_p_full[i]), tile_no[i] & 1u, abort_flag);
+                        if (!ok) break;
+                        ++tile_no[i];
+                        tc_fence_after();
+                        if (lane == 0) {
+                            const uint64_t b = sdesc_mn_sw128(kv_smem + vst * Cfg::kStageBytes, kTileKeys * 128);
+#pragma unroll
+                            for (int ks = 0; ks < kTileKeys / 16; ++ks)
+                                tc_mma_ts(tmem + Cfg::kTmemO + i * DP, tmem + i * 128 + ks * 8,
+                                          b + ((ks * 16 * 128) >> 4), kIdescPV, j > 0 || ks > 0 ? 1u : 0u);
+                            if (!more) tc_commit(smem_u32(&s_o_full[i]));
+                        }
+                        if (more) {
+                            if (i == 0) ok = warp_wait(smem_u32(&s_kv_full[stage]), round & 1u, abort_flag);
+                            if (!ok) break;
+                            tc_fence_after();
+                            qk(i, stage);
+                            if (j + 2 == w.take && lane == 0) tc_commit(smem_u32(&s_q_empty[i]));
+                        }
+                    }
+                    if (!ok) break;
+                    if (lane == 0) tc_commit(smem_u32(&s_kv_empty[vst]));
+                    if (more) {
+                        if (lane == 0) tc_commit(smem_u32(&s_kv_empty[stage]));
+                        advance();
+                    }
+                }
+                w.next(sh, 2 * tpg);
+            }
+            if (!ok && lane == 0) {
+                if (!*reinterpret_cast<volatile int*>(&s_abort)) {
+                    s_abort = 1;
+                    set_error(sh.err, KT_DEVERR_TIMEOUT_MMA);
+                }
+            }
+            // every MMA has ended before the tensor memory is freed
+            if (lane == 0) tc_commit(smem_u32(&s_done));
+            int never = 0;
+            mbar_wait(smem_u32(&s_done), 0, &never);
+        }
+    } else {
+        // ---------------------------------------------------- softmax of one row per thread
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int grp = warp >> 2;
+        const int row = tid & 127;
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lane_base + grp * 128;
+        const uint32_t t_o = tmem + lane_base + Cfg::kTmemO + grp * DP;
+        const float c = sh.scale_log2;
+        uint32_t tile_no = 0, item_no = 0;
+        bool ok = true;
+        TileWalk w;
+        w.start(sh, 2 * tpg, plan);
+        for (; w.left > 0 && ok; w.next(sh, 2 * tpg)) {
+            if (grp >= w.groups(tpg)) continue;
+            const int tok = (w.rt * 2 + grp) * tpg + row / sh.group;
+            const bool valid = row / sh.group < tpg && tok < w.sq.q_len;
+            const int pos = w.sq.first_pos + tok;
+            // keys [first, last] are seen; rows of no token compute without masks and are not stored
+            const int last = valid ? min(pos, w.sq.keys - 1) : 0x7fffffff;
+            const int first = valid ? window_start(pos, sh.window) : 0;
+            const int key_base = (w.it.unit0 + w.uo) * kTileKeys;
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < w.take; ++j) {
+                const int key0 = key_base + j * kTileKeys;
+                ok = warp_wait(smem_u32(&s_s_full[grp]), tile_no & 1u, abort_flag);
+                if (!ok) break;
+                ++tile_no;
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tc_ld_32x32b_x32(t_s + q * 32, s[q]);
+                tc_wait_ld();
+                if (__any_sync(0xffffffffu, last < key0 + kTileKeys - 1 || first > key0)) {
+                    const int hi = last - key0, lo = first - key0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (q * 32 + i > hi || q * 32 + i < lo) s[q][i] = 0xff800000u;   // -inf
+                }
+                float top = m;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float t0 = __uint_as_float(s[q][0]), t1 = __uint_as_float(s[q][1]);
+#pragma unroll
+                    for (int i = 2; i < 32; i += 2) {
+                        t0 = fmaxf(t0, __uint_as_float(s[q][i]));
+                        t1 = fmaxf(t1, __uint_as_float(s[q][i + 1]));
+                    }
+                    top = fmaxf(top, fmaxf(t0, t1));
+                }
+                // the reference follows the maximum only when that has outgrown it
+                const bool grown = (top - m) * c > kLazyLog2;   // also from -inf
+                if (__any_sync(0xffffffffu, grown)) {
+                    const float f = grown ? ex2((m - top) * c) : 1.0f;
+                    if (grown) m = top;
+                    l *= f;
+                    if (j > 0) {
+#pragma unroll
+                        for (int q = 0; q < DP / 32; ++q) {
+                            uint32_t o[32];
+                            tc_ld_32x32b_x32(t_o + q * 32, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tc_st_32x32b_x32(t_o + q * 32, o);
+                        }
+                    }
+                }
+                const float neg = m == -INFINITY ? 0.0f : -m * c;
+                float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int e = 2 * i;
+                        const float a = ex2(fmaf(__uint_as_float(s[2 * q + (e >> 5)][e & 31]), c, neg));
+                        const float b = ex2(fmaf(__uint_as_float(s[2 * q + (e >> 5)][(e & 31) + 1]), c, neg));
+                        sum0 += a;
+                        sum1 += b;
+                        pk[i] = pack2<T>(a, b);
+                    }
+                    tc_st_32x32b_x32(t_s + q * 32, pk);
+                }
+                l += sum0 + sum1;
+                tc_wait_st();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&s_p_full[grp]));
+            }
+            if (!ok) break;
+            ok = warp_wait(smem_u32(&s_o_full[grp]), item_no & 1u, abort_flag);
+            if (!ok) break;
+            ++item_no;
+            tc_fence_after();
+
+            // ---- the item's piece is complete: store it, or leave it for the join
+            const bool whole = w.uo == 0 && w.take == w.it.units;
+            const int head = w.h * sh.group + row % sh.group;
+            T* dst = static_cast<T*>(p.out) + static_cast<long long>(w.sq.first_token + tok) * p.o_token +
+                     static_cast<long long>(head) * p.o_head;
+            auto closing = [&](float mt, float lt, float& scale_o) {   // 1 / sum, the sink's share included
+                scale_o = 1.0f;
+                if (sh.sinks != nullptr && valid) {
+                    const float sk = sh.sinks[head] * kLog2e;
+                    const float mc = mt == -INFINITY ? -INFINITY : mt * c;
+                    const float t = fmaxf(mc, sk);
+                    const float tb = t == -INFINITY ? 0.0f : t;
+                    scale_o = ex2(mc - tb);
+                    lt = lt * scale_o + ex2(sk - tb);
+                }
+                scale_o = lt == 0.0f ? 0.0f : scale_o / lt;
+            };
+            if (whole) {
+                float inv;
+                closing(m, l, inv);
+#pragma unroll
+                for (int q = 0; q < DP / 32; ++q) {
+                    uint32_t o[32];
+                    tc_ld_32x32b_x32(t_o + q * 32, o);
+                    tc_wait_ld();
+                    if (valid) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8) {
+                            if (q * 32 + i >= sh.head_dim) break;
+                            uint4 v;
+                            v.x = pack2<T>(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+                            v.y = pack2<T>(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
+                            v.z = pack2<T>(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
+                            v.w = pack2<T>(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
+                            *reinterpret_cast<uint4*>(dst + q * 32 + i) = v;
+                        }
+                    }
+                }
+                tc_fence_before();
+                continue;
+            }
+            const int c0 = static_cast<int>(w.first_unit / plan.per);
+            const int c1 = static_cast<int>((w.first_unit + w.it.units - 1) / plan.per);
+            const size_t slot = 2 * blockIdx.x + (w.uo == 0 ? 1 : 0);
+            const int prow = grp * 128 + row;
+#pragma unroll
+            for (int q = 0; q < DP / 32; ++q) {
+                uint32_t o[32];
+                tc_ld_32x32b_x32(t_o + q * 32, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    p.part_o[(slot * (DP / 4) + (q * 32 + i) / 4) * 256 + prow] =
+                        make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
+                                    __uint_as_float(o[i + 3]));
+            }
+            tc_fence_before();
+            p.part_ml[slot * 256 + prow] = make_float2(m, l);
+            __threadfence();
+            asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory");
+            if (row == 0) {
+                const unsigned seen = atomicAdd(&p.counters[2 * c0 + grp], 1u);
+                s_last[grp] = seen == static_cast<unsigned>(c1 - c0);
+                if (s_last[grp]) p.counters[2 * c0 + grp] = 0;
+            }
+            asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory");
+            if (!s_last[grp]) continue;
+            __threadfence();
+            float mt = -INFINITY;
+            for (int k = c0; k <= c1; ++k)
+                mt = fmaxf(mt, __ldcg(&p.part_ml[(2 * static_cast<size_t>(k) + (k == c0 ? 1 : 0)) * 256 + prow]).x);
+            const float mref = mt == -INFINITY ? 0.0f : mt;
+            float lt = 0.0f;
+            for (int k = c0; k <= c1; ++k) {
+                const float2 ml = __ldcg(&p.part_ml[(2 * static_cast<size_t>(k) + (k == c0 ? 1 : 0)) * 256 + prow]);
+                lt += ml.y * ex2((ml.x - mref) * c);
+            }
+            float inv;
+            closing(mt, lt, inv);
+#pragma unroll
+            for (int q = 0; q < DP / 32; ++q) {
+                float acc[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) acc[i] = 0.0f;
+                for (int k = c0; k <= c1; ++k) {
+                    const size_t sl = 2 * static_cast<size_t>(k) + (k == c0 ? 1 : 0);
+                    const float f = ex2((__ldcg(&p.part_ml[sl * 256 + prow]).x - mref) * c);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 v = __ldcg(&p.part_o[(sl * (DP / 4) + (q * 32 + i) / 4) * 256 + prow]);
+                        acc[i] += f * v.x;
+                        acc[i + 1] += f * v.y;
+                        acc[i + 2] += f * v.z;
+                        acc[i + 3] += f * v.w;
+                    }
+                }
+                if (valid) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        if (q * 32 + i >= sh.head_dim) break;
+                        uint4 v;
+                        v.x = pack2<T>(acc[i] * inv, acc[i + 1] * inv);
+                        v.y = pack2<T>(acc[i + 2] * inv, acc[i + 3] * inv);
+                        v.z = pack2<T>(acc[i + 4] * inv, acc[i + 5] * inv);
+                        v.w = pack2<T>(acc[i + 6] * inv, acc[i + 7] * inv);
+                        *reinterpret_cast<uint4*>(dst + q * 32 + i) = v;
+                    }
+                }
+            }
+        }
+        if (!ok && !*reinterpret_cast<volatile int*>(&s_abort)) {
+            s_abort = 1;
+            set_error(sh.err, KT_DEVERR_TIMEOUT_EPI);
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tc_dealloc(tmem, 512);
+    }
+}
+
+size_t attn_tile_workspace_bytes() {
+    const size_t c = static_cast<size_t>(sm_count());
+    return align_up(c * 2 * sizeof(unsigned), 1024) + c * 2 * 256 * (128 * sizeof(float) + sizeof(float2));
+}
+
+template <typename T, int DP>
+static kt_status launch_tile_typed(const AttnArgs& a, cudaStream_t s) {
+    using Cfg = TileCfg<DP>;
+    TileParams p{};
+    p.sh = attn_shape(a);
+    p.out = a.out.ptr;
+    p.o_token = a.out.token_stride;
+    p.o_head = a.out.head_stride;
+    p.tokens_per_group = 128 / p.sh.group;
+    p.box_slots = a.kv.page_size & -a.kv.page_size;
+    if (p.box_slots > kTileKeys) p.box_slots = kTileKeys;
+    CUtensorMap qmap, kmap, vmap;
+    const uint64_t qd[3] = {static_cast<uint64_t>(a.kv.head_dim), static_cast<uint64_t>(a.q.heads),
+                            static_cast<uint64_t>(a.batch.tokens)};
+    const uint64_t qs[2] = {2 * static_cast<uint64_t>(a.q.head_stride), 2 * static_cast<uint64_t>(a.q.token_stride)};
+    const uint32_t qb[3] = {64, static_cast<uint32_t>(p.sh.group), static_cast<uint32_t>(p.tokens_per_group)};
+    if (!encode_tiled_map(&qmap, a.kv.dtype == KT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                          a.q.ptr, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_kv_map(&kmap, a.kv, false, p.box_slots) || !encode_kv_map(&vmap, a.kv, true, p.box_slots))
+        return report(KT_ERR_CUDA, "tensor map encoding failed");
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(attn_tile_kernel<T, DP>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+        if (e != cudaSuccess) return cuda_status(e);
+        attr_set[dev] = true;
+    }
+    const size_t c = static_cast<size_t>(sm_count());
+    p.counters = reinterpret_cast<unsigned*>(a.ws);
+    p.part_o = reinterpret_cast<float4*>(a.ws + align_up(c * 2 * sizeof(unsigned), 1024));
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + c * 2 * 256 * 32);
+    count_launches(1);
+    return cuda_status(launch_chained(attn_tile_kernel<T, DP>, dim3(static_cast<unsigned>(c)), dim3(kTileThreads),
+                                      Cfg::kSmem, s, static_cast<const TileParams&>(p),
+                                      static_cast<const CUtensorMap&>(qmap), static_cast<const CUtensorMap&>(kmap),
+                                      static_cast<const CUtensorMap&>(vmap)));
+}
+
+kt_status launch_attn_tile(const AttnArgs& a, cudaStream_t s) {
+    const bool wide = a.kv.head_dim > 64;
+    if (a.kv.dtype == KT_DTYPE_BF16)
+        return wide ? launch_tile_typed<__nv_bfloat16, 128>(a, s) : launch_tile_typed<__nv_bfloat16, 64>(a, s);
+    return wide ? launch_tile_typed<__half, 128>(a, s) : launch_tile_typed<__half, 64>(a, s);
+}
+
+}  // namespace kt
