@@ -24,9 +24,13 @@ namespace kt {
 
 constexpr int kTileKeys = 128;
 constexpr int kTileThreads = 384;
-constexpr int kTileMinUnits = 2;      // least key tiles of a CTA's run
+constexpr int kItemUnits = 3;         // what an item costs besides its key tiles, in key tiles
+constexpr int kTileMinUnits = kItemUnits + 2;   // least units of a CTA's run
 constexpr int kPlanSeqs = 512;        // sequences planned at a time
 constexpr float kLazyLog2 = 8.0f;     // growth of the maximum (log2) that is let stand
+
+// Tensor memory: the CTA takes all 512 columns, so it starts at 0.  S of the groups (P in its first half), then O.
+constexpr uint32_t kTmemS = 0, kTmemO = 256;
 
 template <int DP>
 struct TileCfg {
@@ -34,7 +38,6 @@ struct TileCfg {
     static constexpr int kStageBytes = kTileKeys * DP * 2;   // one tile of K or V
     static constexpr int kStages = DP == 128 ? 5 : 10;
     static constexpr int kSmem = 2 * kQBytes + kStages * kStageBytes + 1024;
-    static constexpr uint32_t kTmemO = 256;              // S0, S1 at 0, 128; O0, O1 at 256, 256 + DP
 };
 
 struct TileParams {
@@ -49,7 +52,7 @@ struct TileParams {
 };
 
 struct TileItem {
-    int lo, hi, unit0, units;
+    int lo, hi, tile0, tiles;   // keys that some row sees; first key tile, key tiles (at least one)
 };
 __device__ __forceinline__ TileItem tile_item(const AttnShape& s, const SeqInfo& q, int tokens_per_item, int rt) {
     TileItem it;
@@ -58,39 +61,47 @@ __device__ __forceinline__ TileItem tile_item(const AttnShape& s, const SeqInfo&
     it.hi = max(0, min(q.first_pos + t1 + 1, q.keys));
     it.lo = window_start(q.first_pos + t0, s.window);
     if (it.lo >= it.hi) it.lo = it.hi = 0;
-    it.unit0 = it.lo / kTileKeys;
-    it.units = max(1, (it.hi + kTileKeys - 1) / kTileKeys - it.unit0);
+    it.tile0 = it.lo / kTileKeys;
+    it.tiles = max(1, (it.hi + kTileKeys - 1) / kTileKeys - it.tile0);
     return it;
 }
 
-// Walks a CTA's run item by item; every role of the CTA walks it for itself.
+// Units of item rt on the line: its key tiles, and the tiles' worth of time that any item takes besides.
+__device__ __forceinline__ int item_units(const TileItem& it) { return it.tiles + kItemUnits; }
+
+// Walks a CTA's run [begin, end) of units item by item; every role of the CTA walks it for itself.
 struct TileWalk {
-    int b, rt, tiles, h, uo, take;
-    long long left, first_unit;   // units of the run from here on; the item's first unit on the whole line
+    int b, rt, row_tiles, h;
+    int t0, t1;               // the item's key tiles in this run
+    long long first, end;     // the item's first key tile on the line; end of the run
     SeqInfo sq;
     TileItem it;
 
-    __device__ __forceinline__ void load_seq(const AttnShape& s, int tpi) {
-        while (b < s.seqs) {
+    __device__ __forceinline__ bool load_seq(const AttnShape& s, int tpi) {
+        for (; b < s.seqs; ++b) {
             sq = seq_info(s, b);
-            tiles = (sq.q_len + tpi - 1) / tpi;
-            if (tiles > 0) return;
-            ++b;
+            row_tiles = (sq.q_len + tpi - 1) / tpi;
+            if (row_tiles > 0) return true;
         }
-        left = 0;
+        return false;
     }
-    // whole warp: finds the item of unit plan.in_seq of sequence plan.seq
-    __device__ __forceinline__ void start(const AttnShape& s, int tpi, const RunPlan& plan) {
+    __device__ __forceinline__ void cut(long long begin) {
+        t0 = static_cast<int>(max(begin - first, 0ll));
+        t1 = static_cast<int>(min(end - first, static_cast<long long>(it.tiles)));
+    }
+    // whole warp: finds the item of unit plan.in_seq of sequence plan.seq; false: no work
+    __device__ __forceinline__ bool start(const AttnShape& s, int tpi, const RunPlan& plan) {
         const int lane = static_cast<int>(threadIdx.x) & 31;
-        left = min(plan.per, plan.total - plan.begin);
-        if (left <= 0) return;
+        end = min(plan.begin + plan.per, plan.total);
+        if (plan.begin >= end) return false;
         b = plan.seq;
-        rt = h = uo = 0;
+        rt = 0;
         load_seq(s, tpi);
         long long before = 0;
-        for (int r0 = 0; r0 < tiles; r0 += 32) {
+        for (int r0 = 0; r0 < row_tiles; r0 += 32) {
             const int r = r0 + lane;
-            const long long n = r < tiles ? static_cast<long long>(tile_item(s, sq, tpi, r).units) * s.kv_heads : 0;
+            const long long n =
+                r < row_tiles ? static_cast<long long>(item_units(tile_item(s, sq, tpi, r))) * s.kv_heads : 0;
             long long incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -108,27 +119,26 @@ struct TileWalk {
         }
         it = tile_item(s, sq, tpi, rt);
         const long long in = plan.in_seq - before;
-        h = static_cast<int>(in / it.units);
-        uo = static_cast<int>(in - static_cast<long long>(h) * it.units);
-        first_unit = plan.begin - uo;
-        take = static_cast<int>(min(static_cast<long long>(it.units - uo), left));
+        h = static_cast<int>(in / item_units(it));
+        first = plan.begin - (in - static_cast<long long>(h) * item_units(it)) + kItemUnits;
+        cut(plan.begin);
+        return t1 > t0 || next(s, tpi);
     }
-    __device__ __forceinline__ void next(const AttnShape& s, int tpi) {
-        left -= take;
-        if (left <= 0) return;
-        first_unit += it.units;   // a run that goes on has finished this item
-        uo = 0;
+    __device__ __forceinline__ bool next(const AttnShape& s, int tpi) {
+        first += it.tiles + kItemUnits;   // a run that goes on has finished this item
+        if (first >= end) return false;
         if (++h == s.kv_heads) {
             h = 0;
-            if (++rt == tiles) {
+            if (++rt == row_tiles) {
                 rt = 0;
                 ++b;
-                load_seq(s, tpi);
-                if (left <= 0) return;
+                if (!load_seq(s, tpi)) return false;
             }
             it = tile_item(s, sq, tpi, rt);
         }
-        take = static_cast<int>(min(static_cast<long long>(it.units), left));
+        t0 = 0;
+        t1 = static_cast<int>(min(end - first, static_cast<long long>(it.tiles)));
+        return true;
     }
     __device__ __forceinline__ int groups(int tpg) const { return sq.q_len - rt * 2 * tpg > tpg ? 2 : 1; }
 };
@@ -143,7 +153,7 @@ __device__ __forceinline__ RunPlan plan_tiles(const AttnShape& s, int tpi, unsig
             const SeqInfo q = seq_info(s, b);
             const int tiles = (q.q_len + tpi - 1) / tpi;
             unsigned n = 0;
-            for (int r = lane; r < tiles; r += 32) n += static_cast<unsigned>(tile_item(s, q, tpi, r).units);
+            for (int r = lane; r < tiles; r += 32) n += static_cast<unsigned>(item_units(tile_item(s, q, tpi, r)));
             n = __reduce_add_sync(0xffffffffu, n);
             if (lane == 0) costs[b - b0] = n;
         }
@@ -199,11 +209,21 @@ __device__ __forceinline__ RunPlan plan_tiles(const AttnShape& s, int tpi, unsig
     return *shared;
 }
 
-// Matrix descriptor of a value tile as the MN-major B operand (128-byte swizzle): 64-element blocks of the head
-// `lbo` bytes apart, groups of 8 keys 1024 bytes apart.
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t lbo) {
-    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | static_cast<uint64_t>(lbo >> 4) << 16 |
-           static_cast<uint64_t>(1024u >> 4) << 32 | static_cast<uint64_t>(1u) << 46 | static_cast<uint64_t>(2u) << 61;
+// Shared-memory matrix descriptors (128-byte swizzle, 8-row groups 1024 bytes apart) from the low word of the start
+// address.  K-major operands (queries, keys) advance 32 bytes per 16 elements inside the 128-byte row; the values are
+// the MN-major B operand, with 64-element blocks of the head `leading` bytes apart, and advance 16 rows per 16 keys.
+__device__ __forceinline__ uint32_t sdesc_low(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4; }
+__device__ __forceinline__ uint64_t sdesc(uint32_t low, uint32_t leading) {
+    const uint32_t high = (1024u >> 4) | (1u << 14) | (2u << 29);   // stride offset, descriptor version, swizzle
+    return static_cast<uint64_t>(high) << 32 | (low | (leading >> 4) << 16);
+}
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred P1;\n\telect.sync _|P1, 0xffffffff;\n\tselp.b32 %0, 1, 0, P1;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
 // Instruction descriptor of kind::f16: fp32 accumulate, M = 128, N = n, A and B both bf16 or both fp16.
@@ -249,9 +269,106 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+__device__ __forceinline__ void tc_ld_f32(uint32_t taddr, float (&x)[32]) {
+    tc_ld_32x32b_x32(taddr, reinterpret_cast<uint32_t(&)[32]>(x));
+}
+
+// Waits for the tensor-memory loads; x is among them, so nothing that uses it moves before the wait.
+__device__ __forceinline__ void tc_wait_ld_of(float (&x)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]),
+                 "+f"(x[7]), "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]),
+                 "+f"(x[13]), "+f"(x[14]), "+f"(x[15]), "+f"(x[16]), "+f"(x[17]), "+f"(x[18]),
+                 "+f"(x[19]), "+f"(x[20]), "+f"(x[21]), "+f"(x[22]), "+f"(x[23]), "+f"(x[24]),
+                 "+f"(x[25]), "+f"(x[26]), "+f"(x[27]), "+f"(x[28]), "+f"(x[29]), "+f"(x[30]),
+                 "+f"(x[31])
+                 :
+                 : "memory");
+}
+
+// x[i] = -inf outside lo <= i <= hi
+__device__ __forceinline__ void mask32(float (&x)[32], int lo, int hi) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        if (i < lo || i > hi) x[i] = -INFINITY;
+}
+__device__ __forceinline__ float max32(float top, const float (&x)[32]) {
+    float a = top, b = x[0];
+#pragma unroll
+    for (int i = 1; i < 31; i += 2) {
+        a = fmaxf(a, x[i]);
+        b = fmaxf(b, x[i + 1]);
+    }
+    return fmaxf(fmaxf(a, x[31]), b);
+}
+
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The row's 128 softmax weights 2^(c s - c m) from its scores in tensor memory, packed in pairs, with their sum and
+// the scores' maximum.  Chunks of 32 scores: the next one is under way while one is worked on.
+template <typename T>
+__device__ __forceinline__ void weights128(uint32_t t_s, float m, float c, bool masked, int lo, int hi,
+                                           uint32_t (&pk)[64], float& sum, float& top) {
+    const float neg = m == -INFINITY ? 0.0f : -m * c;
+    const uint64_t c2 = pair(c, c), neg2 = pair(neg, neg);
+    uint64_t sum_a = 0, sum_b = 0;   // two zeros each
+    top = -INFINITY;
+    float x[2][32];
+    tc_ld_f32(t_s, x[0]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float(&y)[32] = x[q & 1];
+        tc_wait_ld_of(y);
+        if (q < 3) tc_ld_f32(t_s + (q + 1) * 32, x[(q + 1) & 1]);
+        if (masked) mask32(y, lo - q * 32, hi - q * 32);
+        top = max32(top, y);
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            float a0, a1, b0, b1;
+            unpair(fma2(pair(y[i], y[i + 1]), c2, neg2), a0, a1);
+            unpair(fma2(pair(y[i + 2], y[i + 3]), c2, neg2), b0, b1);
+            a0 = ex2(a0);
+            a1 = ex2(a1);
+            b0 = ex2(b0);
+            b1 = ex2(b1);
+            sum_a = add2(sum_a, pair(a0, a1));
+            sum_b = add2(sum_b, pair(b0, b1));
+            pk[q * 16 + i / 2] = pack2<T>(a0, a1);
+            pk[q * 16 + i / 2 + 1] = pack2<T>(b0, b1);
+        }
+    }
+    float s0, s1;
+    unpair(add2(sum_a, sum_b), s0, s1);
+    sum = s0 + s1;
+}
+
 // mbar_wait with one answer for the whole warp.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
+}
+
+// The item's tile whose last rows lie past the sequence's end inside a page, if it is in this run; else -1.
+__device__ __forceinline__ int ragged_tile(const TileWalk& w, int box_slots) {
+    const int j = w.sq.keys / kTileKeys - w.it.tile0;
+    return j >= w.t0 && j < w.t1 && (w.sq.keys & (box_slots - 1)) != 0 ? j : -1;
 }
 
 template <typename T, int DP>
@@ -307,13 +424,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     fence_proxy_async_smem();   // the plan's and the zeros' generic writes before the first loads
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
     const int* abort_flag = &s_abort;
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         TileWalk w;
-        w.start(sh, 2 * tpg, plan);
+        bool more_items = w.start(sh, 2 * tpg, plan);
         if (warp == 9) {
             // ------------------------------------------------ loads
             uint32_t stage = 0, round = 0, item_no[2] = {0, 0};
@@ -342,9 +458,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     ++round;
                 }
             };
-            while (w.left > 0 && ok) {
+            while (more_items && ok) {
                 const int32_t* pages = sh.block_table + w.b * sh.table_stride;
-                const int key0 = (w.it.unit0 + w.uo) * kTileKeys;
+                const int key0 = (w.it.tile0 + w.t0) * kTileKeys, take = w.t1 - w.t0;
                 const int groups = w.groups(tpg);
                 for (int i = 0; i < groups && ok; ++i) {
                     if (item_no[i] > 0)
@@ -361,11 +477,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     __syncwarp();
                     if (i == 0) load_tile(&kmap, key0, pages);
                 }
-                for (int j = 0; j < w.take && ok; ++j) {
+                for (int j = 0; j < take && ok; ++j) {
                     load_tile(&vmap, key0 + j * kTileKeys, pages);
-                    if (ok && j + 1 < w.take) load_tile(&kmap, key0 + (j + 1) * kTileKeys, pages);
+                    if (ok && j + 1 < take) load_tile(&kmap, key0 + (j + 1) * kTileKeys, pages);
                 }
-                w.next(sh, 2 * tpg);
+                more_items = w.next(sh, 2 * tpg);
             }
             if (!ok && !*reinterpret_cast<volatile int*>(&s_abort)) {
                 if (lane == 0) {
@@ -382,101 +498,84 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int i = 0; i < 2; ++i)
                     if (item_no[i] > 0) mbar_wait(smem_u32(&s_q_full[i]), (item_no[i] - 1) & 1u, &never, 1000000);
             }
-        } else if (warp == 8) {
-            // ------------------------------------------------ MMAs (lane 0 issues)
+        } else if (warp == 8 && elect_one()) {
+            // ------------------------------------------------ MMAs, issued by one thread
             constexpr uint32_t kIdescQK = idesc_f16<T>(kTileKeys, false);
             constexpr uint32_t kIdescPV = idesc_f16<T>(DP, true);
-            uint32_t stage = 0, round = 0, item_no[2] = {0, 0}, tile_no[2] = {0, 0};
-            bool ok = true;
+            uint32_t stage = 0, parity = 0, q_parity[2] = {0, 0}, p_parity[2] = {0, 0};
+            auto wait = [&](uint64_t& bar, uint32_t par) { return mbar_wait(smem_u32(&bar), par, abort_flag); };
             auto advance = [&]() {
                 if (++stage == Cfg::kStages) {
                     stage = 0;
-                    ++round;
+                    parity ^= 1u;
                 }
             };
             auto qk = [&](int i, uint32_t st) {   // S_i = Q_i K^T
-                if (lane == 0) {
-                    const uint64_t a = sdesc_k_sw128(q_smem + i * Cfg::kQBytes);
-                    const uint64_t b = sdesc_k_sw128(kv_smem + st * Cfg::kStageBytes);
+                const uint32_t a = sdesc_low(q_smem + i * Cfg::kQBytes), b = sdesc_low(kv_smem + st * Cfg::kStageBytes);
 #pragma unroll
-                    for (int ks = 0; ks < DP / 16; ++ks) {
-                        const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
-                        tc_mma_ss(tmem + i * 128, a + off, b + off, kIdescQK, ks > 0 ? 1u : 0u);
-                    }
-                    tc_commit(smem_u32(&s_s_full[i]));
+                for (int ks = 0; ks < DP / 16; ++ks) {
+                    const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
+                    tc_mma_ss(kTmemS + i * 128, sdesc(a + off, 16), sdesc(b + off, 16), kIdescQK, ks > 0 ? 1u : 0u);
                 }
+                tc_commit(smem_u32(&s_s_full[i]));
             };
-            while (w.left > 0 && ok) {
-                const int groups = w.groups(tpg);
-                const int key0 = (w.it.unit0 + w.uo) * kTileKeys;
-                for (int i = 0; i < groups && ok; ++i) {
-                    ok = warp_wait(smem_u32(&s_q_full[i]), item_no[i] & 1u, abort_flag);
-                    if (ok && i == 0) ok = warp_wait(smem_u32(&s_kv_full[stage]), round & 1u, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    qk(i, stage);
-                    if (w.take == 1 && lane == 0) tc_commit(smem_u32(&s_q_empty[i]));
-                    ++item_no[i];
-                }
-                if (!ok) break;
-                if (lane == 0) tc_commit(smem_u32(&s_kv_empty[stage]));
-                advance();
-                for (int j = 0; j < w.take && ok; ++j) {
-                    const uint32_t vst = stage;
-                    ok = warp_wait(smem_u32(&s_kv_full[vst]), round & 1u, abort_flag);
-                    if (!ok) break;
-                    advance();
-                    // values past the sequence's end are whatever the page holds: zeros, for 0 x NaN is NaN
-                    const int past = w.sq.keys - (key0 + j * kTileKeys);
-                    if (past < kTileKeys && past % p.box_slots != 0 && past > 0) {
-                        const int end = (past / p.box_slots + 1) * p.box_slots;   // the rest was loaded as zeros
-                        for (int c = lane; c < (end - past) * (DP / 8); c += 32) {
-                            const int r = past + c / (DP / 8), x = c % (DP / 8);
-                            *reinterpret_cast<uint4*>(kv_ptr + vst * Cfg::kStageBytes + (x >> 3) * (kTileKeys * 128) +
-                                                      r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    const bool more = j + 1 < w.take;
-                    for (int i = 0; i < groups && ok; ++i) {
-                        ok = warp_wait(smem_u32(&s_p_full[i]), tile_no[i] & 1u, abort_flag);
-                        if (!ok) break;
-                        ++tile_no[i];
+            auto run = [&]() -> bool {
+                for (; more_items; more_items = w.next(sh, 2 * tpg)) {
+                    const int groups = w.groups(tpg);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (i >= groups) break;
+                        if (!wait(s_q_full[i], q_parity[i])) return false;
+                        q_parity[i] ^= 1u;
+                        if (i == 0 && !wait(s_kv_full[stage], parity)) return false;
                         tc_fence_after();
-                        if (lane == 0) {
-                            const uint64_t b = sdesc_mn_sw128(kv_smem + vst * Cfg::kStageBytes, kTileKeys * 128);
+                        qk(i, stage);
+                        if (w.t1 - w.t0 == 1) tc_commit(smem_u32(&s_q_empty[i]));
+                    }
+                    tc_commit(smem_u32(&s_kv_empty[stage]));
+                    advance();
+                    for (int j = w.t0; j < w.t1; ++j) {
+                        const uint32_t vst = stage;
+                        if (!wait(s_kv_full[vst], parity)) return false;
+                        advance();
+                        const bool more = j + 1 < w.t1;
+                        const uint32_t b = sdesc_low(kv_smem + vst * Cfg::kStageBytes);
+                        const uint32_t acc = j > w.t0 ? 1u : 0u;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (i >= groups) break;
+                            if (!wait(s_p_full[i], p_parity[i])) return false;
+                            p_parity[i] ^= 1u;
+                            tc_fence_after();
 #pragma unroll
                             for (int ks = 0; ks < kTileKeys / 16; ++ks)
-                                tc_mma_ts(tmem + Cfg::kTmemO + i * DP, tmem + i * 128 + ks * 8,
-                                          b + ((ks * 16 * 128) >> 4), kIdescPV, j > 0 || ks > 0 ? 1u : 0u);
-                            if (!more) tc_commit(smem_u32(&s_o_full[i]));
+                                tc_mma_ts(kTmemO + i * DP, kTmemS + i * 128 + ks * 8,
+                                          sdesc(b + ((ks * 16 * 128) >> 4), kTileKeys * 128), kIdescPV,
+                                          ks > 0 ? 1u : acc);
+                            if (more) {
+                                if (i == 0 && !wait(s_kv_full[stage], parity)) return false;
+                                tc_fence_after();
+                                qk(i, stage);
+                                if (j + 2 == w.t1) tc_commit(smem_u32(&s_q_empty[i]));
+                            } else {
+                                tc_commit(smem_u32(&s_o_full[i]));
+                            }
                         }
+                        tc_commit(smem_u32(&s_kv_empty[vst]));
                         if (more) {
-                            if (i == 0) ok = warp_wait(smem_u32(&s_kv_full[stage]), round & 1u, abort_flag);
-                            if (!ok) break;
-                            tc_fence_after();
-                            qk(i, stage);
-                            if (j + 2 == w.take && lane == 0) tc_commit(smem_u32(&s_q_empty[i]));
+                            tc_commit(smem_u32(&s_kv_empty[stage]));
+                            advance();
                         }
                     }
-                    if (!ok) break;
-                    if (lane == 0) tc_commit(smem_u32(&s_kv_empty[vst]));
-                    if (more) {
-                        if (lane == 0) tc_commit(smem_u32(&s_kv_empty[stage]));
-                        advance();
-                    }
                 }
-                w.next(sh, 2 * tpg);
-            }
-            if (!ok && lane == 0) {
-                if (!*reinterpret_cast<volatile int*>(&s_abort)) {
-                    s_abort = 1;
-                    set_error(sh.err, KT_DEVERR_TIMEOUT_MMA);
-                }
+                return true;
+            };
+            if (!run() && !*reinterpret_cast<volatile int*>(&s_abort)) {
+                s_abort = 1;
+                set_error(sh.err, KT_DEVERR_TIMEOUT_MMA);
             }
             // every MMA has ended before the tensor memory is freed
-            if (lane == 0) tc_commit(smem_u32(&s_done));
+            tc_commit(smem_u32(&s_done));
             int never = 0;
             mbar_wait(smem_u32(&s_done), 0, &never);
         }
@@ -486,14 +585,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int grp = warp >> 2;
         const int row = tid & 127;
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t t_s = tmem + lane_base + grp * 128;
-        const uint32_t t_o = tmem + lane_base + Cfg::kTmemO + grp * DP;
+        const uint32_t t_s = kTmemS + lane_base + grp * 128;
+        const uint32_t t_o = kTmemO + lane_base + grp * DP;
         const float c = sh.scale_log2;
-        uint32_t tile_no = 0, item_no = 0;
+        uint32_t tile_no = 0, item_no = 0, loads = 0;   // loads: key and value tiles of the items so far
         bool ok = true;
         TileWalk w;
-        w.start(sh, 2 * tpg, plan);
-        for (; w.left > 0 && ok; w.next(sh, 2 * tpg)) {
+        for (bool more = w.start(sh, 2 * tpg, plan); more && ok; more = w.next(sh, 2 * tpg)) {
             if (grp >= w.groups(tpg)) continue;
             const int tok = (w.rt * 2 + grp) * tpg + row / sh.group;
             const bool valid = row / sh.group < tpg && tok < w.sq.q_len;
@@ -501,84 +599,83 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // keys [first, last] are seen; rows of no token compute without masks and are not stored
             const int last = valid ? min(pos, w.sq.keys - 1) : 0x7fffffff;
             const int first = valid ? window_start(pos, sh.window) : 0;
-            const int key_base = (w.it.unit0 + w.uo) * kTileKeys;
+            const int rag = ragged_tile(w, p.box_slots);
             float m = -INFINITY, l = 0.0f;
-            for (int j = 0; j < w.take; ++j) {
-                const int key0 = key_base + j * kTileKeys;
+            for (int j = w.t0; j < w.t1; ++j) {
+                const int key0 = (w.it.tile0 + j) * kTileKeys;
                 ok = warp_wait(smem_u32(&s_s_full[grp]), tile_no & 1u, abort_flag);
                 if (!ok) break;
                 ++tile_no;
                 tc_fence_after();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tc_ld_32x32b_x32(t_s + q * 32, s[q]);
-                tc_wait_ld();
-                if (__any_sync(0xffffffffu, last < key0 + kTileKeys - 1 || first > key0)) {
-                    const int hi = last - key0, lo = first - key0;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (q * 32 + i > hi || q * 32 + i < lo) s[q][i] = 0xff800000u;   // -inf
-                }
-                float top = m;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float t0 = __uint_as_float(s[q][0]), t1 = __uint_as_float(s[q][1]);
-#pragma unroll
-                    for (int i = 2; i < 32; i += 2) {
-                        t0 = fmaxf(t0, __uint_as_float(s[q][i]));
-                        t1 = fmaxf(t1, __uint_as_float(s[q][i + 1]));
+                const bool masked = __any_sync(0xffffffffu, last < key0 + kTileKeys - 1 || first > key0);
+                const int hi = last - key0, lo = first - key0;
+                float top = -INFINITY;
+                if (__any_sync(0xffffffffu, m == -INFINITY)) {   // rows that have seen no key yet: take the maximum first
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        float x[32];
+                        tc_ld_f32(t_s + q * 32, x);
+                        tc_wait_ld_of(x);
+                        if (masked) mask32(x, lo - q * 32, hi - q * 32);
+                        top = max32(top, x);
                     }
-                    top = fmaxf(top, fmaxf(t0, t1));
+                    if (m == -INFINITY) m = top;
                 }
-                // the reference follows the maximum only when that has outgrown it
-                const bool grown = (top - m) * c > kLazyLog2;   // also from -inf
-                if (__any_sync(0xffffffffu, grown)) {
+                // weights under the present reference; the maximum comes along, and where it has outgrown the
+                // reference, that follows and the weights are taken once more
+                uint32_t pk[64];
+                float sum;
+                while (true) {
+                    weights128<T>(t_s, m, c, masked, lo, hi, pk, sum, top);
+                    const bool grown = (top - m) * c > kLazyLog2;
+                    if (!__any_sync(0xffffffffu, grown)) break;
                     const float f = grown ? ex2((m - top) * c) : 1.0f;
                     if (grown) m = top;
                     l *= f;
-                    if (j > 0) {
-#pragma unroll
+                    if (j > w.t0) {
+#pragma unroll 1
                         for (int q = 0; q < DP / 32; ++q) {
-                            uint32_t o[32];
-                            tc_ld_32x32b_x32(t_o + q * 32, o);
-                            tc_wait_ld();
+                            float o[32];
+                            tc_ld_f32(t_o + q * 32, o);
+                            tc_wait_ld_of(o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            tc_st_32x32b_x32(t_o + q * 32, o);
+                            for (int i = 0; i < 32; ++i) o[i] *= f;
+                            tc_st_32x32b_x32(t_o + q * 32, reinterpret_cast<const uint32_t(&)[32]>(o));
                         }
                     }
                 }
-                const float neg = m == -INFINITY ? 0.0f : -m * c;
-                float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int e = 2 * i;
-                        const float a = ex2(fmaf(__uint_as_float(s[2 * q + (e >> 5)][e & 31]), c, neg));
-                        const float b = ex2(fmaf(__uint_as_float(s[2 * q + (e >> 5)][(e & 31) + 1]), c, neg));
-                        sum0 += a;
-                        sum1 += b;
-                        pk[i] = pack2<T>(a, b);
+                if (grp == 0 && j == rag) {
+                    // Values past the sequence's end are whatever the page holds, and 0 x NaN is NaN: zeros, before
+                    // this group lets the tile be multiplied (group 1's product is issued after it).
+                    const uint32_t load = loads + 2 * static_cast<uint32_t>(j - w.t0) + 1;   // K0 V0 K1 V1 ...
+                    const uint32_t st = load % Cfg::kStages;
+                    ok = warp_wait(smem_u32(&s_kv_full[st]), (load / Cfg::kStages) & 1u, abort_flag);
+                    if (!ok) break;
+                    const int past = w.sq.keys - key0;
+                    const int end = (past / p.box_slots + 1) * p.box_slots;   // the rest was loaded as zeros
+                    for (int i = row; i < (end - past) * (DP / 8); i += 128) {
+                        const int r = past + i / (DP / 8), x = i % (DP / 8);
+                        *reinterpret_cast<uint4*>(kv_ptr + st * Cfg::kStageBytes + (x >> 3) * (kTileKeys * 128) +
+                                                  r * 128 + (x & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
-                    tc_st_32x32b_x32(t_s + q * 32, pk);
+                    fence_proxy_async_smem();
                 }
-                l += sum0 + sum1;
+                l += sum;
+                tc_st_32x32b_x32(t_s, reinterpret_cast<const uint32_t(&)[32]>(pk[0]));
+                tc_st_32x32b_x32(t_s + 32, reinterpret_cast<const uint32_t(&)[32]>(pk[32]));
                 tc_wait_st();
                 tc_fence_before();
                 mbar_arrive(smem_u32(&s_p_full[grp]));
             }
             if (!ok) break;
+            loads += 2 * static_cast<uint32_t>(w.t1 - w.t0);
             ok = warp_wait(smem_u32(&s_o_full[grp]), item_no & 1u, abort_flag);
             if (!ok) break;
             ++item_no;
             tc_fence_after();
 
             // ---- the item's piece is complete: store it, or leave it for the join
-            const bool whole = w.uo == 0 && w.take == w.it.units;
+            const bool whole = w.t0 == 0 && w.t1 == w.it.tiles;
             const int head = w.h * sh.group + row % sh.group;
             T* dst = static_cast<T*>(p.out) + static_cast<long long>(w.sq.first_token + tok) * p.o_token +
                      static_cast<long long>(head) * p.o_head;
@@ -597,20 +694,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (whole) {
                 float inv;
                 closing(m, l, inv);
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < DP / 32; ++q) {
-                    uint32_t o[32];
-                    tc_ld_32x32b_x32(t_o + q * 32, o);
-                    tc_wait_ld();
+                    float o[32];
+                    tc_ld_f32(t_o + q * 32, o);
+                    tc_wait_ld_of(o);
                     if (valid) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 8) {
                             if (q * 32 + i >= sh.head_dim) break;
                             uint4 v;
-                            v.x = pack2<T>(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-                            v.y = pack2<T>(__uint_as_float(o[i + 2]) * inv, __uint_as_float(o[i + 3]) * inv);
-                            v.z = pack2<T>(__uint_as_float(o[i + 4]) * inv, __uint_as_float(o[i + 5]) * inv);
-                            v.w = pack2<T>(__uint_as_float(o[i + 6]) * inv, __uint_as_float(o[i + 7]) * inv);
+                            v.x = pack2<T>(o[i] * inv, o[i + 1] * inv);
+                            v.y = pack2<T>(o[i + 2] * inv, o[i + 3] * inv);
+                            v.z = pack2<T>(o[i + 4] * inv, o[i + 5] * inv);
+                            v.w = pack2<T>(o[i + 6] * inv, o[i + 7] * inv);
                             *reinterpret_cast<uint4*>(dst + q * 32 + i) = v;
                         }
                     }
@@ -618,20 +715,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 tc_fence_before();
                 continue;
             }
-            const int c0 = static_cast<int>(w.first_unit / plan.per);
-            const int c1 = static_cast<int>((w.first_unit + w.it.units - 1) / plan.per);
-            const size_t slot = 2 * blockIdx.x + (w.uo == 0 ? 1 : 0);
+            // pieces of the item: the run of its first tile (that CTA's slot 1), then the following ones (slot 0)
+            const int c0 = static_cast<int>(w.first / plan.per);
+            const int c1 = static_cast<int>((w.first + w.it.tiles - 1) / plan.per);
+            const size_t slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
             const int prow = grp * 128 + row;
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < DP / 32; ++q) {
-                uint32_t o[32];
-                tc_ld_32x32b_x32(t_o + q * 32, o);
-                tc_wait_ld();
+                float o[32];
+                tc_ld_f32(t_o + q * 32, o);
+                tc_wait_ld_of(o);
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
                     p.part_o[(slot * (DP / 4) + (q * 32 + i) / 4) * 256 + prow] =
-                        make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]),
-                                    __uint_as_float(o[i + 3]));
+                        make_float4(o[i], o[i + 1], o[i + 2],
+                                    o[i + 3]);
             }
             tc_fence_before();
             p.part_ml[slot * 256 + prow] = make_float2(m, l);
@@ -656,7 +754,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             float inv;
             closing(mt, lt, inv);
-#pragma unroll
+#pragma unroll 1
             for (int q = 0; q < DP / 32; ++q) {
                 float acc[32];
 #pragma unroll
@@ -696,7 +794,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncthreads();
     if (warp == 8) {
         tc_fence_after();
-        tc_dealloc(tmem, 512);
+        tc_dealloc(s_tmem, 512);
     }
 }
 
