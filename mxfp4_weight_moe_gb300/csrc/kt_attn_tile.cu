@@ -17,7 +17,7 @@
 // Work is dealt as in the split kernel: all items' key tiles form one line, cut
 // into equal runs; the last CTA of a cut item joins its partial sums in order.
 //
-// Warps: 0-3 softmax of group 0, 4-7 of group 1, 8 issues the MMAs, 9 the TMA loads.
+// Warps: 0-3 softmax of group 0, 4-7 of group 1, 8 issues the MMAs, 9 and 10 the TMA loads.
 #include "kt_attn_dev.cuh"
 
 namespace kt {
@@ -250,15 +250,22 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
         "r"(accumulate)
         : "memory");
 }
-__device__ __forceinline__ void tc_st_32x32b_x32(uint32_t taddr, const uint32_t (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
+__device__ __forceinline__ void tc_st_16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+                 : "memory");
+}
+__device__ __forceinline__ void tc_ld_16(uint32_t taddr, float (&x)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]), "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld_16(float (&x)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]), "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15])
+                 :
+                 : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -286,20 +293,31 @@ __device__ __forceinline__ void tc_wait_ld_of(float (&x)[32]) {
                  : "memory");
 }
 
+// Nothing that uses x moves before this point.
+__device__ __forceinline__ void pin(float (&x)[32]) {
+    asm volatile("" : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]), "+f"(x[8]), "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15]), "+f"(x[16]), "+f"(x[17]), "+f"(x[18]), "+f"(x[19]), "+f"(x[20]), "+f"(x[21]), "+f"(x[22]), "+f"(x[23]), "+f"(x[24]), "+f"(x[25]), "+f"(x[26]), "+f"(x[27]), "+f"(x[28]), "+f"(x[29]), "+f"(x[30]), "+f"(x[31]));
+}
+
 // x[i] = -inf outside lo <= i <= hi
 __device__ __forceinline__ void mask32(float (&x)[32], int lo, int hi) {
+    const uint32_t below = hi >= 31 ? 0xffffffffu : hi < 0 ? 0u : (2u << hi) - 1u;
+    const uint32_t seen = lo <= 0 ? below : lo > 31 ? 0u : below & (0xffffffffu << lo);
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        if (i < lo || i > hi) x[i] = -INFINITY;
+    for (int i = 0; i < 32; ++i) x[i] = (seen >> i) & 1u ? x[i] : -INFINITY;
 }
-__device__ __forceinline__ float max32(float top, const float (&x)[32]) {
-    float a = top, b = x[0];
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max32(const float (&x)[32]) {
+    float a = max3(x[0], x[1], x[2]), b = max3(x[3], x[4], x[5]);
 #pragma unroll
-    for (int i = 1; i < 31; i += 2) {
-        a = fmaxf(a, x[i]);
-        b = fmaxf(b, x[i + 1]);
+    for (int i = 6; i < 30; i += 4) {
+        a = max3(a, x[i], x[i + 1]);
+        b = max3(b, x[i + 2], x[i + 3]);
     }
-    return fmaxf(fmaxf(a, x[31]), b);
+    return max3(max3(a, x[30], x[31]), b, b);
 }
 
 // Pairs of fp32 in one instruction.
@@ -322,42 +340,24 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// The row's 128 softmax weights 2^(c s - c m) from its scores in tensor memory, packed in pairs, with their sum and
-// the scores' maximum.  Chunks of 32 scores: the next one is under way while one is worked on.
+// 32 softmax weights 2^(c s + neg), packed in pairs; their sum is added to `sum` (two halves).
 template <typename T>
-__device__ __forceinline__ void weights128(uint32_t t_s, float m, float c, bool masked, int lo, int hi,
-                                           uint32_t (&pk)[64], float& sum, float& top) {
-    const float neg = m == -INFINITY ? 0.0f : -m * c;
-    const uint64_t c2 = pair(c, c), neg2 = pair(neg, neg);
-    uint64_t sum_a = 0, sum_b = 0;   // two zeros each
-    top = -INFINITY;
-    float x[2][32];
-    tc_ld_f32(t_s, x[0]);
+__device__ __forceinline__ void weights32(const float (&x)[32], uint64_t c2, uint64_t neg2, uint32_t (&pk)[16],
+                                          uint64_t& sum_a, uint64_t& sum_b) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        float(&y)[32] = x[q & 1];
-        tc_wait_ld_of(y);
-        if (q < 3) tc_ld_f32(t_s + (q + 1) * 32, x[(q + 1) & 1]);
-        if (masked) mask32(y, lo - q * 32, hi - q * 32);
-        top = max32(top, y);
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            float a0, a1, b0, b1;
-            unpair(fma2(pair(y[i], y[i + 1]), c2, neg2), a0, a1);
-            unpair(fma2(pair(y[i + 2], y[i + 3]), c2, neg2), b0, b1);
-            a0 = ex2(a0);
-            a1 = ex2(a1);
-            b0 = ex2(b0);
-            b1 = ex2(b1);
-            sum_a = add2(sum_a, pair(a0, a1));
-            sum_b = add2(sum_b, pair(b0, b1));
-            pk[q * 16 + i / 2] = pack2<T>(a0, a1);
-            pk[q * 16 + i / 2 + 1] = pack2<T>(b0, b1);
-        }
+    for (int i = 0; i < 32; i += 4) {
+        float a0, a1, b0, b1;
+        unpair(fma2(pair(x[i], x[i + 1]), c2, neg2), a0, a1);
+        unpair(fma2(pair(x[i + 2], x[i + 3]), c2, neg2), b0, b1);
+        a0 = ex2(a0);
+        a1 = ex2(a1);
+        b0 = ex2(b0);
+        b1 = ex2(b1);
+        sum_a = add2(sum_a, pair(a0, a1));
+        sum_b = add2(sum_b, pair(b0, b1));
+        pk[i / 2] = pack2<T>(a0, a1);
+        pk[i / 2 + 1] = pack2<T>(b0, b1);
     }
-    float s0, s1;
-    unpair(add2(sum_a, sum_b), s0, s1);
-    sum = s0 + s1;
 }
 
 // mbar_wait with one answer for the whole warp.
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     using Cfg = TileCfg<DP>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_kv_full[Cfg::kStages], s_kv_empty[Cfg::kStages];
-    __shared__ __align__(8) uint64_t s_q_full[2], s_q_empty[2], s_s_full[2], s_p_full[2], s_o_full[2], s_done;
+    __shared__ __align__(8) uint64_t s_q_full[2], s_q_empty[2], s_s_full[2], s_p_full[2][2], s_o_full[2], s_done;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_last[2];
     __shared__ RunPlan s_plan;
@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_init(smem_u32(&s_q_full[i]), 1);
             mbar_init(smem_u32(&s_q_empty[i]), 1);
             mbar_init(smem_u32(&s_s_full[i]), 1);
-            mbar_init(smem_u32(&s_p_full[i]), 128);
+            mbar_init(smem_u32(&s_p_full[i][0]), 4);   // the group's warps
+            mbar_init(smem_u32(&s_p_full[i][1]), 4);
             mbar_init(smem_u32(&s_o_full[i]), 1);
         }
         mbar_init(smem_u32(&s_done), 1);
@@ -430,70 +431,67 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         TileWalk w;
         bool more_items = w.start(sh, 2 * tpg, plan);
-        if (warp == 9) {
-            // ------------------------------------------------ loads
-            uint32_t stage = 0, round = 0, item_no[2] = {0, 0};
+        if (warp == 9 || warp == 10) {
+            // ------------------------------------------------ loads: queries and keys by warp 9, values by warp 10
+            // (with 16-slot pages a tile takes 16 loads, which one warp cannot issue for both at the tensor cores' pace)
+            const bool values = warp == 10;
+            uint32_t load = values ? 1 : 0, item_no[2] = {0, 0};   // tiles lie in the ring as K0 V0 K1 V1 ...
             const int boxes = kTileKeys / p.box_slots;
             const int box = lane % boxes;   // of 1, 2, 4 or 8 per 64 elements (page_size is a multiple of 16)
+            const CUtensorMap* map = values ? &vmap : &kmap;
             bool ok = true;
-            // tile of keys [key0, key0 + 128) of K or V into the next stage
-            auto load_tile = [&](const CUtensorMap* map, int key0, const int32_t* pages) {
+            auto load_tile = [&](int key0, const int32_t* pages) {   // keys [key0, key0 + 128)
+                const uint32_t stage = load % Cfg::kStages, round = load / Cfg::kStages;
                 const uint32_t full = smem_u32(&s_kv_full[stage]);
+                // boxes that no row sees come from outside the cache, as zeros
+                const int key = key0 + box * p.box_slots;
+                int page = -1;
+                if (lane < boxes && key < w.it.hi && key + p.box_slots > w.it.lo) page = checked_page(sh, pages, key);
+                page = __shfl_sync(0xffffffffu, page, box);
                 if (round > 0) ok = ok && warp_wait(smem_u32(&s_kv_empty[stage]), (round - 1) & 1u, abort_flag);
                 if (!ok) return;
                 if (lane == 0) mbar_arrive_expect_tx(full, Cfg::kStageBytes);
                 __syncwarp();
                 if (lane < boxes * (DP / 64)) {
                     const int x = lane / boxes;
-                    const int key = key0 + box * p.box_slots;
-                    // boxes that no row sees come from outside the cache, as zeros
-                    const int page =
-                        key < w.it.hi && key + p.box_slots > w.it.lo ? checked_page(sh, pages, key) : -1;
                     tma_load_4d(kv_smem + stage * Cfg::kStageBytes + x * (kTileKeys * 128) + box * p.box_slots * 128,
                                 map, full, x * 64, key % sh.page_size, w.h, page);
                 }
                 __syncwarp();
-                if (++stage == Cfg::kStages) {
-                    stage = 0;
-                    ++round;
-                }
+                load += 2;
             };
-            while (more_items && ok) {
+            for (; more_items && ok; more_items = w.next(sh, 2 * tpg)) {
                 const int32_t* pages = sh.block_table + w.b * sh.table_stride;
-                const int key0 = (w.it.tile0 + w.t0) * kTileKeys, take = w.t1 - w.t0;
-                const int groups = w.groups(tpg);
-                for (int i = 0; i < groups && ok; ++i) {
-                    if (item_no[i] > 0)
-                        ok = warp_wait(smem_u32(&s_q_empty[i]), (item_no[i] - 1) & 1u, abort_flag);
-                    if (!ok) break;
-                    ++item_no[i];
-                    if (lane == 0) {
-                        const uint32_t bar = smem_u32(&s_q_full[i]);
-                        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(tpg * sh.group * DP * 2));
-                        for (int x = 0; x < DP; x += 64)
-                            tma_load_3d(q_smem + i * Cfg::kQBytes + (x / 64) * (128 * 128), &qmap, bar, x,
-                                        w.h * sh.group, w.sq.first_token + (w.rt * 2 + i) * tpg);
+                if (!values) {
+                    const int groups = w.groups(tpg);
+                    for (int i = 0; i < groups && ok; ++i) {
+                        if (item_no[i] > 0)
+                            ok = warp_wait(smem_u32(&s_q_empty[i]), (item_no[i] - 1) & 1u, abort_flag);
+                        if (!ok) break;
+                        ++item_no[i];
+                        if (lane == 0) {
+                            const uint32_t bar = smem_u32(&s_q_full[i]);
+                            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(tpg * sh.group * DP * 2));
+                            for (int x = 0; x < DP; x += 64)
+                                tma_load_3d(q_smem + i * Cfg::kQBytes + (x / 64) * (128 * 128), &qmap, bar, x,
+                                            w.h * sh.group, w.sq.first_token + (w.rt * 2 + i) * tpg);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    if (i == 0) load_tile(&kmap, key0, pages);
                 }
-                for (int j = 0; j < take && ok; ++j) {
-                    load_tile(&vmap, key0 + j * kTileKeys, pages);
-                    if (ok && j + 1 < take) load_tile(&kmap, key0 + (j + 1) * kTileKeys, pages);
-                }
-                more_items = w.next(sh, 2 * tpg);
+                for (int j = w.t0; j < w.t1 && ok; ++j) load_tile((w.it.tile0 + j) * kTileKeys, pages);
             }
-            if (!ok && !*reinterpret_cast<volatile int*>(&s_abort)) {
-                if (lane == 0) {
+            if (!ok) {
+                if (lane == 0 && !*reinterpret_cast<volatile int*>(&s_abort)) {
                     s_abort = 1;
                     set_error(sh.err, KT_DEVERR_TIMEOUT_LOAD);
                 }
-            }
-            if (!ok) {   // loads still in flight land before the CTA ends (each wait bounded)
+                // loads still in flight land before the CTA ends (each wait bounded)
                 int never = 0;
-                for (uint32_t i = 0; i < Cfg::kStages; ++i) {
-                    const uint32_t r = i < stage ? round : round - 1;   // the stage's last load
-                    if (i < stage || round > 0) mbar_wait(smem_u32(&s_kv_full[i]), r & 1u, &never, 1000000);
+                for (int i = 0; i < Cfg::kStages && load >= 2; ++i) {
+                    load -= 2;
+                    mbar_wait(smem_u32(&s_kv_full[load % Cfg::kStages]), (load / Cfg::kStages) & 1u, &never, 1000000);
+                    if (load < 2) break;
                 }
                 for (int i = 0; i < 2; ++i)
                     if (item_no[i] > 0) mbar_wait(smem_u32(&s_q_full[i]), (item_no[i] - 1) & 1u, &never, 1000000);
@@ -544,14 +542,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             if (i >= groups) break;
-                            if (!wait(s_p_full[i], p_parity[i])) return false;
-                            p_parity[i] ^= 1u;
+                            if (!wait(s_p_full[i][0], p_parity[i])) return false;
                             tc_fence_after();
 #pragma unroll
-                            for (int ks = 0; ks < kTileKeys / 16; ++ks)
+                            for (int ks = 0; ks < kTileKeys / 16; ++ks) {
+                                if (ks == kTileKeys / 16 * 3 / 4) {
+                                    if (!wait(s_p_full[i][1], p_parity[i])) return false;
+                                    tc_fence_after();
+                                }
                                 tc_mma_ts(kTmemO + i * DP, kTmemS + i * 128 + ks * 8,
                                           sdesc(b + ((ks * 16 * 128) >> 4), kTileKeys * 128), kIdescPV,
                                           ks > 0 ? 1u : acc);
+                            }
+                            p_parity[i] ^= 1u;
                             if (more) {
                                 if (i == 0 && !wait(s_kv_full[stage], parity)) return false;
                                 tc_fence_after();
@@ -609,38 +612,33 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 tc_fence_after();
                 const bool masked = __any_sync(0xffffffffu, last < key0 + kTileKeys - 1 || first > key0);
                 const int hi = last - key0, lo = first - key0;
-                float top = -INFINITY;
-                if (__any_sync(0xffffffffu, m == -INFINITY)) {   // rows that have seen no key yet: take the maximum first
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        float x[32];
-                        tc_ld_f32(t_s + q * 32, x);
-                        tc_wait_ld_of(x);
-                        if (masked) mask32(x, lo - q * 32, hi - q * 32);
-                        top = max32(top, x);
-                    }
-                    if (m == -INFINITY) m = top;
+                float x[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tc_ld_f32(t_s + q * 32, x[q]);
+                tc_wait_ld_of(x[0]);
+#pragma unroll
+                for (int q = 1; q < 4; ++q) pin(x[q]);
+                if (masked) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (__any_sync(0xffffffffu, hi < q * 32 + 31 || lo > q * 32)) mask32(x[q], lo - q * 32, hi - q * 32);
                 }
-                // weights under the present reference; the maximum comes along, and where it has outgrown the
-                // reference, that follows and the weights are taken once more
-                uint32_t pk[64];
-                float sum;
-                while (true) {
-                    weights128<T>(t_s, m, c, masked, lo, hi, pk, sum, top);
-                    const bool grown = (top - m) * c > kLazyLog2;
-                    if (!__any_sync(0xffffffffu, grown)) break;
+                const float top = max3(max3(max32(x[0]), max32(x[1]), max32(x[2])), max32(x[3]), m);
+                // the reference follows the maximum only when that has outgrown it (also from -inf)
+                const bool grown = (top - m) * c > kLazyLog2;
+                if (__any_sync(0xffffffffu, grown)) {
                     const float f = grown ? ex2((m - top) * c) : 1.0f;
                     if (grown) m = top;
                     l *= f;
                     if (j > w.t0) {
 #pragma unroll 1
-                        for (int q = 0; q < DP / 32; ++q) {
-                            float o[32];
-                            tc_ld_f32(t_o + q * 32, o);
-                            tc_wait_ld_of(o);
+                        for (int q = 0; q < DP / 16; ++q) {
+                            float o[16];
+                            tc_ld_16(t_o + q * 16, o);
+                            tc_wait_ld_16(o);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] *= f;
-                            tc_st_32x32b_x32(t_o + q * 32, reinterpret_cast<const uint32_t(&)[32]>(o));
+                            for (int i = 0; i < 16; ++i) o[i] *= f;
+                            tc_st_16(t_o + q * 16, reinterpret_cast<const uint32_t(&)[16]>(o));
                         }
                     }
                 }
@@ -660,12 +658,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                l += sum;
-                tc_st_32x32b_x32(t_s, reinterpret_cast<const uint32_t(&)[32]>(pk[0]));
-                tc_st_32x32b_x32(t_s + 32, reinterpret_cast<const uint32_t(&)[32]>(pk[32]));
-                tc_wait_st();
-                tc_fence_before();
-                mbar_arrive(smem_u32(&s_p_full[grp]));
+                const float neg = m == -INFINITY ? 0.0f : -m * c;
+                const uint64_t c2 = pair(c, c), neg2 = pair(neg, neg);
+                uint64_t sum_a = 0, sum_b = 0;   // two zeros each
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t pk[16];
+                    weights32<T>(x[q], c2, neg2, pk, sum_a, sum_b);
+                    tc_st_16(t_s + q * 16, pk);
+                    if (q >= 2) {   // three quarters of the keys, then the rest: the product starts with the first
+                        tc_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&s_p_full[grp][q - 2]));
+                    }
+                }
+                float s0, s1;
+                unpair(add2(sum_a, sum_b), s0, s1);
+                l += s0 + s1;
             }
             if (!ok) break;
             loads += 2 * static_cast<uint32_t>(w.t1 - w.t0);
