@@ -116,7 +116,9 @@ kt_status kt_kv_append(const kt_paged_kv* cache, const kt_paged_batch* batch, co
                        const kt_heads* q, const kt_heads* q_out, const kt_head_transform* transform, int* err,
                        void* stream);
 
-/* Workspace bytes of kt_paged_attention on the current device (0 on an error). */
+/* Workspace bytes of kt_paged_attention on the current device.  Its first
+ * KT_PAGED_ATTENTION_ZEROED bytes are counters. */
+#define KT_PAGED_ATTENTION_ZEROED 4096
 size_t kt_paged_attention_workspace_bytes(void);
 
 /*
@@ -130,7 +132,8 @@ size_t kt_paged_attention_workspace_bytes(void);
  *              only; results hold for any value)
  *   scale      finite, > 0
  *   ws         >= kt_paged_attention_workspace_bytes() bytes, 256-byte aligned,
- *              ZEROED before its first use; every call leaves its counters zero
+ *              its first KT_PAGED_ATTENTION_ZEROED bytes zeroed before the first
+ *              use; every call leaves them zero
  * q and out: 16-byte aligned, strides multiples of 8 elements.
  */
 kt_status kt_paged_attention(const kt_paged_kv* cache, const kt_paged_batch* batch, const kt_heads* q,

@@ -15,6 +15,8 @@ included, so that its last new token has position seq_lens[b] - 1).
 from __future__ import annotations
 
 import ctypes
+import struct
+import threading
 
 import torch
 
@@ -27,82 +29,82 @@ ROPE_STYLES = {"halves": 0, "interleaved": 1}
 KT_DEVERR_BAD_PAGE = 0x20
 KT_DEVERR_BAD_POSITION = 0x40
 
-_VP, _I, _I64, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
+# The descriptors of kt_attn.h as packed fields (64-bit hosts).  A decode step's calls take a few microseconds on the
+# GPU, so a call packs its descriptors into one buffer of the thread's and passes addresses in it.
+HEADS = "Pqqixxxx"                    # kt_heads: ptr, token_stride, head_stride, heads
+PAGED_KV = "PPqqqqqqiiiiixxxx"        # kt_paged_kv: k, v, strides, num_pages, page_size, heads, head_dim, dtype
+PAGED_BATCH = "PqixxxxPPii"           # kt_paged_batch: block_table, table_stride, max_pages, cu_q, seq_lens, seqs, tokens
+HEAD_TRANSFORM = "PiiixxxxPPif"       # kt_head_transform: table, positions, rotary_dim, style, weights, dtype, eps
+_HEADS_BYTES, _BATCH_BYTES = struct.calcsize(HEADS), struct.calcsize(PAGED_BATCH)
+_NORM_CALL = struct.Struct(HEAD_TRANSFORM + 4 * HEADS)
+_APPEND_CALL = struct.Struct(HEAD_TRANSFORM + PAGED_BATCH + 4 * HEADS)
+_ATTEND_CALL = struct.Struct(PAGED_BATCH + 2 * HEADS)
+_TRANSFORM_BYTES = struct.calcsize(HEAD_TRANSFORM)
+_NO_HEADS = (0, 0, 0, 0)
+
+WORKSPACE_ZEROED = 4096   # KT_PAGED_ATTENTION_ZEROED
 
 
-class Heads(ctypes.Structure):
-    _fields_ = [("ptr", _VP), ("token_stride", _I64), ("head_stride", _I64), ("heads", _I)]
+class _Buffer(threading.local):
+    def __init__(self):
+        self.buf = ctypes.create_string_buffer(512)
+        self.at = ctypes.addressof(self.buf)
 
 
-class PagedKVDesc(ctypes.Structure):
-    _fields_ = [("k", _VP), ("v", _VP),
-                ("k_page_stride", _I64), ("k_slot_stride", _I64), ("k_head_stride", _I64),
-                ("v_page_stride", _I64), ("v_slot_stride", _I64), ("v_head_stride", _I64),
-                ("num_pages", _I), ("page_size", _I), ("heads", _I), ("head_dim", _I), ("dtype", _I)]
+_buffer = _Buffer()
 
-
-class PagedBatch(ctypes.Structure):
-    _fields_ = [("block_table", _VP), ("table_stride", _I64), ("max_pages", _I), ("cu_q", _VP), ("seq_lens", _VP),
-                ("seqs", _I), ("tokens", _I)]
-
-
-class HeadTransform(ctypes.Structure):
-    _fields_ = [("table", _VP), ("positions", _I), ("rotary_dim", _I), ("style", _I), ("q_weight", _VP),
-                ("k_weight", _VP), ("weight_dtype", _I), ("eps", _F)]
-
-
-_P = ctypes.POINTER
+_VP, _I, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 SIGNATURES = {
-    "kt_qk_norm_rope": ([_P(Heads), _P(Heads), _P(Heads), _P(Heads), _VP, _I, _I, _I, _P(HeadTransform), _VP, _VP], _I),
-    "kt_kv_append": ([_P(PagedKVDesc), _P(PagedBatch), _P(Heads), _P(Heads), _P(Heads), _P(Heads), _P(HeadTransform),
-                      _VP, _VP], _I),
+    "kt_qk_norm_rope": ([_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _VP, _VP, _VP], _I),
+    "kt_kv_append": ([_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], _I),
     "kt_paged_attention_workspace_bytes": ([], ctypes.c_size_t),
-    "kt_paged_attention": ([_P(PagedKVDesc), _P(PagedBatch), _P(Heads), _P(Heads), _I, _F, _I, _VP, _VP, _VP,
-                            ctypes.c_size_t, _VP], _I),
+    "kt_paged_attention": ([_VP, _VP, _VP, _VP, _I, _F, _I, _VP, _VP, _VP, ctypes.c_size_t, _VP], _I),
 }
 
 
-def _heads(t, name: str, dtype, dim: int, device, tokens: int | None = None, heads: int | None = None) -> Heads:
-    """Descriptor of a [tokens, heads, dim] tensor with contiguous heads."""
+def _heads(t, name: str, dtype, dim: int, device: int, tokens: int, heads: int):
+    """(ptr, token stride, head stride, heads) of a [tokens, heads, dim] tensor with contiguous heads on CUDA device
+    `device` (tokens, heads: -1 for any)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device or device < 0:
+        raise ValueError(f"{name} is on {t.device}, expected " + (f"cuda:{device}" if device >= 0 else "a CUDA device"))
     shape = t.shape
-    if len(shape) != 3 or shape[2] != dim or (tokens is not None and shape[0] != tokens) or \
-            (heads is not None and shape[1] != heads):
-        raise ValueError(f"{name} must be [{'tokens' if tokens is None else tokens}, "
-                         f"{'heads' if heads is None else heads}, {dim}], got {tuple(shape)}")
-    if t.device != device or not t.is_cuda:
-        raise ValueError(f"{name} is on {t.device}, expected {device if device.type == 'cuda' else 'a CUDA device'}")
-    st = t.stride()
-    if st[2] != 1 and dim != 1:
-        raise ValueError(f"{name}: the elements of a head must be contiguous, strides are {st}")
+    if len(shape) != 3 or shape[2] != dim or (tokens >= 0 and shape[0] != tokens) or (heads >= 0 and shape[1] != heads):
+        raise ValueError(f"{name} must be [{tokens if tokens >= 0 else 'tokens'}, {heads if heads >= 0 else 'heads'}, "
+                         f"{dim}], got {tuple(shape)}")
+    by_token, by_head, by_element = t.stride()
+    if by_element != 1 and dim != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous, strides are {t.stride()}")
     # the stride of a dimension of one entry says nothing
-    return Heads(t.data_ptr(), st[0] if shape[0] > 1 else dim, st[1] if shape[1] > 1 else dim, shape[1])
+    n, h, _ = shape
+    return t.data_ptr(), (by_token if n > 1 else dim), (by_head if h > 1 else dim), h
 
 
 def _written(t, name: str):
     """An output whose elements overlap would be written by several threads at once."""
-    shape, st = t.shape, t.stride()
-    if t.numel() and ((shape[1] > 1 and st[1] < shape[2]) or (shape[0] > 1 and st[0] < shape[2])
-                      or (shape[0] > 1 and shape[1] > 1
-                          and st[0] < (shape[1] - 1) * st[1] + shape[2] and st[1] < (shape[0] - 1) * st[0] + shape[2])):
+    if t.is_contiguous():
+        return
+    (n, h, d), st = t.shape, t.stride()
+    if t.numel() and ((h > 1 and st[1] < d) or (n > 1 and st[0] < d)
+                      or (n > 1 and h > 1 and st[0] < (h - 1) * st[1] + d and st[1] < (n - 1) * st[0] + d)):
         raise ValueError(f"{name}: its rows overlap, strides are {st}")
 
 
-def _ints(t, name: str, ndim: int, device):
+def _ints(t, name: str, ndim: int, device: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not torch.int32:
         raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-    if t.dim() != ndim or t.device != device:
-        raise ValueError(f"{name} must have {ndim} dims on {device}, got {tuple(t.shape)} on {t.device}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.dim() != ndim or t.get_device() != device:
+        raise ValueError(f"{name} must have {ndim} dims on cuda:{device}, got {tuple(t.shape)} on {t.device}")
+    if not t.is_contiguous() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous")
 
 
-def _batch(block_table, cu_q, seq_lens, tokens: int, device) -> PagedBatch:
+def _batch(block_table, cu_q, seq_lens, tokens: int, device: int):
     _ints(block_table, "block_table", 2, device)
     _ints(cu_q, "cu_q", 1, device)
     _ints(seq_lens, "seq_lens", 1, device)
@@ -110,53 +112,63 @@ def _batch(block_table, cu_q, seq_lens, tokens: int, device) -> PagedBatch:
     if seq_lens.shape[0] != seqs or cu_q.shape[0] != seqs + 1:
         raise ValueError(f"block_table {tuple(block_table.shape)}, cu_q {tuple(cu_q.shape)} and seq_lens "
                          f"{tuple(seq_lens.shape)} must be [B, max_pages], [B + 1] and [B]")
-    return PagedBatch(block_table.data_ptr(), block_table.stride(0) if seqs > 1 else max_pages, max_pages,
-                      cu_q.data_ptr(), seq_lens.data_ptr(), seqs, tokens)
+    return (block_table.data_ptr(), block_table.stride(0) if seqs > 1 else max_pages, max_pages, cu_q.data_ptr(),
+            seq_lens.data_ptr(), seqs, tokens)
 
 
-def _transform(table, q_weight, k_weight, eps: float, style: str, dtype, dim: int, device) -> HeadTransform:
-    t = HeadTransform()
-    t.eps = eps
+def _weight(w, name: str, dtype, dim: int, device: int):
+    if w.dtype is not dtype and w.dtype is not torch.float32:
+        raise TypeError(f"{name} must be {dtype} or torch.float32, got {w.dtype}")
+    if w.shape != (dim,) or w.get_device() != device or not w.is_contiguous():
+        raise ValueError(f"{name} must be contiguous [{dim}] on cuda:{device}")
+    return w.data_ptr()
+
+
+def _transform(table, q_weight, k_weight, eps: float, style: str, dtype, dim: int, device: int):
+    t = positions = rot = code = qw = kw = weight_dtype = 0
     if table is not None:
         if table.dtype is not torch.float32:
             raise TypeError(f"table must be torch.float32, got {table.dtype}")
-        if table.dim() != 2 or table.device != device or not table.is_contiguous():
-            raise ValueError(f"table must be contiguous [positions, rotary_dim] on {device}")
+        if table.dim() != 2 or table.get_device() != device or not table.is_contiguous():
+            raise ValueError(f"table must be contiguous [positions, rotary_dim] on cuda:{device}")
         if style not in ROPE_STYLES:
             raise ValueError(f"style must be one of {tuple(ROPE_STYLES)}")
-        t.table = table.data_ptr()
-        t.positions, t.rotary_dim = table.shape
-        t.style = ROPE_STYLES[style]
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is None:
-            continue
-        if w.dtype is not dtype and w.dtype is not torch.float32:
-            raise TypeError(f"{name} must be {dtype} or torch.float32, got {w.dtype}")
-        if w.shape != (dim,) or w.device != device or not w.is_contiguous():
-            raise ValueError(f"{name} must be contiguous [{dim}] on {device}")
-        setattr(t, name, w.data_ptr())
-        t.weight_dtype = DTYPE_CODES.get(w.dtype, KT_DTYPE_F32)
-    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
-        raise TypeError("q_weight and k_weight must have one dtype")
-    return t
+        t, (positions, rot), code = table.data_ptr(), table.shape, ROPE_STYLES[style]
+    if q_weight is not None:
+        qw = _weight(q_weight, "q_weight", dtype, dim, device)
+        weight_dtype = DTYPE_CODES.get(q_weight.dtype, KT_DTYPE_F32)
+    if k_weight is not None:
+        kw = _weight(k_weight, "k_weight", dtype, dim, device)
+        weight_dtype = DTYPE_CODES.get(k_weight.dtype, KT_DTYPE_F32)
+        if q_weight is not None and q_weight.dtype is not k_weight.dtype:
+            raise TypeError("q_weight and k_weight must have one dtype")
+    return t, positions, rot, code, qw, kw, weight_dtype, eps
 
 
-class _allocating_on:
-    """Tensors made inside belong to `stream` (None: the current one), whose pointer is `.ptr`."""
-    __slots__ = ("ctx", "ptr")
+def _output(like, stream):
+    """A contiguous output of like's shape that belongs to `stream` (None: the current one)."""
+    if stream is None:
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
 
-    def __init__(self, stream, device):
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
-        self.ptr = kt._stream_ptr(stream, device)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self
+_functions = {}
 
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+
+def _call(device: int, stream, name: str, *args):
+    """The library's `name` on the device, with args and the stream's pointer."""
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(kt.lib(), name)
+    ptr = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == device:
+        status = fn(*args, ptr)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, ptr)
+    if status:
+        kt._check(status, name)
 
 
 def rope_table(positions: int, rotary_dim: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -181,33 +193,38 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     [1] tensor that gets KT_DEVERR_BAD_POSITION for a position outside the table (that token is not written)."""
     if not isinstance(q, torch.Tensor) or q.dtype not in DTYPE_CODES or q.dim() != 3:
         raise TypeError("q must be a bf16 or fp16 tensor [tokens, heads, head_dim]")
-    dev, dt = q.device, q.dtype
-    n, _, dim = q.shape
-    hq = _heads(q, "q", dt, dim, dev)
-    hk = None if k is None else _heads(k, "k", dt, dim, dev, n)
+    dev, dt = q.get_device(), q.dtype
+    n, heads, dim = q.shape
+    hq = _heads(q, "q", dt, dim, dev, -1, -1)
+    hk = _NO_HEADS if k is None else _heads(k, "k", dt, dim, dev, n, -1)
+    pos = 0
     if table is not None:
         if positions is None:
             raise ValueError("a rotation needs positions")
         _ints(positions, "positions", 1, dev)
         if positions.shape[0] != n:
             raise ValueError(f"positions must be [{n}]")
+        pos = positions.data_ptr()
     tf = _transform(table, q_weight, k_weight, eps, style, dt, dim, dev)
     if error is not None:
         _ints(error, "error", 1, dev)
-    with _allocating_on(stream, dev) as s:
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dt, device=dev)
+    if q_out is None:
+        q_out = _output(q, stream)
+    else:
+        _written(q_out, "q_out")
+    hqo, hko = _heads(q_out, "q_out", dt, dim, dev, n, heads), _NO_HEADS
+    if k is not None:
+        if k_out is None:
+            k_out = _output(k, stream)
         else:
-            _written(q_out, "q_out")
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=dt, device=dev)
-        elif k_out is not None:
             _written(k_out, "k_out")
-    hqo = _heads(q_out, "q_out", dt, dim, dev, n, q.shape[1])
-    hko = None if k is None else _heads(k_out, "k_out", dt, dim, dev, n, k.shape[1])
-    with kt._on_device(dev):
-        kt._check(kt.lib().kt_qk_norm_rope(hq, hk, hqo, hko, kt._ptr(positions) if table is not None else None, n, dim,
-                                           DTYPE_CODES[dt], tf, kt._ptr(error), s.ptr), "kt_qk_norm_rope")
+        hko = _heads(k_out, "k_out", dt, dim, dev, n, hk[3])
+    b = _buffer
+    _NORM_CALL.pack_into(b.buf, 0, *tf, *hq, *hk, *hqo, *hko)
+    at = b.at + _TRANSFORM_BYTES
+    _call(dev, stream, "kt_qk_norm_rope", at, at + _HEADS_BYTES if k is not None else None, at + 2 * _HEADS_BYTES,
+          at + 3 * _HEADS_BYTES if k is not None else None, pos, n, dim, DTYPE_CODES[dt], b.at,
+          None if error is None else error.data_ptr())
     return q_out, (k_out if k is not None else None)
 
 
@@ -237,8 +254,11 @@ class PagedKV:
         dense = (self.page_size * self.heads * self.head_dim, self.heads * self.head_dim, self.head_dim)
         strides = [st if size > 1 else d for t in (k_pages, v_pages)
                    for st, size, d in zip(t.stride(), t.shape[:3], dense)]
-        self._desc = PagedKVDesc(k_pages.data_ptr(), v_pages.data_ptr(), *strides, self.num_pages, self.page_size,
-                                 self.heads, self.head_dim, DTYPE_CODES[self.dtype])
+        self._index = k_pages.get_device()
+        self._desc = ctypes.create_string_buffer(struct.pack(
+            PAGED_KV, k_pages.data_ptr(), v_pages.data_ptr(), *strides, self.num_pages, self.page_size, self.heads,
+            self.head_dim, DTYPE_CODES[self.dtype]))
+        self._desc_at = ctypes.addressof(self._desc)
         self._error = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._err = self._error.data_ptr()
         self._workspaces = {}
@@ -251,17 +271,23 @@ class PagedKV:
         return code
 
     def workspace(self) -> torch.Tensor:
-        """A zeroed workspace for `attend`; calls that share one must not overlap."""
-        with kt._on_device(self.device):
+        """A workspace for `attend`; calls that share one must not overlap."""
+        with torch.cuda.device(self.device):
             n = int(kt.lib().kt_paged_attention_workspace_bytes())
-        return torch.zeros(n, dtype=torch.uint8, device=self.device)
+            ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+            ws[:WORKSPACE_ZEROED].zero_()
+        return ws
 
-    def _workspace(self, stream_ptr) -> torch.Tensor:
+    def _workspace(self, stream) -> torch.Tensor:
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self._workspace(None)
         if torch.cuda.is_current_stream_capturing():
-            return self.workspace()   # lives in the graph's memory, zeroed by the graph
-        ws = self._workspaces.get(stream_ptr)
+            return self.workspace()   # lives in the graph's memory, cleared by the graph
+        ptr = torch._C._cuda_getCurrentRawStream(self._index)
+        ws = self._workspaces.get(ptr)
         if ws is None:
-            ws = self._workspaces[stream_ptr] = self.workspace()
+            ws = self._workspaces[ptr] = self.workspace()
         return ws
 
     def append(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, cu_q: torch.Tensor,
@@ -271,21 +297,26 @@ class PagedKV:
         """Write the step's keys k and values v [tokens, heads, head_dim] to their pages, the keys normed (k_weight)
         and rotated (table) on the way; with q [tokens, q heads, head_dim], also return it normed (q_weight) and
         rotated.  One launch.  Tokens past cu_q[B] are left alone; options as qk_norm_rope's."""
-        dt, dev, dim = self.dtype, self.device, self.head_dim
+        dt, dev, dim = self.dtype, self._index, self.head_dim
+        hk = _heads(k, "k", dt, dim, dev, -1, self.heads)
         n = k.shape[0]
-        hk = _heads(k, "k", dt, dim, dev, None, self.heads)
         hv = _heads(v, "v", dt, dim, dev, n, self.heads)
-        hq = None if q is None else _heads(q, "q", dt, dim, dev, n)
-        batch = _batch(block_table, cu_q, seq_lens, n, dev)
-        tf = _transform(table, q_weight, k_weight, eps, style, dt, dim, dev)
-        with _allocating_on(stream, dev) as s:
-            if q is not None and q_out is None:
-                q_out = torch.empty(q.shape, dtype=dt, device=dev)
-            elif q_out is not None:
+        hq, hqo = _NO_HEADS, _NO_HEADS
+        if q is not None:
+            hq = _heads(q, "q", dt, dim, dev, n, -1)
+            if q_out is None:
+                q_out = _output(q, stream)
+            else:
                 _written(q_out, "q_out")
-        hqo = None if q is None else _heads(q_out, "q_out", dt, dim, dev, n, q.shape[1])
-        with kt._on_device(dev):
-            kt._check(kt.lib().kt_kv_append(self._desc, batch, hk, hv, hq, hqo, tf, self._err, s.ptr), "kt_kv_append")
+            hqo = _heads(q_out, "q_out", dt, dim, dev, n, hq[3])
+        tf = _transform(table, q_weight, k_weight, eps, style, dt, dim, dev)
+        b = _buffer
+        _APPEND_CALL.pack_into(b.buf, 0, *tf, *_batch(block_table, cu_q, seq_lens, n, dev), *hk, *hv, *hq, *hqo)
+        at = b.at + _TRANSFORM_BYTES
+        heads = at + _BATCH_BYTES
+        _call(dev, stream, "kt_kv_append", self._desc_at, at, heads, heads + _HEADS_BYTES,
+              heads + 2 * _HEADS_BYTES if q is not None else None, heads + 3 * _HEADS_BYTES if q is not None else None,
+              b.at, self._err)
         return q_out if q is not None else None
 
     def attend(self, q: torch.Tensor, block_table: torch.Tensor, cu_q: torch.Tensor, seq_lens: torch.Tensor,
@@ -300,24 +331,26 @@ class PagedKV:
 
         A non-finite value row reaches, besides the tokens that see it, others of the sequence that share a tile with
         those; rows past a sequence's keys reach nothing."""
-        dt, dev, dim = self.dtype, self.device, self.head_dim
-        hq = _heads(q, "q", dt, dim, dev)
-        n, heads = q.shape[:2]
+        dt, dev, dim = self.dtype, self._index, self.head_dim
+        hq = _heads(q, "q", dt, dim, dev, -1, -1)
+        n, heads = q.shape[0], hq[3]
         batch = _batch(block_table, cu_q, seq_lens, n, dev)
-        if sinks is not None and (sinks.dtype is not torch.float32 or sinks.shape != (heads,) or sinks.device != dev
-                                  or not sinks.is_contiguous()):
-            raise ValueError(f"sinks must be contiguous float32 [{heads}] on {dev}")
-        with _allocating_on(stream, dev) as s:
-            if out is None:
-                out = torch.empty(q.shape, dtype=dt, device=dev)
-            else:
-                _written(out, "out")
-            if workspace is None:
-                workspace = self._workspace(s.ptr)
-        ho = _heads(out, "out", dt, dim, dev, n, heads)
-        with kt._on_device(dev):
-            kt._check(kt.lib().kt_paged_attention(self._desc, batch, hq, ho, int(max_q_len),
-                                                  dim ** -0.5 if scale is None else float(scale), int(window),
-                                                  kt._ptr(sinks), self._err, workspace.data_ptr(), workspace.numel(),
-                                                  s.ptr), "kt_paged_attention")
+        sink = None
+        if sinks is not None:
+            if (sinks.dtype is not torch.float32 or sinks.shape != (heads,) or sinks.get_device() != dev
+                    or not sinks.is_contiguous()):
+                raise ValueError(f"sinks must be contiguous float32 [{heads}] on {self.device}")
+            sink = sinks.data_ptr()
+        if out is None:
+            out = _output(q, stream)
+        else:
+            _written(out, "out")
+        if workspace is None:
+            workspace = self._workspace(stream)
+        b = _buffer
+        _ATTEND_CALL.pack_into(b.buf, 0, *batch, *hq, *_heads(out, "out", dt, dim, dev, n, heads))
+        at = b.at + _BATCH_BYTES
+        _call(dev, stream, "kt_paged_attention", self._desc_at, b.at, at, at + _HEADS_BYTES, int(max_q_len),
+              dim ** -0.5 if scale is None else float(scale), int(window), sink, self._err, workspace.data_ptr(),
+              workspace.numel())
         return out

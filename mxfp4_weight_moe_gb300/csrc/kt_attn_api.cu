@@ -230,7 +230,7 @@ kt_status kt_kv_append(const kt_paged_kv* cache, const kt_paged_batch* batch, co
 
 size_t kt_paged_attention_workspace_bytes(void) {
     const size_t a = attn_split_workspace_bytes(), b = attn_tile_workspace_bytes();
-    return a + b;
+    return KT_PAGED_ATTENTION_ZEROED + (a > b ? a : b);
 }
 
 kt_status kt_paged_attention(const kt_paged_kv* cache, const kt_paged_batch* batch, const kt_heads* q,
@@ -259,13 +259,13 @@ kt_status kt_paged_attention(const kt_paged_kv* cache, const kt_paged_batch* bat
     if (ws_bytes < kt_paged_attention_workspace_bytes())
         return refuse(KT_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes,
                       kt_paged_attention_workspace_bytes());
-    AttnArgs a{*cache, *batch, *q, *out, scale, window, sinks, err, static_cast<uint8_t*>(ws)};
+    AttnArgs a{*cache, *batch, *q, *out, scale, window, sinks, err, static_cast<unsigned*>(ws),
+               static_cast<uint8_t*>(ws) + KT_PAGED_ATTENTION_ZEROED};
     // The split kernel's tiles hold 16 query rows: it reads the keys once for chunks of up to so many.  The tile
     // kernel loads its queries by TMA, which needs strides.
     const long long rows = static_cast<long long>(max_q_len) * (q->heads / cache->heads);
     if (rows <= 16 || q->token_stride == 0 || q->head_stride == 0)
         return launch_attn_split(a, static_cast<cudaStream_t>(stream));
-    a.ws += attn_split_workspace_bytes();
     return launch_attn_tile(a, static_cast<cudaStream_t>(stream));
 }
 

@@ -49,8 +49,10 @@ struct AttnArgs {
     int window;
     const float* sinks;
     int* err;
-    uint8_t* ws;
+    unsigned* counters;   // KT_PAGED_ATTENTION_ZEROED bytes
+    uint8_t* ws;          // partial results
 };
+constexpr size_t kAttnMaxCounters = KT_PAGED_ATTENTION_ZEROED / sizeof(unsigned);
 size_t attn_split_workspace_bytes();
 kt_status launch_attn_split(const AttnArgs& a, cudaStream_t s);
 size_t attn_tile_workspace_bytes();

@@ -10,6 +10,8 @@
 // CTA; one that is cut leaves partial sums (maximum, sum, unnormalised output)
 // in the workspace, and the CTA that finishes last joins them in order, so the
 // result does not depend on which one that was.
+#include <algorithm>
+
 #include "kt_attn_dev.cuh"
 
 namespace kt {
@@ -398,11 +400,13 @@ __global__ void __launch_bounds__(kSplitWarps * 32, kSplitCtasPerSm)
     }
 }
 
-static int split_ctas() { return sm_count() * kSplitCtasPerSm; }
+static int split_ctas() {
+    return std::min(sm_count() * kSplitCtasPerSm, static_cast<int>(kAttnMaxCounters));
+}
 
 size_t attn_split_workspace_bytes() {
     const size_t c = static_cast<size_t>(split_ctas());
-    return align_up(align_up(c * sizeof(unsigned), 1024) + c * 2 * kSplitRows * (128 + 2) * sizeof(float), 1024);
+    return c * 2 * kSplitRows * (128 + 2) * sizeof(float);
 }
 
 template <typename T, int DP>
@@ -429,8 +433,8 @@ static kt_status launch_split_typed(const AttnArgs& a, cudaStream_t s) {
     p.o_token = a.out.token_stride;
     p.o_head = a.out.head_stride;
     const size_t c = static_cast<size_t>(split_ctas());
-    p.counters = reinterpret_cast<unsigned*>(a.ws);
-    p.part_o = reinterpret_cast<float*>(a.ws + align_up(c * sizeof(unsigned), 1024));
+    p.counters = a.counters;
+    p.part_o = reinterpret_cast<float*>(a.ws);
     p.part_ml = p.part_o + c * 2 * kSplitRows * 128;
     count_launches(1);
     return cuda_status(launch_chained(attn_split_kernel<T, DP>, dim3(static_cast<unsigned>(c)), dim3(kSplitWarps * 32),

@@ -18,6 +18,8 @@
 // into equal runs; the last CTA of a cut item joins its partial sums in order.
 //
 // Warps: 0-3 softmax of group 0, 4-7 of group 1, 8 issues the MMAs, 9 and 10 the TMA loads.
+#include <algorithm>
+
 #include "kt_attn_dev.cuh"
 
 namespace kt {
@@ -808,9 +810,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
 }
 
+static int tile_ctas() { return std::min(sm_count(), static_cast<int>(kAttnMaxCounters / 2)); }
+
 size_t attn_tile_workspace_bytes() {
-    const size_t c = static_cast<size_t>(sm_count());
-    return align_up(c * 2 * sizeof(unsigned), 1024) + c * 2 * 256 * (128 * sizeof(float) + sizeof(float2));
+    const size_t c = static_cast<size_t>(tile_ctas());
+    return c * 2 * 256 * (128 * sizeof(float) + sizeof(float2));
 }
 
 template <typename T, int DP>
@@ -843,9 +847,9 @@ static kt_status launch_tile_typed(const AttnArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return cuda_status(e);
         attr_set[dev] = true;
     }
-    const size_t c = static_cast<size_t>(sm_count());
-    p.counters = reinterpret_cast<unsigned*>(a.ws);
-    p.part_o = reinterpret_cast<float4*>(a.ws + align_up(c * 2 * sizeof(unsigned), 1024));
+    const size_t c = static_cast<size_t>(tile_ctas());
+    p.counters = a.counters;
+    p.part_o = reinterpret_cast<float4*>(a.ws);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + c * 2 * 256 * 32);
     count_launches(1);
     return cuda_status(launch_chained(attn_tile_kernel<T, DP>, dim3(static_cast<unsigned>(c)), dim3(kTileThreads),
