@@ -16,12 +16,15 @@
 
 namespace kt {
 
+#ifndef KT_MINU
+#define KT_MINU 2
+#endif
 constexpr int kSplitWarps = 4;
 constexpr int kSplitKeys = 16;                          // keys of one warp's block
 constexpr int kSplitUnit = kSplitWarps * kSplitKeys;    // keys of one unit
 constexpr int kSplitRows = 16;
 constexpr int kSplitCtasPerSm = 2;
-constexpr int kSplitMinUnits = 2;                       // least units of a CTA's run
+constexpr int kSplitMinUnits = KT_MINU;                       // least units of a CTA's run
 
 template <int DP>
 struct SplitCfg {
@@ -347,8 +350,9 @@ __global__ void __launch_bounds__(kSplitWarps * 32, kSplitCtasPerSm)
             const int c1 = static_cast<int>((first_unit + it.units - 1) / plan.per);
             const int slot = 2 * static_cast<int>(blockIdx.x) + (uo == 0 ? 1 : 0);
             float* po = p.part_o + (static_cast<size_t>(slot) * kSplitRows + row) * DP + d0;
+            const bool used = (rt * kSplitRows + row) / sh.group < sq.q_len;   // rows of no token are not joined
 #pragma unroll
-            for (int i = 0; i < DP / 8; i += 4)
+            for (int i = 0; i < DP / 8 && used; i += 4)
                 *reinterpret_cast<float4*>(po + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
             if ((tid & 7) == 0) {
                 p.part_ml[(slot * kSplitRows + row) * 2] = mt;
@@ -364,25 +368,37 @@ __global__ void __launch_bounds__(kSplitWarps * 32, kSplitCtasPerSm)
             __syncthreads();
             if (s_last) {
                 __threadfence();
+                // maxima and sums of all pieces into shared memory, then their outputs, several loads under way
+                const int pieces = c1 - c0 + 1;
+                float2* ml = reinterpret_cast<float2*>(merge + kSplitWarps * kSplitRows * DP);   // [pieces][16]
+                for (int i = tid; i < pieces * kSplitRows; i += kSplitWarps * 32) {
+                    const int sl = 2 * (c0 + i / kSplitRows) + (i < kSplitRows ? 1 : 0);
+                    ml[i] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + sl * kSplitRows + i % kSplitRows);
+                }
+                __syncthreads();
                 mt = -INFINITY;
-                for (int c = c0; c <= c1; ++c)
-                    mt = fmaxf(mt, __ldcg(&p.part_ml[((2 * c + (c == c0 ? 1 : 0)) * kSplitRows + row) * 2]));
+                for (int k = 0; k < pieces; ++k) mt = fmaxf(mt, ml[k * kSplitRows + row].x);
                 const float top = mt == -INFINITY ? 0.0f : mt;
                 lt = 0.0f;
 #pragma unroll
                 for (int i = 0; i < DP / 8; ++i) acc[i] = 0.0f;
-                for (int c = c0; c <= c1; ++c) {
-                    const int sl = (2 * c + (c == c0 ? 1 : 0)) * kSplitRows + row;
-                    const float f = ex2(__ldcg(&p.part_ml[sl * 2]) - top);
-                    lt += f * __ldcg(&p.part_ml[sl * 2 + 1]);
-                    const float* src = p.part_o + static_cast<size_t>(sl) * DP + d0;
+                if (used) {
+#pragma unroll 4
+                    for (int k = 0; k < pieces; ++k) {
+                        const float2 e = ml[k * kSplitRows + row];
+                        const float f = ex2(e.x - top);
+                        lt += f * e.y;
+                        const float* src = p.part_o +
+                                           static_cast<size_t>((2 * (c0 + k) + (k == 0 ? 1 : 0)) * kSplitRows + row) * DP +
+                                           d0;
 #pragma unroll
-                    for (int i = 0; i < DP / 8; i += 4) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + i));
-                        acc[i] += f * v.x;
-                        acc[i + 1] += f * v.y;
-                        acc[i + 2] += f * v.z;
-                        acc[i + 3] += f * v.w;
+                        for (int i = 0; i < DP / 8; i += 4) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + i));
+                            acc[i] += f * v.x;
+                            acc[i + 1] += f * v.y;
+                            acc[i + 2] += f * v.z;
+                            acc[i + 3] += f * v.w;
+                        }
                     }
                 }
                 store();

@@ -767,16 +767,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             float inv;
             closing(mt, lt, inv);
 #pragma unroll 1
-            for (int q = 0; q < DP / 32; ++q) {
-                float acc[32];
+            for (int q = 0; q < DP; q += 64) {   // 16 loads under way for each piece
+                float acc[64];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) acc[i] = 0.0f;
+                for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
                 for (int k = c0; k <= c1; ++k) {
                     const size_t sl = 2 * static_cast<size_t>(k) + (k == c0 ? 1 : 0);
                     const float f = ex2((__ldcg(&p.part_ml[sl * 256 + prow]).x - mref) * c);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        const float4 v = __ldcg(&p.part_o[(sl * (DP / 4) + (q * 32 + i) / 4) * 256 + prow]);
+                    for (int i = 0; i < 64; i += 4) {
+                        const float4 v = __ldcg(&p.part_o[(sl * (DP / 4) + (q + i) / 4) * 256 + prow]);
                         acc[i] += f * v.x;
                         acc[i + 1] += f * v.y;
                         acc[i + 2] += f * v.z;
@@ -785,14 +785,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 if (valid) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        if (q * 32 + i >= sh.head_dim) break;
+                    for (int i = 0; i < 64; i += 8) {
+                        if (q + i >= sh.head_dim) break;
                         uint4 v;
                         v.x = pack2<T>(acc[i] * inv, acc[i + 1] * inv);
                         v.y = pack2<T>(acc[i + 2] * inv, acc[i + 3] * inv);
                         v.z = pack2<T>(acc[i + 4] * inv, acc[i + 5] * inv);
                         v.w = pack2<T>(acc[i + 6] * inv, acc[i + 7] * inv);
-                        *reinterpret_cast<uint4*>(dst + q * 32 + i) = v;
+                        *reinterpret_cast<uint4*>(dst + q + i) = v;
                     }
                 }
             }
@@ -835,7 +835,7 @@ static kt_status launch_tile_typed(const AttnArgs& a, cudaStream_t s) {
     const uint32_t qb[3] = {64, static_cast<uint32_t>(p.sh.group), static_cast<uint32_t>(p.tokens_per_group)};
     if (!encode_tiled_map(&qmap, a.kv.dtype == KT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                          a.q.ptr, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+                          a.q.ptr, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
         !encode_kv_map(&kmap, a.kv, false, p.box_slots) || !encode_kv_map(&vmap, a.kv, true, p.box_slots))
         return report(KT_ERR_CUDA, "tensor map encoding failed");
     static bool attr_set[64] = {};
