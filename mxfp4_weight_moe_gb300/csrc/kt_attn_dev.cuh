@@ -82,63 +82,6 @@ __device__ __forceinline__ int checked_page(const AttnShape& s, const int32_t* p
     return -1;
 }
 
-// A CTA's run of the units of all sequences: [begin, begin + per) of `total`,
-// its first unit being unit in_seq of sequence seq.
-struct RunPlan {
-    long long total, per, begin, in_seq;
-    int seq;
-};
-
-// Deals the sequences' units (units_of(b)) in equal contiguous runs of at least
-// min_units.  All THREADS threads of the CTA call it; `shared` is theirs.
-template <int THREADS, typename UnitsOf>
-__device__ __forceinline__ RunPlan plan_run(int seqs, int min_units, UnitsOf units_of, RunPlan* shared) {
-    __shared__ long long s_warp[THREADS / 32];
-    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
-    // totals, then (once the runs' length is known) the sequence that holds this CTA's first unit
-    long long total = 0;
-    long long mine = tid < seqs ? units_of(tid) : 0;
-    const long long first_mine = mine;
-    for (int b0 = THREADS; b0 < seqs; b0 += THREADS) mine += b0 + tid < seqs ? units_of(b0 + tid) : 0;
-    long long sum = mine;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) s_warp[warp] = sum;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) total += s_warp[w];
-    const long long even = (total + gridDim.x - 1) / gridDim.x;
-    const long long per = even > min_units ? even : min_units;
-    const long long begin = per * blockIdx.x;
-    if (tid == 0) *shared = RunPlan{total, per, begin, 0, seqs};
-    long long before = 0;
-    for (int b0 = 0; b0 < seqs && begin < total; b0 += THREADS) {
-        const long long n = b0 == 0 ? first_mine : (b0 + tid < seqs ? units_of(b0 + tid) : 0);
-        long long incl = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += up;
-        }
-        __syncthreads();
-        if (lane == 31) s_warp[warp] = incl;
-        __syncthreads();
-        long long prefix = before;
-#pragma unroll
-        for (int w = 0; w < THREADS / 32; ++w) {
-            if (w < warp) prefix += s_warp[w];
-            before += s_warp[w];
-        }
-        if (begin >= prefix + incl - n && begin < prefix + incl) {
-            shared->seq = b0 + tid;
-            shared->in_seq = begin - (prefix + incl - n);
-        }
-        if (before > begin) break;   // the same for every thread
-    }
-    __syncthreads();
-    return *shared;
-}
-
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
                                             int w) {
     asm volatile(

@@ -16,15 +16,15 @@
 
 namespace kt {
 
-#ifndef KT_MINU
-#define KT_MINU 2
-#endif
 constexpr int kSplitWarps = 4;
+constexpr int kSplitThreads = kSplitWarps * 32;
 constexpr int kSplitKeys = 16;                          // keys of one warp's block
 constexpr int kSplitUnit = kSplitWarps * kSplitKeys;    // keys of one unit
 constexpr int kSplitRows = 16;
 constexpr int kSplitCtasPerSm = 2;
-constexpr int kSplitMinUnits = KT_MINU;                       // least units of a CTA's run
+constexpr int kSplitMinUnits = 2;                       // least units of a piece
+constexpr int kSplitItemUnits = 3;                      // what an item costs besides its units, in units
+constexpr int kSplitJoinUnits = 4;                      // what cutting an item costs its last CTA, in units
 
 template <int DP>
 struct SplitCfg {
@@ -32,6 +32,9 @@ struct SplitCfg {
     static constexpr int kStages = DP == 128 ? 3 : 6;
     static constexpr int kRing = kStages * 2 * kBlockBytes;          // per warp
     static constexpr int kSmem = kSplitWarps * kRing + 1024;
+    static constexpr int kMergeRow = DP + 8;                         // floats of a row, so that rows start 8 banks apart
+    static constexpr int kMergeBytes = kSplitWarps * kSplitRows * kMergeRow * 4;
+    static constexpr int kParts = kSplitRows * DP / 4 / kSplitThreads;   // float4 per thread of 16 rows
 };
 
 struct SplitParams {
@@ -39,8 +42,8 @@ struct SplitParams {
     const void* q;
     void* out;
     long long q_token, q_head, o_token, o_head;
-    float* part_o;       // [CTAs][2][16][DP]
-    float* part_ml;      // [CTAs][2][16][2]
+    float4* part_o;      // [CTAs][2][16][DP / 4]
+    float2* part_ml;     // [CTAs][2][16]
     unsigned* counters;  // [CTAs]
 };
 
@@ -53,7 +56,7 @@ __device__ __forceinline__ SplitItem split_item(const AttnShape& s, const SeqInf
     const int t0 = rt * kSplitRows / s.group;
     const int t1 = min((rt * kSplitRows + kSplitRows - 1) / s.group, q.q_len - 1);
     it.hi = max(0, min(q.first_pos + t1 + 1, q.keys));
-    it.lo = s.window > 0 ? max(0, q.first_pos + t0 - s.window + 1) : 0;
+    it.lo = window_start(q.first_pos + t0, s.window);
     if (it.lo >= it.hi) it.lo = it.hi = 0;
     it.unit0 = it.lo / kSplitUnit;
     it.units = max(1, (it.hi + kSplitUnit - 1) / kSplitUnit - it.unit0);
@@ -62,29 +65,127 @@ __device__ __forceinline__ SplitItem split_item(const AttnShape& s, const SeqInf
 __device__ __forceinline__ int split_row_tiles(const AttnShape& s, const SeqInfo& q) {
     return (q.q_len * s.group + kSplitRows - 1) / kSplitRows;
 }
-__device__ __forceinline__ long long split_seq_units(const AttnShape& s, int b) {
+
+// How the items are dealt to the CTAs.  Few items: each is cut into pieces of at most `piece` units, a CTA takes one
+// piece (piece > 0).  Many: they lie on a line, kSplitItemUnits before each one's units, that is cut into equal runs
+// (piece == 0).  In both, [begin, begin + per) of `total` are this CTA's, in pieces or in units of the line.
+struct SplitPlan {
+    long long total, per, begin;
+    long long in_seq;   // begin's place in sequence seq
+    int piece, seq;
+};
+__device__ __forceinline__ int pieces_of(int units, int piece) { return (units + piece - 1) / piece; }
+__device__ __forceinline__ int item_measure(const SplitItem& it, int piece) {
+    return piece > 0 ? pieces_of(it.units, piece) : it.units + kSplitItemUnits;
+}
+__device__ __forceinline__ long long seq_measure(const AttnShape& s, int b, int piece) {
     const SeqInfo q = seq_info(s, b);
     const int tiles = split_row_tiles(s, q);
     long long n = 0;
-    for (int rt = 0; rt < tiles; ++rt) n += split_item(s, q, rt).units;
+    for (int rt = 0; rt < tiles; ++rt) n += item_measure(split_item(s, q, rt), piece);
     return n * s.kv_heads;
 }
 
+// All threads of the CTA; `shared` is theirs.
+__device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, SplitPlan* shared) {
+    __shared__ long long s_units[kSplitWarps], s_items[kSplitWarps];
+    __shared__ int s_most[kSplitWarps];
+    const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    long long units = 0, items = 0;
+    int most = 0;
+    for (int b = tid; b < s.seqs; b += kSplitThreads) {
+        const SeqInfo q = seq_info(s, b);
+        const int tiles = split_row_tiles(s, q);
+        for (int rt = 0; rt < tiles; ++rt) {
+            const int n = split_item(s, q, rt).units;
+            units += n;
+            most = max(most, n);
+        }
+        items += tiles;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        units += __shfl_xor_sync(0xffffffffu, units, o);
+        items += __shfl_xor_sync(0xffffffffu, items, o);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+        s_units[warp] = units;
+        s_items[warp] = items;
+        s_most[warp] = most;
+    }
+    __syncthreads();
+    units = items = 0;
+#pragma unroll
+    for (int w = 0; w < kSplitWarps; ++w) {
+        units += s_units[w];
+        items += s_items[w];
+        most = max(most, s_most[w]);
+    }
+    units *= s.kv_heads;
+    items *= s.kv_heads;
+    const long long ctas = gridDim.x;
+    const long long line = units + items * kSplitItemUnits;
+    const long long run = (line + ctas - 1) / ctas;
+    int piece = 0;
+    if (items <= ctas) {
+        // sum of ceil(u / piece) <= units / piece + items <= CTAs
+        const long long even = ctas > items ? (units + ctas - items - 1) / (ctas - items) : most;
+        const long long least = even < most ? (even > kSplitMinUnits ? even : kSplitMinUnits) : most;
+        if (least <= run + kSplitJoinUnits) piece = static_cast<int>(least);
+    }
+    SplitPlan plan;
+    plan.piece = piece;
+    plan.per = piece > 0 ? 1 : (run > kSplitItemUnits + kSplitMinUnits ? run : kSplitItemUnits + kSplitMinUnits);
+    plan.begin = plan.per * blockIdx.x;
+    // the sequence of this CTA's first piece or unit
+    if (tid == 0) shared->seq = s.seqs;
+    long long before = 0;
+    for (int b0 = 0; b0 < s.seqs; b0 += kSplitThreads) {
+        const long long n = b0 + tid < s.seqs ? seq_measure(s, b0 + tid, piece) : 0;
+        long long incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        __syncthreads();
+        if (lane == 31) s_units[warp] = incl;
+        __syncthreads();
+        long long prefix = before;
+#pragma unroll
+        for (int w = 0; w < kSplitWarps; ++w) {
+            if (w < warp) prefix += s_units[w];
+            before += s_units[w];
+        }
+        if (plan.begin >= prefix + incl - n && plan.begin < prefix + incl) {
+            shared->seq = b0 + tid;
+            shared->in_seq = plan.begin - (prefix + incl - n);
+        }
+        if (before > plan.begin) break;   // the same for every thread
+    }
+    __syncthreads();
+    plan.total = piece > 0 ? before : line;   // (pieces: only whether begin lies below it counts)
+    plan.seq = shared->seq;
+    plan.in_seq = shared->in_seq;
+    return plan;
+}
+
 template <typename T, int DP>
-__global__ void __launch_bounds__(kSplitWarps * 32, kSplitCtasPerSm)
+__global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     attn_split_kernel(const SplitParams p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
     using Cfg = SplitCfg<DP>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[kSplitWarps][Cfg::kStages];
     __shared__ int s_abort, s_last;
-    __shared__ float s_ml[kSplitWarps][kSplitRows][2];
-    __shared__ RunPlan s_plan;
+    __shared__ float2 s_ml[kSplitWarps][kSplitRows];
+    __shared__ SplitPlan s_plan;
     const AttnShape& sh = p.sh;
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     uint8_t* ring_base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* ring = ring_base + warp * Cfg::kRing;
-    float* merge = reinterpret_cast<float*>(ring_base);   // [warps][16][DP], once every warp has left its ring
+    float* merge = reinterpret_cast<float*>(ring_base);   // [warps][16][kMergeRow], once every warp has left its ring
 
     if (tid == 0) {
         s_abort = 0;
@@ -96,40 +197,44 @@ __global__ void __launch_bounds__(kSplitWarps * 32, kSplitCtasPerSm)
     }
     griddep_wait();
     griddep_launch_dependents();
-    const RunPlan plan = plan_run<kSplitWarps * 32>(
-        sh.seqs, kSplitMinUnits, [&](int b) { return split_seq_units(sh, b); }, &s_plan);
-    long long left = min(plan.per, plan.total - plan.begin);
-    if (left <= 0) return;
+    const SplitPlan plan = split_plan(sh, &s_plan);
+    if (plan.seq >= sh.seqs) return;
 
-    int b = plan.seq;
-    long long at = plan.in_seq;              // unit inside the sequence
-    long long global = plan.begin;
-    uint32_t loads = 0;                      // blocks this warp has consumed so far
-    while (left > 0 && b < sh.seqs) {
-        const SeqInfo sq = seq_info(sh, b);
-        const int tiles = split_row_tiles(sh, sq);
-        // item of unit `at`: row tiles in order, each with its cache heads side by side
-        int rt = 0;
-        SplitItem it{};
-        for (; rt < tiles; ++rt) {
-            it = split_item(sh, sq, rt);
-            const long long n = static_cast<long long>(it.units) * sh.kv_heads;
-            if (at < n) break;
-            at -= n;
+    // ---- the item of this CTA's first piece or unit
+    int b = plan.seq, rt = 0;
+    SeqInfo sq = seq_info(sh, b);
+    int row_tiles = split_row_tiles(sh, sq);
+    SplitItem it = split_item(sh, sq, 0);
+    long long at = plan.in_seq;
+    while (at >= static_cast<long long>(item_measure(it, plan.piece)) * sh.kv_heads) {
+        at -= static_cast<long long>(item_measure(it, plan.piece)) * sh.kv_heads;
+        it = split_item(sh, sq, ++rt);
+    }
+    int h, u0, u1;                 // cache head; the item's units in this run
+    long long first = 0;           // line: the item's first unit
+    const long long end = plan.begin + plan.per;
+    {
+        const int n = item_measure(it, plan.piece);
+        h = at >> 31 == 0 ? static_cast<int>(at) / n : static_cast<int>(at / n);
+        const int in = static_cast<int>(at - static_cast<long long>(h) * n);
+        if (plan.piece > 0) {
+            const int chunk = (it.units + n - 1) / n;   // the pieces of an item alike
+            u0 = in * chunk;
+            u1 = min(it.units, u0 + chunk);
+        } else {
+            first = plan.begin - in + kSplitItemUnits;
+            u0 = max(in - kSplitItemUnits, 0);
+            u1 = static_cast<int>(min(end - first, static_cast<long long>(it.units)));
         }
-        if (rt == tiles) {
-            ++b;
-            at = 0;
-            continue;
-        }
-        const int h = static_cast<int>(at / it.units);
-        const int uo = static_cast<int>(at - static_cast<long long>(h) * it.units);
-        const int take = static_cast<int>(min(static_cast<long long>(it.units - uo), left));
+    }
+    uint32_t loads = 0;            // blocks this warp has consumed so far
+    while (true) {
+        if (u1 > u0) {
         const int32_t* pages = sh.block_table + b * sh.table_stride;
 
         // ---- this warp's blocks: keys base + 64 i, i in [i0, i1)
-        const int base = (it.unit0 + uo) * kSplitUnit + warp * kSplitKeys;
-        int i0 = 0, i1 = take;
+        const int base = (it.unit0 + u0) * kSplitUnit + warp * kSplitKeys;
+        int i0 = 0, i1 = u1 - u0;
         while (i0 < i1 && base + i0 * kSplitUnit + kSplitKeys <= it.lo) ++i0;
         while (i1 > i0 && base + (i1 - 1) * kSplitUnit >= it.hi) --i1;
         int page_batch = -1, my_page = -1;
@@ -203,15 +308,20 @@ __global__ void __launch_bounds__(kSplitWarps * 32, kSplitCtasPerSm)
             const int key0 = base + i * kSplitUnit;
 
             // ---- S = Q K^T, 16 rows x 16 keys
-            float s0[4] = {0, 0, 0, 0}, s1[4] = {0, 0, 0, 0};
+            float s0[4] = {0, 0, 0, 0}, s1[4] = {0, 0, 0, 0}, r0[4] = {0, 0, 0, 0}, r1[4] = {0, 0, 0, 0};
             const int krow = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
             for (int ks = 0; ks < DP / 16; ++ks) {
                 uint32_t kf[4];
                 const int chunk = (ks & 3) * 2 + ((lane >> 3) & 1);
                 ldmatrix_x4(kf, kb + (ks >> 2) * 2048 + krow * 128 + ((chunk ^ (krow & 7)) << 4));
-                mma_16816<T>(s0, qa[ks], kf[0], kf[1]);
-                mma_16816<T>(s1, qa[ks], kf[2], kf[3]);
+                mma_16816<T>(ks & 1 ? r0 : s0, qa[ks], kf[0], kf[1]);   // two chains each, for their latency
+                mma_16816<T>(ks & 1 ? r1 : s1, qa[ks], kf[2], kf[3]);
+            }
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                s0[f] += r0[f];
+                s1[f] += r1[f];
             }
             // ---- scale, mask, running maximum (base-2 exponents)
             float x[2][4];
@@ -276,143 +386,164 @@ __global__ void __launch_bounds__(kSplitWarps * 32, kSplitCtasPerSm)
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
         }
 
-        // ---- join the warps
+        // ---- join the warps: a thread takes the float4 tid, tid + 128, .. of the tile's rows that hold tokens
+        const int rows = min(kSplitRows, sq.q_len * sh.group - rt * kSplitRows);
         __syncthreads();
         {
-            float* mo = merge + warp * kSplitRows * DP;
+            float* mo = merge + warp * kSplitRows * Cfg::kMergeRow;
 #pragma unroll
-            for (int n = 0; n < DP / 8; ++n)
+            for (int e = 0; e < 2; ++e) {
+                if (8 * e >= rows) break;
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    *reinterpret_cast<float2*>(mo + (g + 8 * e) * DP + n * 8 + t4 * 2) =
+                for (int n = 0; n < DP / 8; ++n)
+                    *reinterpret_cast<float2*>(mo + (g + 8 * e) * Cfg::kMergeRow + n * 8 + t4 * 2) =
                         make_float2(o[n][2 * e], o[n][2 * e + 1]);
-            if (t4 == 0) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    s_ml[warp][g + 8 * e][0] = m[e];
-                    s_ml[warp][g + 8 * e][1] = l[e];
-                }
+                if (t4 == 0) s_ml[warp][g + 8 * e] = make_float2(m[e], l[e]);
             }
         }
         __syncthreads();
-        const bool whole = uo == 0 && take == it.units;
-        const int row = tid >> 3, d0 = (tid & 7) * (DP / 8);
-        float mt = -INFINITY, lt = 0.0f, acc[DP / 8];
+        float4 acc[Cfg::kParts];
+        float2 ml[Cfg::kParts];
+        auto part_row = [&](int k) { return (tid + k * kSplitThreads) / (DP / 4); };
+        const int d = (tid % (DP / 4)) * 4;   // kSplitThreads is a multiple of DP / 4
 #pragma unroll
-        for (int i = 0; i < DP / 8; ++i) acc[i] = 0.0f;
+        for (int k = 0; k < Cfg::kParts; ++k) {
+            const int row = part_row(k);
+            if (row >= rows) break;
+            float top = s_ml[0][row].x;
 #pragma unroll
-        for (int w = 0; w < kSplitWarps; ++w) mt = fmaxf(mt, s_ml[w][row][0]);
-        const float mb = mt == -INFINITY ? 0.0f : mt;
+            for (int w = 1; w < kSplitWarps; ++w) top = fmaxf(top, s_ml[w][row].x);
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f;
+            float4 a = make_float4(0, 0, 0, 0);
 #pragma unroll
-        for (int w = 0; w < kSplitWarps; ++w) {
-            const float f = ex2(s_ml[w][row][0] - mb);
-            lt += f * s_ml[w][row][1];
-            const float* mo = merge + (w * kSplitRows + row) * DP + d0;
-#pragma unroll
-            for (int i = 0; i < DP / 8; ++i) acc[i] += f * mo[i];
+            for (int w = 0; w < kSplitWarps; ++w) {
+                const float2 e = s_ml[w][row];
+                const float f = ex2(e.x - ref);
+                const float4 v =
+                    *reinterpret_cast<const float4*>(merge + (w * kSplitRows + row) * Cfg::kMergeRow + d);
+                sum += f * e.y;
+                a.x += f * v.x;
+                a.y += f * v.y;
+                a.z += f * v.z;
+                a.w += f * v.w;
+            }
+            acc[k] = a;
+            ml[k] = make_float2(top, sum);
         }
-
-        auto store = [&]() {   // acc, mt, lt -> the output row
+        auto store = [&](int row, float4 a, float2 e) {
             const int r = rt * kSplitRows + row;
             const int tok = r / sh.group;
-            if (tok >= sq.q_len) return;
             const int head = h * sh.group + r - tok * sh.group;
+            if (d >= sh.head_dim) return;
+            float f = 1.0f;
             if (sh.sinks != nullptr) {
                 const float sk = sh.sinks[head] * kLog2e;
-                const float top = fmaxf(mt, sk);
-                const float tb = top == -INFINITY ? 0.0f : top;
-                const float f = ex2(mt - tb);
-                lt = lt * f + ex2(sk - tb);
-#pragma unroll
-                for (int i = 0; i < DP / 8; ++i) acc[i] *= f;
+                const float top = fmaxf(e.x, sk);
+                const float ref = top == -INFINITY ? 0.0f : top;
+                f = ex2(e.x - ref);
+                e.y = e.y * f + ex2(sk - ref);
             }
-            const float inv = lt == 0.0f ? 0.0f : 1.0f / lt;
+            f = e.y == 0.0f ? 0.0f : f / e.y;
             T* dst = static_cast<T*>(p.out) + static_cast<long long>(sq.first_token + tok) * p.o_token +
-                     static_cast<long long>(head) * p.o_head;
-#pragma unroll
-            for (int i = 0; i < DP / 8; i += 8) {
-                if (d0 + i >= sh.head_dim) break;
-                uint4 v;
-                v.x = pack2<T>(acc[i] * inv, acc[i + 1] * inv);
-                v.y = pack2<T>(acc[i + 2] * inv, acc[i + 3] * inv);
-                v.z = pack2<T>(acc[i + 4] * inv, acc[i + 5] * inv);
-                v.w = pack2<T>(acc[i + 6] * inv, acc[i + 7] * inv);
-                *reinterpret_cast<uint4*>(dst + d0 + i) = v;
-            }
+                     static_cast<long long>(head) * p.o_head + d;
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(a.x * f, a.y * f), pack2<T>(a.z * f, a.w * f));
         };
 
-        if (whole) {
-            store();
-        } else {
-            // pieces of the item: the CTA where it begins (its slot 1), then the following ones (slot 0)
-            const long long first_unit = global - uo;
-            const int c0 = static_cast<int>(first_unit / plan.per);
-            const int c1 = static_cast<int>((first_unit + it.units - 1) / plan.per);
-            const int slot = 2 * static_cast<int>(blockIdx.x) + (uo == 0 ? 1 : 0);
-            float* po = p.part_o + (static_cast<size_t>(slot) * kSplitRows + row) * DP + d0;
-            const bool used = (rt * kSplitRows + row) / sh.group < sq.q_len;   // rows of no token are not joined
+        if (u0 == 0 && u1 == it.units) {
 #pragma unroll
-            for (int i = 0; i < DP / 8 && used; i += 4)
-                *reinterpret_cast<float4*>(po + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-            if ((tid & 7) == 0) {
-                p.part_ml[(slot * kSplitRows + row) * 2] = mt;
-                p.part_ml[(slot * kSplitRows + row) * 2 + 1] = lt;
+            for (int k = 0; k < Cfg::kParts; ++k)
+                if (part_row(k) < rows) store(part_row(k), acc[k], ml[k]);
+        } else {
+            // The item's pieces lie with CTAs c0 .. c0 + n - 1.  On the line, the first is its CTA's last piece (slot
+            // 1), the others their CTAs' first (slot 0).
+            int c0, n;
+            if (plan.piece > 0) {
+                n = pieces_of(it.units, plan.piece);
+                c0 = static_cast<int>(blockIdx.x) - u0 / ((it.units + n - 1) / n);
+            } else {
+                c0 = static_cast<int>(first / plan.per);
+                n = static_cast<int>((first + it.units - 1) / plan.per) - c0 + 1;
             }
-            __threadfence();
+            const int slot = 2 * static_cast<int>(blockIdx.x) + (u0 == 0 ? 1 : 0);
+#pragma unroll
+            for (int k = 0; k < Cfg::kParts; ++k) {
+                const int row = part_row(k);
+                if (row >= rows) break;
+                p.part_o[(slot * kSplitRows + row) * (DP / 4) + d / 4] = acc[k];
+                if (d == 0) p.part_ml[slot * kSplitRows + row] = ml[k];
+            }
             __syncthreads();
             if (tid == 0) {
+                __threadfence();
                 const unsigned seen = atomicAdd(&p.counters[c0], 1u);
-                s_last = seen == static_cast<unsigned>(c1 - c0);
+                s_last = seen == static_cast<unsigned>(n - 1);
                 if (s_last) p.counters[c0] = 0;
+                __threadfence();
             }
             __syncthreads();
             if (s_last) {
-                __threadfence();
                 // maxima and sums of all pieces into shared memory, then their outputs, several loads under way
-                const int pieces = c1 - c0 + 1;
-                float2* ml = reinterpret_cast<float2*>(merge + kSplitWarps * kSplitRows * DP);   // [pieces][16]
-                for (int i = tid; i < pieces * kSplitRows; i += kSplitWarps * 32) {
-                    const int sl = 2 * (c0 + i / kSplitRows) + (i < kSplitRows ? 1 : 0);
-                    ml[i] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + sl * kSplitRows + i % kSplitRows);
-                }
+                float2* all = reinterpret_cast<float2*>(ring_base + Cfg::kMergeBytes);   // [pieces][16]
+                auto slot_of = [&](int c) { return 2 * (c0 + c) + (c == 0 ? 1 : 0); };
+                for (int i = tid; i < n * kSplitRows; i += kSplitThreads)
+                    all[i] = __ldcg(&p.part_ml[slot_of(i / kSplitRows) * kSplitRows + i % kSplitRows]);
                 __syncthreads();
-                mt = -INFINITY;
-                for (int k = 0; k < pieces; ++k) mt = fmaxf(mt, ml[k * kSplitRows + row].x);
-                const float top = mt == -INFINITY ? 0.0f : mt;
-                lt = 0.0f;
+                float ref[Cfg::kParts];
 #pragma unroll
-                for (int i = 0; i < DP / 8; ++i) acc[i] = 0.0f;
-                if (used) {
+                for (int k = 0; k < Cfg::kParts; ++k) {
+                    const int row = part_row(k);
+                    if (row >= rows) break;
+                    float top = -INFINITY;
+                    for (int c = 0; c < n; ++c) top = fmaxf(top, all[c * kSplitRows + row].x);
+                    ref[k] = top == -INFINITY ? 0.0f : top;
+                    ml[k] = make_float2(top, 0.0f);
+                    acc[k] = make_float4(0, 0, 0, 0);
+                }
 #pragma unroll 4
-                    for (int k = 0; k < pieces; ++k) {
-                        const float2 e = ml[k * kSplitRows + row];
-                        const float f = ex2(e.x - top);
-                        lt += f * e.y;
-                        const float* src = p.part_o +
-                                           static_cast<size_t>((2 * (c0 + k) + (k == 0 ? 1 : 0)) * kSplitRows + row) * DP +
-                                           d0;
+                for (int c = 0; c < n; ++c) {
 #pragma unroll
-                        for (int i = 0; i < DP / 8; i += 4) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(src + i));
-                            acc[i] += f * v.x;
-                            acc[i + 1] += f * v.y;
-                            acc[i + 2] += f * v.z;
-                            acc[i + 3] += f * v.w;
-                        }
+                    for (int k = 0; k < Cfg::kParts; ++k) {
+                        const int row = part_row(k);
+                        if (row >= rows) break;
+                        const float2 e = all[c * kSplitRows + row];
+                        const float4 v = __ldcg(&p.part_o[(slot_of(c) * kSplitRows + row) * (DP / 4) + d / 4]);
+                        const float f = ex2(e.x - ref[k]);
+                        ml[k].y += f * e.y;
+                        acc[k].x += f * v.x;
+                        acc[k].y += f * v.y;
+                        acc[k].z += f * v.z;
+                        acc[k].w += f * v.w;
                     }
                 }
-                store();
+#pragma unroll
+                for (int k = 0; k < Cfg::kParts; ++k)
+                    if (part_row(k) < rows) store(part_row(k), acc[k], ml[k]);
             }
         }
+        }   // of an item with units in the run
+
+        // ---- the run's next item
+        if (plan.piece > 0) break;
+        first += it.units + kSplitItemUnits;
+        if (first >= end) break;
+        if (++h == sh.kv_heads) {
+            h = 0;
+            if (++rt == row_tiles) {
+                rt = 0;
+                do {
+                    if (++b >= sh.seqs) return;
+                    sq = seq_info(sh, b);
+                    row_tiles = split_row_tiles(sh, sq);
+                } while (row_tiles == 0);
+            }
+            it = split_item(sh, sq, rt);
+        }
+        u0 = 0;
+        u1 = static_cast<int>(min(end - first, static_cast<long long>(it.units)));
         // generic reads and writes of the merge area come before the next item's loads into it
         fence_proxy_async_smem();
         __syncthreads();
-
-        // ---- next unit of the run
-        at = static_cast<long long>(h) * it.units + uo + take;
-        for (int r = 0; r < rt; ++r) at += static_cast<long long>(split_item(sh, sq, r).units) * sh.kv_heads;
-        left -= take;
-        global += take;
     }
 }
 
@@ -450,10 +581,10 @@ static kt_status launch_split_typed(const AttnArgs& a, cudaStream_t s) {
     p.o_head = a.out.head_stride;
     const size_t c = static_cast<size_t>(split_ctas());
     p.counters = a.counters;
-    p.part_o = reinterpret_cast<float*>(a.ws);
-    p.part_ml = p.part_o + c * 2 * kSplitRows * 128;
+    p.part_o = reinterpret_cast<float4*>(a.ws);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + c * 2 * kSplitRows * 32);
     count_launches(1);
-    return cuda_status(launch_chained(attn_split_kernel<T, DP>, dim3(static_cast<unsigned>(c)), dim3(kSplitWarps * 32),
+    return cuda_status(launch_chained(attn_split_kernel<T, DP>, dim3(static_cast<unsigned>(c)), dim3(kSplitThreads),
                                       Cfg::kSmem, s, static_cast<const SplitParams&>(p),
                                       static_cast<const CUtensorMap&>(kmap), static_cast<const CUtensorMap&>(vmap)));
 }

@@ -71,6 +71,12 @@ __device__ __forceinline__ TileItem tile_item(const AttnShape& s, const SeqInfo&
 // Units of item rt on the line: its key tiles, and the tiles' worth of time that any item takes besides.
 __device__ __forceinline__ int item_units(const TileItem& it) { return it.tiles + kItemUnits; }
 
+// A CTA's run of the line: [begin, begin + per) of `total` units, its first unit being unit in_seq of sequence seq.
+struct RunPlan {
+    long long total, per, begin, in_seq;
+    int seq;
+};
+
 // Walks a CTA's run [begin, end) of units item by item; every role of the CTA walks it for itself.
 struct TileWalk {
     int b, rt, row_tiles, h;
@@ -145,7 +151,7 @@ struct TileWalk {
     __device__ __forceinline__ int groups(int tpg) const { return sq.q_len - rt * 2 * tpg > tpg ? 2 : 1; }
 };
 
-// plan_run with a warp per sequence (a long chunk has many items, whose units are summed by the warp's lanes).
+// Deals all sequences' units in equal runs.  A warp sums a sequence: a long chunk has many items.
 __device__ __forceinline__ RunPlan plan_tiles(const AttnShape& s, int tpi, unsigned* costs, RunPlan* shared) {
     constexpr int kWarps = kTileThreads / 32;
     __shared__ long long s_sum[kWarps];
