@@ -11,6 +11,7 @@
 // in the workspace, and the CTA that finishes last joins them in order, so the
 // result does not depend on which one that was.
 #include <algorithm>
+#include <type_traits>
 
 #include "kt_attn_dev.cuh"
 
@@ -18,8 +19,7 @@ namespace kt {
 
 constexpr int kSplitWarps = 4;
 constexpr int kSplitThreads = kSplitWarps * 32;
-constexpr int kSplitKeys = 16;                          // keys of one warp's block
-constexpr int kSplitUnit = kSplitWarps * kSplitKeys;    // keys of one unit
+constexpr int kSplitKeys = 16;                          // keys of one load (pages hold a multiple of it)
 constexpr int kSplitRows = 16;
 constexpr int kSplitCtasPerSm = 2;
 constexpr int kSplitMinUnits = 2;                       // least units of a piece
@@ -28,8 +28,11 @@ constexpr int kSplitJoinUnits = 4;                      // what cutting an item 
 
 template <int DP>
 struct SplitCfg {
-    static constexpr int kBlockBytes = kSplitKeys * DP * 2;          // one of K, V
-    static constexpr int kStages = DP == 128 ? 3 : 6;
+    static constexpr int kSub = DP == 128 ? 1 : 2;                   // loads of K and of V that make a warp's block
+    static constexpr int kBlockKeys = kSub * kSplitKeys;
+    static constexpr int kUnit = kSplitWarps * kBlockKeys;           // keys of one unit
+    static constexpr int kBlockBytes = kBlockKeys * DP * 2;          // one of K, V
+    static constexpr int kStages = 3;
     static constexpr int kRing = kStages * 2 * kBlockBytes;          // per warp
     static constexpr int kSmem = kSplitWarps * kRing + 1024;
     static constexpr int kMergeRow = DP + 8;                         // floats of a row, so that rows start 8 banks apart
@@ -51,15 +54,15 @@ struct SplitParams {
 struct SplitItem {
     int lo, hi, unit0, units;
 };
-__device__ __forceinline__ SplitItem split_item(const AttnShape& s, const SeqInfo& q, int rt) {
+__device__ __forceinline__ SplitItem split_item(const AttnShape& s, const SeqInfo& q, int rt, int unit) {
     SplitItem it;
     const int t0 = rt * kSplitRows / s.group;
     const int t1 = min((rt * kSplitRows + kSplitRows - 1) / s.group, q.q_len - 1);
     it.hi = max(0, min(q.first_pos + t1 + 1, q.keys));
     it.lo = window_start(q.first_pos + t0, s.window);
     if (it.lo >= it.hi) it.lo = it.hi = 0;
-    it.unit0 = it.lo / kSplitUnit;
-    it.units = max(1, (it.hi + kSplitUnit - 1) / kSplitUnit - it.unit0);
+    it.unit0 = it.lo / unit;
+    it.units = max(1, (it.hi + unit - 1) / unit - it.unit0);
     return it;
 }
 __device__ __forceinline__ int split_row_tiles(const AttnShape& s, const SeqInfo& q) {
@@ -78,16 +81,16 @@ __device__ __forceinline__ int pieces_of(int units, int piece) { return (units +
 __device__ __forceinline__ int item_measure(const SplitItem& it, int piece) {
     return piece > 0 ? pieces_of(it.units, piece) : it.units + kSplitItemUnits;
 }
-__device__ __forceinline__ long long seq_measure(const AttnShape& s, int b, int piece) {
+__device__ __forceinline__ long long seq_measure(const AttnShape& s, int b, int piece, int unit) {
     const SeqInfo q = seq_info(s, b);
     const int tiles = split_row_tiles(s, q);
     long long n = 0;
-    for (int rt = 0; rt < tiles; ++rt) n += item_measure(split_item(s, q, rt), piece);
+    for (int rt = 0; rt < tiles; ++rt) n += item_measure(split_item(s, q, rt, unit), piece);
     return n * s.kv_heads;
 }
 
 // All threads of the CTA; `shared` is theirs.
-__device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, SplitPlan* shared) {
+__device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, int unit, SplitPlan* shared) {
     __shared__ long long s_units[kSplitWarps], s_items[kSplitWarps];
     __shared__ int s_most[kSplitWarps];
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
@@ -97,7 +100,7 @@ __device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, SplitPlan* s
         const SeqInfo q = seq_info(s, b);
         const int tiles = split_row_tiles(s, q);
         for (int rt = 0; rt < tiles; ++rt) {
-            const int n = split_item(s, q, rt).units;
+            const int n = split_item(s, q, rt, unit).units;
             units += n;
             most = max(most, n);
         }
@@ -142,7 +145,7 @@ __device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, SplitPlan* s
     if (tid == 0) shared->seq = s.seqs;
     long long before = 0;
     for (int b0 = 0; b0 < s.seqs; b0 += kSplitThreads) {
-        const long long n = b0 + tid < s.seqs ? seq_measure(s, b0 + tid, piece) : 0;
+        const long long n = b0 + tid < s.seqs ? seq_measure(s, b0 + tid, piece, unit) : 0;
         long long incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -197,18 +200,18 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     }
     griddep_wait();
     griddep_launch_dependents();
-    const SplitPlan plan = split_plan(sh, &s_plan);
+    const SplitPlan plan = split_plan(sh, Cfg::kUnit, &s_plan);
     if (plan.seq >= sh.seqs) return;
 
     // ---- the item of this CTA's first piece or unit
     int b = plan.seq, rt = 0;
     SeqInfo sq = seq_info(sh, b);
     int row_tiles = split_row_tiles(sh, sq);
-    SplitItem it = split_item(sh, sq, 0);
+    SplitItem it = split_item(sh, sq, 0, Cfg::kUnit);
     long long at = plan.in_seq;
     while (at >= static_cast<long long>(item_measure(it, plan.piece)) * sh.kv_heads) {
         at -= static_cast<long long>(item_measure(it, plan.piece)) * sh.kv_heads;
-        it = split_item(sh, sq, ++rt);
+        it = split_item(sh, sq, ++rt, Cfg::kUnit);
     }
     int h, u0, u1;                 // cache head; the item's units in this run
     long long first = 0;           // line: the item's first unit
@@ -232,30 +235,42 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
         if (u1 > u0) {
         const int32_t* pages = sh.block_table + b * sh.table_stride;
 
-        // ---- this warp's blocks: keys base + 64 i, i in [i0, i1)
-        const int base = (it.unit0 + u0) * kSplitUnit + warp * kSplitKeys;
+        // ---- this warp's blocks: keys base + kUnit i, i in [i0, i1)
+        const int base = (it.unit0 + u0) * Cfg::kUnit + warp * Cfg::kBlockKeys;
         int i0 = 0, i1 = u1 - u0;
-        while (i0 < i1 && base + i0 * kSplitUnit + kSplitKeys <= it.lo) ++i0;
-        while (i1 > i0 && base + (i1 - 1) * kSplitUnit >= it.hi) --i1;
-        int page_batch = -1, my_page = -1;
+        while (i0 < i1 && base + i0 * Cfg::kUnit + Cfg::kBlockKeys <= it.lo) ++i0;
+        while (i1 > i0 && base + (i1 - 1) * Cfg::kUnit >= it.hi) --i1;
+        int page_batch = -1, my_page = -1, my_slot = 0;
         auto issue = [&](int i) {   // whole warp; block i into its stage
-            const int batch = (i - i0) >> 5;
+            // lanes look up the pages of the next 32 loads at a time
+            const int batch = (i - i0) / (32 / Cfg::kSub);
             if (batch != page_batch) {
                 page_batch = batch;
-                const int mine = i0 + batch * 32 + lane;
-                my_page = mine < i1 ? checked_page(sh, pages, base + mine * kSplitUnit) : -1;
+                const int mine = i0 + batch * (32 / Cfg::kSub) + lane / Cfg::kSub;
+                const int key = base + mine * Cfg::kUnit + lane % Cfg::kSub * kSplitKeys;
+                my_page = -1;
+                my_slot = 0;
+                if (mine < i1 && key < it.hi) {   // (past the keys: zeros from outside the cache)
+                    my_page = checked_page(sh, pages, key);
+                    my_slot = key % sh.page_size;
+                }
             }
-            const int page = __shfl_sync(0xffffffffu, my_page, (i - i0) & 31);
-            if (lane == 0) {
-                const uint32_t st = (loads + static_cast<uint32_t>(i - i0)) % Cfg::kStages;
-                const uint32_t bar = smem_u32(&s_full[warp][st]);
-                const int slot = (base + i * kSplitUnit) % sh.page_size;
-                uint8_t* k = ring + st * 2 * Cfg::kBlockBytes;
-                mbar_arrive_expect_tx(bar, 2 * Cfg::kBlockBytes);
+            const uint32_t st = (loads + static_cast<uint32_t>(i - i0)) % Cfg::kStages;
+            const uint32_t bar = smem_u32(&s_full[warp][st]);
+            const uint32_t k = smem_u32(ring + st * 2 * Cfg::kBlockBytes);
+            if (lane == 0) mbar_arrive_expect_tx(bar, 2 * Cfg::kBlockBytes);
 #pragma unroll
-                for (int x = 0; x < DP; x += 64) {
-                    tma_load_4d(smem_u32(k + x * 2 * kSplitKeys), &kmap, bar, x, slot, h, page);
-                    tma_load_4d(smem_u32(k + Cfg::kBlockBytes + x * 2 * kSplitKeys), &vmap, bar, x, slot, h, page);
+            for (int sub = 0; sub < Cfg::kSub; ++sub) {
+                const int src = (i - i0) % (32 / Cfg::kSub) * Cfg::kSub + sub;
+                const int page = __shfl_sync(0xffffffffu, my_page, src);
+                const int slot = __shfl_sync(0xffffffffu, my_slot, src);
+                if (lane == 0) {
+#pragma unroll
+                    for (int x = 0; x < DP; x += 64) {
+                        const uint32_t at_block = (x * Cfg::kBlockKeys + sub * kSplitKeys * 64) * 2;
+                        tma_load_4d(k + at_block, &kmap, bar, x, slot, h, page);
+                        tma_load_4d(k + Cfg::kBlockBytes + at_block, &vmap, bar, x, slot, h, page);
+                    }
                 }
             }
         };
@@ -265,7 +280,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
         // ---- queries: rows g and g + 8 of the tile in the MMA's A layout
         const int g = lane >> 2, t4 = lane & 3;
         uint32_t qa[DP / 16][4];
-        int last_key[2], first_key[2];   // what the row sees; nothing for a row of no token
+        int last_key[2], first_key[2];   // what the row sees; rows of no token need no mask
         {
             const T* qp[2];
 #pragma unroll
@@ -273,8 +288,8 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                 const int row = rt * kSplitRows + g + 8 * e;
                 const int tok = row / sh.group;
                 const bool ok = tok < sq.q_len;
-                last_key[e] = ok ? min(sq.first_pos + tok, sq.keys - 1) : -1;
-                first_key[e] = window_start(sq.first_pos + tok, sh.window);
+                last_key[e] = ok ? min(sq.first_pos + tok, sq.keys - 1) : 0x7fffffff;
+                first_key[e] = ok ? window_start(sq.first_pos + tok, sh.window) : 0;
                 qp[e] = ok ? static_cast<const T*>(p.q) + static_cast<long long>(sq.first_token + tok) * p.q_token +
                                  static_cast<long long>(h * sh.group + row - tok * sh.group) * p.q_head
                            : nullptr;
@@ -305,35 +320,50 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
             }
             const uint32_t kb = smem_u32(ring + st * 2 * Cfg::kBlockBytes);
             const uint32_t vb = kb + Cfg::kBlockBytes;
-            const int key0 = base + i * kSplitUnit;
+            const int key0 = base + i * Cfg::kUnit;
 
-            // ---- S = Q K^T, 16 rows x 16 keys
-            float s0[4] = {0, 0, 0, 0}, s1[4] = {0, 0, 0, 0}, r0[4] = {0, 0, 0, 0}, r1[4] = {0, 0, 0, 0};
+            // ---- S = Q K^T, 16 rows x kBlockKeys keys; two chains per product where there are few products
+            constexpr int kCols = 2 * Cfg::kSub, kChains = Cfg::kSub == 1 ? 2 : 1;
+            float sc[kChains][kCols][4];
+#pragma unroll
+            for (int c = 0; c < kChains * kCols * 4; ++c) sc[c / (kCols * 4)][c / 4 % kCols][c % 4] = 0.0f;
             const int krow = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
-            for (int ks = 0; ks < DP / 16; ++ks) {
-                uint32_t kf[4];
-                const int chunk = (ks & 3) * 2 + ((lane >> 3) & 1);
-                ldmatrix_x4(kf, kb + (ks >> 2) * 2048 + krow * 128 + ((chunk ^ (krow & 7)) << 4));
-                mma_16816<T>(ks & 1 ? r0 : s0, qa[ks], kf[0], kf[1]);   // two chains each, for their latency
-                mma_16816<T>(ks & 1 ? r1 : s1, qa[ks], kf[2], kf[3]);
-            }
+            for (int ks = 0; ks < DP / 16; ++ks)
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                s0[f] += r0[f];
-                s1[f] += r1[f];
-            }
-            // ---- scale, mask, running maximum (base-2 exponents)
-            float x[2][4];
+                for (int sub = 0; sub < Cfg::kSub; ++sub) {
+                    uint32_t kf[4];
+                    const int chunk = (ks & 3) * 2 + ((lane >> 3) & 1);
+                    ldmatrix_x4(kf, kb + (ks >> 2) * (Cfg::kBlockKeys * 128) + sub * 2048 + krow * 128 +
+                                        ((chunk ^ (krow & 7)) << 4));
+                    mma_16816<T>(sc[ks % kChains][2 * sub], qa[ks], kf[0], kf[1]);
+                    mma_16816<T>(sc[ks % kChains][2 * sub + 1], qa[ks], kf[2], kf[3]);
+                }
+            // ---- scale, mask, running maximum (base-2 exponents); x[e]: row g + 8 e, keys k0 + 8 c and the next
+            float x[2][2 * kCols];
             const int k0 = key0 + t4 * 2;
+            const bool masked = __any_sync(0xffffffffu, min(last_key[0], last_key[1]) < key0 + Cfg::kBlockKeys - 1 ||
+                                                            max(first_key[0], first_key[1]) > key0);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int keys[4] = {k0, k0 + 1, k0 + 8, k0 + 9};
-                const float raw[4] = {s0[2 * e], s0[2 * e + 1], s1[2 * e], s1[2 * e + 1]};
 #pragma unroll
-                for (int f = 0; f < 4; ++f)
-                    x[e][f] = keys[f] <= last_key[e] && keys[f] >= first_key[e] ? raw[f] * sh.scale_log2 : -INFINITY;
-                float top = fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3]));
+                for (int c = 0; c < kCols; ++c)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        float v = sc[0][c][2 * e + f];
+                        if (kChains == 2) v += sc[kChains - 1][c][2 * e + f];
+                        x[e][2 * c + f] = v * sh.scale_log2;
+                    }
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < 2 * kCols; ++c) {
+                        const int key = k0 + (c >> 1) * 8 + (c & 1);
+                        if (key > last_key[e] || key < first_key[e]) x[e][c] = -INFINITY;
+                    }
+                }
+                float top = x[e][0];
+#pragma unroll
+                for (int c = 1; c < 2 * kCols; ++c) top = fmaxf(top, x[e][c]);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 const float mn = fmaxf(m[e], top);
@@ -342,9 +372,9 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                 m[e] = mn;
                 float sum = 0.0f;
 #pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    x[e][f] = ex2(x[e][f] - base_m);
-                    sum += x[e][f];
+                for (int c = 0; c < 2 * kCols; ++c) {
+                    x[e][c] = ex2(x[e][c] - base_m);
+                    sum += x[e][c];
                 }
                 l[e] = l[e] * scale + sum;
                 if (__any_sync(0xffffffffu, scale != 1.0f)) {
@@ -356,25 +386,31 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                 }
             }
             // ---- O += P V; value rows past the keys are not multiplied (0 x NaN)
-            uint32_t pa[4] = {pack2<T>(x[0][0], x[0][1]), pack2<T>(x[1][0], x[1][1]), pack2<T>(x[0][2], x[0][3]),
-                              pack2<T>(x[1][2], x[1][3])};
             const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3);
-            const bool ragged = key0 + kSplitKeys > it.hi || key0 < it.lo;
+            const bool ragged = key0 + Cfg::kBlockKeys > it.hi || key0 < it.lo;
 #pragma unroll
-            for (int n = 0; n < DP / 8; n += 2) {
-                uint32_t vf[4];
-                const int chunk = (n & 7) + (lane >> 4);
-                ldmatrix_x4_trans(vf, vb + (n >> 3) * 2048 + vrow * 128 + ((chunk ^ (vrow & 7)) << 4));
-                if (ragged) {
+            for (int sub = 0; sub < Cfg::kSub; ++sub) {
+                const uint32_t pa[4] = {pack2<T>(x[0][4 * sub], x[0][4 * sub + 1]),
+                                        pack2<T>(x[1][4 * sub], x[1][4 * sub + 1]),
+                                        pack2<T>(x[0][4 * sub + 2], x[0][4 * sub + 3]),
+                                        pack2<T>(x[1][4 * sub + 2], x[1][4 * sub + 3])};
 #pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        const int key = k0 + (f & 1) * 8;
-                        if (key >= it.hi || key < it.lo) vf[f] &= 0xffff0000u;
-                        if (key + 1 >= it.hi || key + 1 < it.lo) vf[f] &= 0x0000ffffu;
+                for (int n = 0; n < DP / 8; n += 2) {
+                    uint32_t vf[4];
+                    const int chunk = (n & 7) + (lane >> 4);
+                    ldmatrix_x4_trans(vf, vb + (n >> 3) * (Cfg::kBlockKeys * 128) + sub * 2048 + vrow * 128 +
+                                              ((chunk ^ (vrow & 7)) << 4));
+                    if (ragged) {
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const int key = k0 + sub * kSplitKeys + (f & 1) * 8;
+                            if (key >= it.hi || key < it.lo) vf[f] &= 0xffff0000u;
+                            if (key + 1 >= it.hi || key + 1 < it.lo) vf[f] &= 0x0000ffffu;
+                        }
                     }
+                    mma_16816<T>(o[n], pa, vf[0], vf[1]);
+                    mma_16816<T>(o[n + 1], pa, vf[2], vf[3]);
                 }
-                mma_16816<T>(o[n], pa, vf[0], vf[1]);
-                mma_16816<T>(o[n + 1], pa, vf[2], vf[3]);
             }
             __syncwarp();
             if (i + Cfg::kStages < i1) issue(i + Cfg::kStages);
@@ -489,36 +525,42 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                 for (int i = tid; i < n * kSplitRows; i += kSplitThreads)
                     all[i] = __ldcg(&p.part_ml[slot_of(i / kSplitRows) * kSplitRows + i % kSplitRows]);
                 __syncthreads();
-                float ref[Cfg::kParts];
+                auto join = [&](auto live) {   // live: parts per thread that hold rows, so that 16 loads are under way
+                    constexpr int kLive = decltype(live)::value;
+                    float ref[kLive];
 #pragma unroll
-                for (int k = 0; k < Cfg::kParts; ++k) {
-                    const int row = part_row(k);
-                    if (row >= rows) break;
-                    float top = -INFINITY;
-                    for (int c = 0; c < n; ++c) top = fmaxf(top, all[c * kSplitRows + row].x);
-                    ref[k] = top == -INFINITY ? 0.0f : top;
-                    ml[k] = make_float2(top, 0.0f);
-                    acc[k] = make_float4(0, 0, 0, 0);
-                }
-#pragma unroll 4
-                for (int c = 0; c < n; ++c) {
-#pragma unroll
-                    for (int k = 0; k < Cfg::kParts; ++k) {
+                    for (int k = 0; k < kLive; ++k) {
                         const int row = part_row(k);
-                        if (row >= rows) break;
-                        const float2 e = all[c * kSplitRows + row];
-                        const float4 v = __ldcg(&p.part_o[(slot_of(c) * kSplitRows + row) * (DP / 4) + d / 4]);
-                        const float f = ex2(e.x - ref[k]);
-                        ml[k].y += f * e.y;
-                        acc[k].x += f * v.x;
-                        acc[k].y += f * v.y;
-                        acc[k].z += f * v.z;
-                        acc[k].w += f * v.w;
+                        float top = -INFINITY;
+                        for (int c = 0; c < n; ++c) top = fmaxf(top, all[c * kSplitRows + row].x);
+                        ref[k] = top == -INFINITY ? 0.0f : top;
+                        ml[k] = make_float2(top, 0.0f);
+                        acc[k] = make_float4(0, 0, 0, 0);
                     }
-                }
+#pragma unroll (16 / kLive)
+                    for (int c = 0; c < n; ++c) {
 #pragma unroll
-                for (int k = 0; k < Cfg::kParts; ++k)
-                    if (part_row(k) < rows) store(part_row(k), acc[k], ml[k]);
+                        for (int k = 0; k < kLive; ++k) {
+                            const int row = part_row(k);
+                            const float2 e = all[c * kSplitRows + row];
+                            const float4 v = row < rows
+                                                 ? __ldcg(&p.part_o[(slot_of(c) * kSplitRows + row) * (DP / 4) + d / 4])
+                                                 : make_float4(0, 0, 0, 0);
+                            const float f = ex2(e.x - ref[k]);
+                            ml[k].y += f * e.y;
+                            acc[k].x += f * v.x;
+                            acc[k].y += f * v.y;
+                            acc[k].z += f * v.z;
+                            acc[k].w += f * v.w;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < kLive; ++k)
+                        if (part_row(k) < rows) store(part_row(k), acc[k], ml[k]);
+                };
+                if (rows * (DP / 4) <= kSplitThreads) join(std::integral_constant<int, 1>());
+                else if (Cfg::kParts > 2 && rows * (DP / 4) <= 2 * kSplitThreads) join(std::integral_constant<int, 2>());
+                else join(std::integral_constant<int, Cfg::kParts>());
             }
         }
         }   // of an item with units in the run
@@ -537,7 +579,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                     row_tiles = split_row_tiles(sh, sq);
                 } while (row_tiles == 0);
             }
-            it = split_item(sh, sq, rt);
+            it = split_item(sh, sq, rt, Cfg::kUnit);
         }
         u0 = 0;
         u1 = static_cast<int>(min(end - first, static_cast<long long>(it.units)));
