@@ -29,12 +29,15 @@ bool encode_kv_map(CUtensorMap* m, const kt_paged_kv& kv, bool values, int box_s
                                  2 * static_cast<uint64_t>(values ? kv.v_head_stride : kv.k_head_stride),
                                  2 * static_cast<uint64_t>(values ? kv.v_page_stride : kv.k_page_stride)};
     const uint32_t box[4] = {64, static_cast<uint32_t>(box_slots), 1, 1};
+    // L2 fetches in units that divide a row: what follows it in memory may be another head's, read much later
+    const int row = 2 * kv.head_dim;
+    const CUtensorMapL2promotion promotion = row % 256 == 0   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                             : row % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                             : row % 64 == 0  ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                                              : CU_TENSOR_MAP_L2_PROMOTION_NONE;
     return encode_tiled_map(m, kv.dtype == KT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                            values ? kv.v : kv.k, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
-                            // no more than a row: the next one in memory may be another head's, read much later
-                            2 * kv.head_dim % 256 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
-                                                       : CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+                            values ? kv.v : kv.k, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, promotion);
 }
 
 static kt_status check_heads(const kt_heads* h, const char* name, size_t align, int64_t step) {
