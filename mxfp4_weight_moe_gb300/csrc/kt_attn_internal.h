@@ -35,7 +35,7 @@ struct HeadRowsParams {
     long long table_stride;
     int seqs, max_pages, page_size, num_pages;
     int* err;
-    int units_per_token, lanes, lanes_log2, row_lanes;   // set by the launcher
+    int units_per_token, lanes, lanes_log2, row_lanes, weight_vector;   // set by the launcher
 };
 // wide: every pointer is 16-byte aligned, every stride a multiple of 8 and head_dim and rotary_dim multiples of 16.
 cudaError_t launch_head_rows(HeadRowsParams& p, int dtype, bool wide, cudaStream_t s);

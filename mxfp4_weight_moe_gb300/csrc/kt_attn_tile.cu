@@ -328,26 +328,6 @@ __device__ __forceinline__ float max32(const float (&x)[32]) {
     return max3(max3(a, x[30], x[31]), b, b);
 }
 
-// Pairs of fp32 in one instruction.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // 32 softmax weights 2^(c s + neg), packed in pairs; their sum is added to `sum` (two halves).
 template <typename T>
 __device__ __forceinline__ void weights32(const float (&x)[32], uint64_t c2, uint64_t neg2, uint32_t (&pk)[16],
