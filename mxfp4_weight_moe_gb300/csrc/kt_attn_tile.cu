@@ -17,8 +17,10 @@
 // Work is dealt as in the split kernel: all items' key tiles form one line, cut
 // into equal runs; the last CTA of a cut item joins its partial sums in order.
 //
-// Warps: 0-3 softmax of group 0, 4-7 of group 1, 8 issues the MMAs, 9 and 10 the TMA loads.
+// Warps: 0-3 softmax of group 0, 4-7 of group 1, 8 issues the MMAs, 9 to 11 the TMA loads of
+// keys, values and queries.
 #include <algorithm>
+#include <type_traits>
 
 #include "kt_attn_dev.cuh"
 
@@ -31,40 +33,50 @@ constexpr int kTileMinUnits = kItemUnits + 2;   // least units of a CTA's run
 constexpr int kPlanSeqs = 512;        // sequences planned at a time
 constexpr float kLazyLog2 = 8.0f;     // growth of the maximum (log2) that is let stand
 
-// Tensor memory: the CTA takes all 512 columns, so it starts at 0.  S of the groups (P in its first half), then O.
+// Tensor memory: the CTA takes all 512 columns, so it starts at 0.  S of the groups, then O.  Heads of up to 64 leave
+// room for P of its own, so that a group's next S is computed while its weights are; else P lies in S's first half.
 constexpr uint32_t kTmemS = 0, kTmemO = 256;
 
 template <int DP>
 struct TileCfg {
     static constexpr int kQBytes = 128 * DP * 2;         // one row group
     static constexpr int kStageBytes = kTileKeys * DP * 2;   // one tile of K or V
-    static constexpr int kStages = DP == 128 ? 5 : 10;
-    static constexpr int kSmem = 2 * kQBytes + kStages * kStageBytes + 1024;
+    static constexpr int kStages = DP == 128 ? 5 : 9;        // odd: K and V alternate in a stage
+    static constexpr bool kOwnP = DP == 64;
+    static constexpr uint32_t kTmemP = kOwnP ? 384 : kTmemS, kPStep = kOwnP ? 64 : 128;   // P of group 0, to group 1's
+    static constexpr int kQBufs = DP == 128 ? 1 : 2;
+    static constexpr int kQAll = kQBufs * 2 * kQBytes;
+    static constexpr int kSmem = kQAll + kStages * kStageBytes + 1024;
+};
+
+struct TileGeometry {
+    int tokens;      // of a row group: 128 / group
+    int box_slots;   // slots of one load: the largest power of two that divides page_size, at most 128
 };
 
 struct TileParams {
     AttnShape sh;
     void* out;
     long long o_token, o_head;
-    int tokens_per_group;   // 128 / group
-    int box_slots;          // slots of one load: the largest power of two that divides page_size, at most 128
+    TileGeometry geo;
     float4* part_o;         // [CTAs][2 pieces][DP / 4][256 rows]
     float2* part_ml;        // [CTAs][2][256]
     unsigned* counters;     // [CTAs][2 groups]
 };
 
 struct TileItem {
-    int lo, hi, tile0, tiles;   // keys that some row sees; first key tile, key tiles (at least one)
+    int lo, hi;        // keys that some row sees: [lo, hi)
+    int base, tiles;   // first key of its first key tile, key tiles (at least one)
 };
-__device__ __forceinline__ TileItem tile_item(const AttnShape& s, const SeqInfo& q, int tokens_per_item, int rt) {
+__device__ __forceinline__ TileItem tile_item(const AttnShape& s, const SeqInfo& q, const TileGeometry& g, int rt) {
     TileItem it;
-    const int t0 = rt * tokens_per_item;
-    const int t1 = min(t0 + tokens_per_item, q.q_len) - 1;
+    const int t0 = rt * 2 * g.tokens;
+    const int t1 = min(t0 + 2 * g.tokens, q.q_len) - 1;
     it.hi = max(0, min(q.first_pos + t1 + 1, q.keys));
     it.lo = window_start(q.first_pos + t0, s.window);
     if (it.lo >= it.hi) it.lo = it.hi = 0;
-    it.tile0 = it.lo / kTileKeys;
-    it.tiles = max(1, (it.hi + kTileKeys - 1) / kTileKeys - it.tile0);
+    it.base = it.lo & ~(g.box_slots - 1);
+    it.tiles = max(1, (it.hi - it.base + kTileKeys - 1) / kTileKeys);
     return it;
 }
 
@@ -85,10 +97,10 @@ struct TileWalk {
     SeqInfo sq;
     TileItem it;
 
-    __device__ __forceinline__ bool load_seq(const AttnShape& s, int tpi) {
+    __device__ __forceinline__ bool load_seq(const AttnShape& s, const TileGeometry& g) {
         for (; b < s.seqs; ++b) {
             sq = seq_info(s, b);
-            row_tiles = (sq.q_len + tpi - 1) / tpi;
+            row_tiles = (sq.q_len + 2 * g.tokens - 1) / (2 * g.tokens);
             if (row_tiles > 0) return true;
         }
         return false;
@@ -98,18 +110,18 @@ struct TileWalk {
         t1 = static_cast<int>(min(end - first, static_cast<long long>(it.tiles)));
     }
     // whole warp: finds the item of unit plan.in_seq of sequence plan.seq; false: no work
-    __device__ __forceinline__ bool start(const AttnShape& s, int tpi, const RunPlan& plan) {
+    __device__ __forceinline__ bool start(const AttnShape& s, const TileGeometry& g, const RunPlan& plan) {
         const int lane = static_cast<int>(threadIdx.x) & 31;
         end = min(plan.begin + plan.per, plan.total);
         if (plan.begin >= end) return false;
         b = plan.seq;
         rt = 0;
-        load_seq(s, tpi);
+        load_seq(s, g);
         long long before = 0;
         for (int r0 = 0; r0 < row_tiles; r0 += 32) {
             const int r = r0 + lane;
             const long long n =
-                r < row_tiles ? static_cast<long long>(item_units(tile_item(s, sq, tpi, r))) * s.kv_heads : 0;
+                r < row_tiles ? static_cast<long long>(item_units(tile_item(s, sq, g, r))) * s.kv_heads : 0;
             long long incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -125,14 +137,14 @@ struct TileWalk {
             }
             before += __shfl_sync(0xffffffffu, incl, 31);
         }
-        it = tile_item(s, sq, tpi, rt);
+        it = tile_item(s, sq, g, rt);
         const long long in = plan.in_seq - before;
         h = static_cast<int>(in / item_units(it));
         first = plan.begin - (in - static_cast<long long>(h) * item_units(it)) + kItemUnits;
         cut(plan.begin);
-        return t1 > t0 || next(s, tpi);
+        return t1 > t0 || next(s, g);
     }
-    __device__ __forceinline__ bool next(const AttnShape& s, int tpi) {
+    __device__ __forceinline__ bool next(const AttnShape& s, const TileGeometry& g) {
         first += it.tiles + kItemUnits;   // a run that goes on has finished this item
         if (first >= end) return false;
         if (++h == s.kv_heads) {
@@ -140,9 +152,9 @@ struct TileWalk {
             if (++rt == row_tiles) {
                 rt = 0;
                 ++b;
-                if (!load_seq(s, tpi)) return false;
+                if (!load_seq(s, g)) return false;
             }
-            it = tile_item(s, sq, tpi, rt);
+            it = tile_item(s, sq, g, rt);
         }
         t0 = 0;
         t1 = static_cast<int>(min(end - first, static_cast<long long>(it.tiles)));
@@ -152,16 +164,16 @@ struct TileWalk {
 };
 
 // Deals all sequences' units in equal runs.  A warp sums a sequence: a long chunk has many items.
-__device__ __forceinline__ RunPlan plan_tiles(const AttnShape& s, int tpi, unsigned* costs, RunPlan* shared) {
+__device__ __forceinline__ RunPlan plan_tiles(const AttnShape& s, const TileGeometry& g, unsigned* costs, RunPlan* shared) {
     constexpr int kWarps = kTileThreads / 32;
     __shared__ long long s_sum[kWarps];
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     auto fill = [&](int b0) {   // costs of sequences [b0, b0 + kPlanSeqs): units / kv_heads
         for (int b = b0 + warp; b < min(s.seqs, b0 + kPlanSeqs); b += kWarps) {
             const SeqInfo q = seq_info(s, b);
-            const int tiles = (q.q_len + tpi - 1) / tpi;
+            const int tiles = (q.q_len + 2 * g.tokens - 1) / (2 * g.tokens);
             unsigned n = 0;
-            for (int r = lane; r < tiles; r += 32) n += static_cast<unsigned>(item_units(tile_item(s, q, tpi, r)));
+            for (int r = lane; r < tiles; r += 32) n += static_cast<unsigned>(item_units(tile_item(s, q, g, r)));
             n = __reduce_add_sync(0xffffffffu, n);
             if (lane == 0) costs[b - b0] = n;
         }
@@ -355,7 +367,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const v
 
 // The item's tile whose last rows lie past the sequence's end inside a page, if it is in this run; else -1.
 __device__ __forceinline__ int ragged_tile(const TileWalk& w, int box_slots) {
-    const int j = w.sq.keys / kTileKeys - w.it.tile0;
+    const int j = w.sq.keys >= w.it.base ? (w.sq.keys - w.it.base) / kTileKeys : -1;
     return j >= w.t0 && j < w.t1 && (w.sq.keys & (box_slots - 1)) != 0 ? j : -1;
 }
 
@@ -366,16 +378,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     using Cfg = TileCfg<DP>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_kv_full[Cfg::kStages], s_kv_empty[Cfg::kStages];
-    __shared__ __align__(8) uint64_t s_q_full[2], s_q_empty[2], s_s_full[2], s_p_full[2][2], s_o_full[2], s_done;
+    __shared__ __align__(8) uint64_t s_q_full[Cfg::kQBufs][2], s_q_empty[Cfg::kQBufs][2];
+    __shared__ __align__(8) uint64_t s_s_full[2], s_s_free[2], s_p_full[2][2], s_o_full[2], s_done;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_last[2];
     __shared__ RunPlan s_plan;
     const AttnShape& sh = p.sh;
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-    const int tpg = p.tokens_per_group;
+    const int tpg = p.geo.tokens;
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t q_smem = smem_u32(smem);
-    uint8_t* kv_ptr = smem + 2 * Cfg::kQBytes;
+    uint8_t* kv_ptr = smem + Cfg::kQAll;
     const uint32_t kv_smem = smem_u32(kv_ptr);
 
     if (tid == 0) {
@@ -385,10 +398,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_init(smem_u32(&s_kv_empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&s_q_full[i]), 1);
-            mbar_init(smem_u32(&s_q_empty[i]), 1);
+            for (int b = 0; b < Cfg::kQBufs; ++b) {
+                mbar_init(smem_u32(&s_q_full[b][i]), 1);
+                mbar_init(smem_u32(&s_q_empty[b][i]), 1);
+            }
+            mbar_init(smem_u32(&s_s_free[i]), 4);   // the group's warps
             mbar_init(smem_u32(&s_s_full[i]), 1);
-            mbar_init(smem_u32(&s_p_full[i][0]), 4);   // the group's warps
+            mbar_init(smem_u32(&s_p_full[i][0]), 4);
             mbar_init(smem_u32(&s_p_full[i][1]), 4);
             mbar_init(smem_u32(&s_o_full[i]), 1);
         }
@@ -403,12 +419,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc_relinquish();
     }
     if (tpg * sh.group < 128) {   // rows of no token: zeros for good (the loads do not touch them)
-        for (int i = tid; i < 2 * Cfg::kQBytes / 16; i += kTileThreads)
+        for (int i = tid; i < Cfg::kQAll / 16; i += kTileThreads)
             reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     }
     griddep_wait();
     griddep_launch_dependents();
-    const RunPlan plan = plan_tiles(sh, 2 * tpg, reinterpret_cast<unsigned*>(kv_ptr), &s_plan);
+    const RunPlan plan = plan_tiles(sh, p.geo, reinterpret_cast<unsigned*>(kv_ptr), &s_plan);
     tc_fence_before();
     fence_proxy_async_smem();   // the plan's and the zeros' generic writes before the first loads
     __syncthreads();
@@ -418,56 +434,39 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         TileWalk w;
-        bool more_items = w.start(sh, 2 * tpg, plan);
+        bool more_items = w.start(sh, p.geo, plan);
         if (warp == 9 || warp == 10) {
-            // ------------------------------------------------ loads: queries and keys by warp 9, values by warp 10
+            // ------------------------------------------------ loads of keys by warp 9, of values by warp 10
             // (with 16-slot pages a tile takes 16 loads, which one warp cannot issue for both at the tensor cores' pace)
-            const bool values = warp == 10;
-            uint32_t load = values ? 1 : 0, item_no[2] = {0, 0};   // tiles lie in the ring as K0 V0 K1 V1 ...
-            const int boxes = kTileKeys / p.box_slots;
+            uint32_t load = warp == 10 ? 1 : 0;   // tiles lie in the ring as K0 V0 K1 V1 ...
+            const int boxes = kTileKeys / p.geo.box_slots;
             const int box = lane % boxes;   // of 1, 2, 4 or 8 per 64 elements (page_size is a multiple of 16)
-            const CUtensorMap* map = values ? &vmap : &kmap;
+            const CUtensorMap* map = warp == 10 ? &vmap : &kmap;
             bool ok = true;
-            auto load_tile = [&](int key0, const int32_t* pages) {   // keys [key0, key0 + 128)
-                const uint32_t stage = load % Cfg::kStages, round = load / Cfg::kStages;
-                const uint32_t full = smem_u32(&s_kv_full[stage]);
-                // boxes that no row sees come from outside the cache, as zeros
-                const int key = key0 + box * p.box_slots;
-                int page = -1;
-                if (lane < boxes && key < w.it.hi && key + p.box_slots > w.it.lo) page = checked_page(sh, pages, key);
-                page = __shfl_sync(0xffffffffu, page, box);
-                if (round > 0) ok = ok && warp_wait(smem_u32(&s_kv_empty[stage]), (round - 1) & 1u, abort_flag);
-                if (!ok) return;
-                if (lane == 0) mbar_arrive_expect_tx(full, Cfg::kStageBytes);
-                __syncwarp();
-                if (lane < boxes * (DP / 64)) {
-                    const int x = lane / boxes;
-                    tma_load_4d(kv_smem + stage * Cfg::kStageBytes + x * (kTileKeys * 128) + box * p.box_slots * 128,
-                                map, full, x * 64, key % sh.page_size, w.h, page);
-                }
-                __syncwarp();
-                load += 2;
-            };
-            for (; more_items && ok; more_items = w.next(sh, 2 * tpg)) {
+            for (; more_items && ok; more_items = w.next(sh, p.geo)) {
                 const int32_t* pages = sh.block_table + w.b * sh.table_stride;
-                if (!values) {
-                    const int groups = w.groups(tpg);
-                    for (int i = 0; i < groups && ok; ++i) {
-                        if (item_no[i] > 0)
-                            ok = warp_wait(smem_u32(&s_q_empty[i]), (item_no[i] - 1) & 1u, abort_flag);
-                        if (!ok) break;
-                        ++item_no[i];
-                        if (lane == 0) {
-                            const uint32_t bar = smem_u32(&s_q_full[i]);
-                            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(tpg * sh.group * DP * 2));
-                            for (int x = 0; x < DP; x += 64)
-                                tma_load_3d(q_smem + i * Cfg::kQBytes + (x / 64) * (128 * 128), &qmap, bar, x,
-                                            w.h * sh.group, w.sq.first_token + (w.rt * 2 + i) * tpg);
-                        }
-                        __syncwarp();
+                for (int j = w.t0; j < w.t1; ++j) {
+                    const uint32_t stage = load % Cfg::kStages, round = load / Cfg::kStages;
+                    const uint32_t full = smem_u32(&s_kv_full[stage]);
+                    // boxes that no row sees come from outside the cache, as zeros
+                    const int key = w.it.base + j * kTileKeys + box * p.geo.box_slots;
+                    int page = -1;
+                    if (lane < boxes && key < w.it.hi && key + p.geo.box_slots > w.it.lo)
+                        page = checked_page(sh, pages, key);
+                    page = __shfl_sync(0xffffffffu, page, box);
+                    if (round > 0) ok = warp_wait(smem_u32(&s_kv_empty[stage]), (round - 1) & 1u, abort_flag);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive_expect_tx(full, Cfg::kStageBytes);
+                    __syncwarp();
+                    if (lane < boxes * (DP / 64)) {
+                        const int x = lane / boxes;
+                        tma_load_4d(kv_smem + stage * Cfg::kStageBytes + x * (kTileKeys * 128) +
+                                        box * p.geo.box_slots * 128,
+                                    map, full, x * 64, key % sh.page_size, w.h, page);
                     }
+                    __syncwarp();
+                    load += 2;
                 }
-                for (int j = w.t0; j < w.t1 && ok; ++j) load_tile((w.it.tile0 + j) * kTileKeys, pages);
             }
             if (!ok) {
                 if (lane == 0 && !*reinterpret_cast<volatile int*>(&s_abort)) {
@@ -479,87 +478,148 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int i = 0; i < Cfg::kStages && load >= 2; ++i) {
                     load -= 2;
                     mbar_wait(smem_u32(&s_kv_full[load % Cfg::kStages]), (load / Cfg::kStages) & 1u, &never, 1000000);
-                    if (load < 2) break;
                 }
+            }
+        } else if (warp == 11) {
+            // ------------------------------------------------ loads of queries
+            uint32_t item_no[2] = {0, 0};   // of each group
+            bool ok = true;
+            for (; more_items && ok; more_items = w.next(sh, p.geo)) {
+                const int groups = w.groups(tpg);
+                for (int i = 0; i < groups; ++i) {
+                    const uint32_t buf = item_no[i] % Cfg::kQBufs, round = item_no[i] / Cfg::kQBufs;
+                    if (round > 0) ok = warp_wait(smem_u32(&s_q_empty[buf][i]), (round - 1) & 1u, abort_flag);
+                    if (!ok) break;
+                    ++item_no[i];
+                    if (lane == 0) {
+                        const uint32_t bar = smem_u32(&s_q_full[buf][i]);
+                        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(tpg * sh.group * DP * 2));
+                        for (int x = 0; x < DP; x += 64)
+                            tma_load_3d(q_smem + (buf * 2 + i) * Cfg::kQBytes + (x / 64) * (128 * 128), &qmap, bar, x,
+                                        w.h * sh.group, w.sq.first_token + (w.rt * 2 + i) * tpg);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (!ok) {
+                if (lane == 0 && !*reinterpret_cast<volatile int*>(&s_abort)) {
+                    s_abort = 1;
+                    set_error(sh.err, KT_DEVERR_TIMEOUT_LOAD);
+                }
+                int never = 0;
                 for (int i = 0; i < 2; ++i)
-                    if (item_no[i] > 0) mbar_wait(smem_u32(&s_q_full[i]), (item_no[i] - 1) & 1u, &never, 1000000);
+                    for (uint32_t k = 0; k < Cfg::kQBufs && k < item_no[i]; ++k) {
+                        const uint32_t n = item_no[i] - 1 - k;
+                        mbar_wait(smem_u32(&s_q_full[n % Cfg::kQBufs][i]), (n / Cfg::kQBufs) & 1u, &never, 1000000);
+                    }
             }
         } else if (warp == 8 && elect_one()) {
             // ------------------------------------------------ MMAs, issued by one thread
+            // The run is one stream of tiles, S one tile ahead of O, across the items' ends as well.
             constexpr uint32_t kIdescQK = idesc_f16<T>(kTileKeys, false);
             constexpr uint32_t kIdescPV = idesc_f16<T>(DP, true);
-            uint32_t stage = 0, parity = 0, q_parity[2] = {0, 0}, p_parity[2] = {0, 0};
-            auto wait = [&](uint64_t& bar, uint32_t par) { return mbar_wait(smem_u32(&bar), par, abort_flag); };
-            auto advance = [&]() {
-                if (++stage == Cfg::kStages) {
-                    stage = 0;
-                    parity ^= 1u;
+            struct Tile {
+                int groups;
+                bool first, last;   // of its item's tiles in this run
+            };
+            int ahead = w.t0;                                       // S's next tile, in item w
+            struct Ring {
+                uint32_t stage, parity;
+                __device__ __forceinline__ void step() {   // K and V alternate
+                    stage += 2;
+                    if (stage >= Cfg::kStages) {
+                        stage -= Cfg::kStages;
+                        parity ^= 1u;
+                    }
                 }
             };
-            auto qk = [&](int i, uint32_t st) {   // S_i = Q_i K^T
-                const uint32_t a = sdesc_low(q_smem + i * Cfg::kQBytes), b = sdesc_low(kv_smem + st * Cfg::kStageBytes);
+            Ring k_ring{0, 0}, v_ring{1, 0};
+            // parities of each group's next query item, weights and (kOwnP) release of S; query buffer
+            uint32_t q_parity0 = 0, q_parity1 = 0, q_buf0 = 0, q_buf1 = 0, p_parity0 = 0, p_parity1 = 0;
+            uint32_t free0 = 1, free1 = 1;   // S is free at first: the phase before the first has passed
+            auto wait = [&](uint64_t& bar, uint32_t par) { return mbar_wait(smem_u32(&bar), par, abort_flag); };
+            auto tile_ahead = [&](Tile& t) {   // false: no more
+                if (ahead == w.t1) {
+                    more_items = more_items && w.next(sh, p.geo);
+                    ahead = w.t0;
+                }
+                if (!more_items) return false;
+                t = Tile{w.groups(tpg), ahead == w.t0, ahead + 1 == w.t1};
+                ++ahead;
+                return true;
+            };
+            auto qk = [&](auto group, const Tile& t) -> bool {   // S_i = Q_i K^T
+                constexpr int i = decltype(group)::value;
+                uint32_t& q_parity = i == 0 ? q_parity0 : q_parity1;
+                uint32_t& buf = i == 0 ? q_buf0 : q_buf1;
+                uint32_t& free = i == 0 ? free0 : free1;
+                if (t.first && !wait(s_q_full[buf][i], q_parity)) return false;
+                if (i == 0 && !wait(s_kv_full[k_ring.stage], k_ring.parity)) return false;
+                if (Cfg::kOwnP) {
+                    if (!wait(s_s_free[i], free)) return false;
+                    free ^= 1u;
+                }
+                tc_fence_after();
+                const uint32_t a = sdesc_low(q_smem + (buf * 2 + i) * Cfg::kQBytes);
+                const uint32_t b = sdesc_low(kv_smem + k_ring.stage * Cfg::kStageBytes);
 #pragma unroll
                 for (int ks = 0; ks < DP / 16; ++ks) {
                     const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
                     tc_mma_ss(kTmemS + i * 128, sdesc(a + off, 16), sdesc(b + off, 16), kIdescQK, ks > 0 ? 1u : 0u);
                 }
                 tc_commit(smem_u32(&s_s_full[i]));
-            };
-            auto run = [&]() -> bool {
-                for (; more_items; more_items = w.next(sh, 2 * tpg)) {
-                    const int groups = w.groups(tpg);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (i >= groups) break;
-                        if (!wait(s_q_full[i], q_parity[i])) return false;
-                        q_parity[i] ^= 1u;
-                        if (i == 0 && !wait(s_kv_full[stage], parity)) return false;
-                        tc_fence_after();
-                        qk(i, stage);
-                        if (w.t1 - w.t0 == 1) tc_commit(smem_u32(&s_q_empty[i]));
-                    }
-                    tc_commit(smem_u32(&s_kv_empty[stage]));
-                    advance();
-                    for (int j = w.t0; j < w.t1; ++j) {
-                        const uint32_t vst = stage;
-                        if (!wait(s_kv_full[vst], parity)) return false;
-                        advance();
-                        const bool more = j + 1 < w.t1;
-                        const uint32_t b = sdesc_low(kv_smem + vst * Cfg::kStageBytes);
-                        const uint32_t acc = j > w.t0 ? 1u : 0u;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if (i >= groups) break;
-                            if (!wait(s_p_full[i][0], p_parity[i])) return false;
-                            tc_fence_after();
-#pragma unroll
-                            for (int ks = 0; ks < kTileKeys / 16; ++ks) {
-                                if (ks == kTileKeys / 16 * 3 / 4) {
-                                    if (!wait(s_p_full[i][1], p_parity[i])) return false;
-                                    tc_fence_after();
-                                }
-                                tc_mma_ts(kTmemO + i * DP, kTmemS + i * 128 + ks * 8,
-                                          sdesc(b + ((ks * 16 * 128) >> 4), kTileKeys * 128), kIdescPV,
-                                          ks > 0 ? 1u : acc);
-                            }
-                            p_parity[i] ^= 1u;
-                            if (more) {
-                                if (i == 0 && !wait(s_kv_full[stage], parity)) return false;
-                                tc_fence_after();
-                                qk(i, stage);
-                                if (j + 2 == w.t1) tc_commit(smem_u32(&s_q_empty[i]));
-                            } else {
-                                tc_commit(smem_u32(&s_o_full[i]));
-                            }
-                        }
-                        tc_commit(smem_u32(&s_kv_empty[vst]));
-                        if (more) {
-                            tc_commit(smem_u32(&s_kv_empty[stage]));
-                            advance();
-                        }
-                    }
+                if (t.last) {
+                    tc_commit(smem_u32(&s_q_empty[buf][i]));
+                    if (Cfg::kQBufs == 1 || (buf ^= 1u) == 0) q_parity ^= 1u;
+                }
+                if (i + 1 == t.groups) {
+                    tc_commit(smem_u32(&s_kv_empty[k_ring.stage]));
+                    k_ring.step();
                 }
                 return true;
+            };
+            auto pv = [&](auto group, const Tile& t) -> bool {   // O_i (+)= P_i V
+                constexpr int i = decltype(group)::value;
+                uint32_t& p_parity = i == 0 ? p_parity0 : p_parity1;
+                if (i == 0 && !wait(s_kv_full[v_ring.stage], v_ring.parity)) return false;
+                const uint32_t b = sdesc_low(kv_smem + v_ring.stage * Cfg::kStageBytes);
+                if (!wait(s_p_full[i][0], p_parity)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < kTileKeys / 16; ++ks) {
+                    if (ks == kTileKeys / 16 * 3 / 4) {
+                        if (!wait(s_p_full[i][1], p_parity)) return false;
+                        tc_fence_after();
+                    }
+                    tc_mma_ts(kTmemO + i * DP, Cfg::kTmemP + i * Cfg::kPStep + ks * 8,
+                              sdesc(b + ((ks * 16 * 128) >> 4), kTileKeys * 128), kIdescPV,
+                              ks > 0 || !t.first ? 1u : 0u);
+                }
+                p_parity ^= 1u;
+                if (Cfg::kOwnP || t.last) tc_commit(smem_u32(&s_o_full[i]));
+                if (i + 1 == t.groups) {
+                    tc_commit(smem_u32(&s_kv_empty[v_ring.stage]));
+                    v_ring.step();
+                }
+                return true;
+            };
+            auto run = [&]() -> bool {
+                const std::integral_constant<int, 0> group0{};
+                const std::integral_constant<int, 1> group1{};
+                Tile now, next;
+                if (!tile_ahead(next)) return true;
+                if (!qk(group0, next) || (next.groups > 1 && !qk(group1, next))) return false;
+                while (true) {
+                    now = next;
+                    const bool any = tile_ahead(next);
+                    if (Cfg::kOwnP && any)
+                        if (!qk(group0, next) || (next.groups > 1 && !qk(group1, next))) return false;
+                    if (!pv(group0, now)) return false;
+                    if (!Cfg::kOwnP && any && !qk(group0, next)) return false;
+                    if (now.groups > 1 && !pv(group1, now)) return false;
+                    if (!any) return true;
+                    if (!Cfg::kOwnP && next.groups > 1 && !qk(group1, next)) return false;
+                }
             };
             if (!run() && !*reinterpret_cast<volatile int*>(&s_abort)) {
                 s_abort = 1;
@@ -578,11 +638,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = kTmemS + lane_base + grp * 128;
         const uint32_t t_o = kTmemO + lane_base + grp * DP;
+        const uint32_t t_p = Cfg::kTmemP + lane_base + grp * Cfg::kPStep;
         const float c = sh.scale_log2;
         uint32_t tile_no = 0, item_no = 0, loads = 0;   // loads: key and value tiles of the items so far
         bool ok = true;
         TileWalk w;
-        for (bool more = w.start(sh, 2 * tpg, plan); more && ok; more = w.next(sh, 2 * tpg)) {
+        for (bool more = w.start(sh, p.geo, plan); more && ok; more = w.next(sh, p.geo)) {
             if (grp >= w.groups(tpg)) continue;
             const int tok = (w.rt * 2 + grp) * tpg + row / sh.group;
             const bool valid = row / sh.group < tpg && tok < w.sq.q_len;
@@ -590,10 +651,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // keys [first, last] are seen; rows of no token compute without masks and are not stored
             const int last = valid ? min(pos, w.sq.keys - 1) : 0x7fffffff;
             const int first = valid ? window_start(pos, sh.window) : 0;
-            const int rag = ragged_tile(w, p.box_slots);
+            const int rag = ragged_tile(w, p.geo.box_slots);
             float m = -INFINITY, l = 0.0f;
             for (int j = w.t0; j < w.t1; ++j) {
-                const int key0 = (w.it.tile0 + j) * kTileKeys;
+                const int key0 = w.it.base + j * kTileKeys;
                 ok = warp_wait(smem_u32(&s_s_full[grp]), tile_no & 1u, abort_flag);
                 if (!ok) break;
                 ++tile_no;
@@ -606,12 +667,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 tc_wait_ld_of(x[0]);
 #pragma unroll
                 for (int q = 1; q < 4; ++q) pin(x[q]);
+                if (Cfg::kOwnP) {   // S is in registers: the group's next one may come
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&s_s_free[grp]));
+                }
+                uint32_t dead = 0;   // quarters that no row of the warp sees
                 if (masked) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < 4; ++q) {
+                        if (__all_sync(0xffffffffu, hi < q * 32 || lo > q * 32 + 31)) dead |= 1u << q;
                         if (__any_sync(0xffffffffu, hi < q * 32 + 31 || lo > q * 32)) mask32(x[q], lo - q * 32, hi - q * 32);
+                    }
                 }
                 const float top = max3(max3(max32(x[0]), max32(x[1]), max32(x[2])), max32(x[3]), m);
+                if (Cfg::kOwnP && tile_no > 1) {   // the group's product before this one has been taken: O and P are free
+                    ok = warp_wait(smem_u32(&s_o_full[grp]), (tile_no - 2) & 1u, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
                 // the reference follows the maximum only when that has outgrown it (also from -inf)
                 const bool grown = (top - m) * c > kLazyLog2;
                 if (__any_sync(0xffffffffu, grown)) {
@@ -638,7 +712,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     ok = warp_wait(smem_u32(&s_kv_full[st]), (load / Cfg::kStages) & 1u, abort_flag);
                     if (!ok) break;
                     const int past = w.sq.keys - key0;
-                    const int end = (past / p.box_slots + 1) * p.box_slots;   // the rest was loaded as zeros
+                    const int end = (past / p.geo.box_slots + 1) * p.geo.box_slots;   // the rest was loaded as zeros
                     for (int i = row; i < (end - past) * (DP / 8); i += 128) {
                         const int r = past + i / (DP / 8), x = i % (DP / 8);
                         *reinterpret_cast<uint4*>(kv_ptr + st * Cfg::kStageBytes + (x >> 3) * (kTileKeys * 128) +
@@ -649,16 +723,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 const float neg = m == -INFINITY ? 0.0f : -m * c;
                 const uint64_t c2 = pair(c, c), neg2 = pair(neg, neg);
                 uint64_t sum_a = 0, sum_b = 0;   // two zeros each
+                auto hand_over = [&](int part) {   // three quarters of the keys, then the rest: the product starts early
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&s_p_full[grp][part]));
+                };
+                if (dead == 0) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t pk[16];
-                    weights32<T>(x[q], c2, neg2, pk, sum_a, sum_b);
-                    tc_st_16(t_s + q * 16, pk);
-                    if (q >= 2) {   // three quarters of the keys, then the rest: the product starts with the first
-                        tc_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&s_p_full[grp][q - 2]));
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pk[16];
+                        weights32<T>(x[q], c2, neg2, pk, sum_a, sum_b);
+                        tc_st_16(t_p + q * 16, pk);
+                        if (q >= 2) hand_over(q - 2);
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pk[16] = {};
+                        if (!(dead >> q & 1u)) weights32<T>(x[q], c2, neg2, pk, sum_a, sum_b);
+                        tc_st_16(t_p + q * 16, pk);
+                        if (q >= 2) hand_over(q - 2);
                     }
                 }
                 float s0, s1;
@@ -667,7 +752,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             if (!ok) break;
             loads += 2 * static_cast<uint32_t>(w.t1 - w.t0);
-            ok = warp_wait(smem_u32(&s_o_full[grp]), item_no & 1u, abort_flag);
+            ok = warp_wait(smem_u32(&s_o_full[grp]), (Cfg::kOwnP ? tile_no - 1 : item_no) & 1u, abort_flag);
             if (!ok) break;
             ++item_no;
             tc_fence_after();
@@ -689,6 +774,32 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 scale_o = lt == 0.0f ? 0.0f : scale_o / lt;
             };
+            // A row's 64 bytes lie with one lane; four lanes exchange 16-byte pieces so that they write a row at a time.
+            const uint64_t to = valid ? reinterpret_cast<uint64_t>(dst) : 0;   // 0: not stored
+            auto store_64 = [&](uint32_t(&v)[16], int d) {   // elements [d, d + 32) of the row
+                const bool odd = lane & 1, upper = lane & 2;
+#pragma unroll
+                for (int i = 0; i < 16; i += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[i + k] : v[i + 4 + k], 1);
+                        if (odd) v[i + k] = got;
+                        else v[i + 4 + k] = got;
+                    }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? v[k] : v[8 + k], 2);
+                    if (upper) v[k] = got;
+                    else v[8 + k] = got;
+                }
+                const int at = d + (lane & 3) * 8;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {   // row k of the four
+                    T* row_k = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, to, (lane & ~3) + k));
+                    if (row_k != nullptr && at < sh.head_dim)
+                        *reinterpret_cast<uint4*>(row_k + at) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                }
+            };
             if (whole) {
                 float inv;
                 closing(m, l, inv);
@@ -697,18 +808,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     float o[32];
                     tc_ld_f32(t_o + q * 32, o);
                     tc_wait_ld_of(o);
-                    if (valid) {
+                    uint32_t v[16];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            if (q * 32 + i >= sh.head_dim) break;
-                            uint4 v;
-                            v.x = pack2<T>(o[i] * inv, o[i + 1] * inv);
-                            v.y = pack2<T>(o[i + 2] * inv, o[i + 3] * inv);
-                            v.z = pack2<T>(o[i + 4] * inv, o[i + 5] * inv);
-                            v.w = pack2<T>(o[i + 6] * inv, o[i + 7] * inv);
-                            *reinterpret_cast<uint4*>(dst + q * 32 + i) = v;
-                        }
-                    }
+                    for (int i = 0; i < 16; ++i) v[i] = pack2<T>(o[2 * i] * inv, o[2 * i + 1] * inv);
+                    store_64(v, q * 32);
                 }
                 tc_fence_before();
                 continue;
@@ -769,17 +872,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         acc[i + 3] += f * v.w;
                     }
                 }
-                if (valid) {
 #pragma unroll
-                    for (int i = 0; i < 64; i += 8) {
-                        if (q + i >= sh.head_dim) break;
-                        uint4 v;
-                        v.x = pack2<T>(acc[i] * inv, acc[i + 1] * inv);
-                        v.y = pack2<T>(acc[i + 2] * inv, acc[i + 3] * inv);
-                        v.z = pack2<T>(acc[i + 4] * inv, acc[i + 5] * inv);
-                        v.w = pack2<T>(acc[i + 6] * inv, acc[i + 7] * inv);
-                        *reinterpret_cast<uint4*>(dst + q + i) = v;
-                    }
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t v[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        v[i] = pack2<T>(acc[half * 32 + 2 * i] * inv, acc[half * 32 + 2 * i + 1] * inv);
+                    store_64(v, q + half * 32);
                 }
             }
         }
@@ -811,18 +910,18 @@ static kt_status launch_tile_typed(const AttnArgs& a, cudaStream_t s) {
     p.out = a.out.ptr;
     p.o_token = a.out.token_stride;
     p.o_head = a.out.head_stride;
-    p.tokens_per_group = 128 / p.sh.group;
-    p.box_slots = a.kv.page_size & -a.kv.page_size;
-    if (p.box_slots > kTileKeys) p.box_slots = kTileKeys;
+    p.geo.tokens = 128 / p.sh.group;
+    p.geo.box_slots = a.kv.page_size & -a.kv.page_size;
+    if (p.geo.box_slots > kTileKeys) p.geo.box_slots = kTileKeys;
     CUtensorMap qmap, kmap, vmap;
     const uint64_t qd[3] = {static_cast<uint64_t>(a.kv.head_dim), static_cast<uint64_t>(a.q.heads),
                             static_cast<uint64_t>(a.batch.tokens)};
     const uint64_t qs[2] = {2 * static_cast<uint64_t>(a.q.head_stride), 2 * static_cast<uint64_t>(a.q.token_stride)};
-    const uint32_t qb[3] = {64, static_cast<uint32_t>(p.sh.group), static_cast<uint32_t>(p.tokens_per_group)};
+    const uint32_t qb[3] = {64, static_cast<uint32_t>(p.sh.group), static_cast<uint32_t>(p.geo.tokens)};
     if (!encode_tiled_map(&qmap, a.kv.dtype == KT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                           a.q.ptr, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
-        !encode_kv_map(&kmap, a.kv, false, p.box_slots) || !encode_kv_map(&vmap, a.kv, true, p.box_slots))
+        !encode_kv_map(&kmap, a.kv, false, p.geo.box_slots) || !encode_kv_map(&vmap, a.kv, true, p.geo.box_slots))
         return report(KT_ERR_CUDA, "tensor map encoding failed");
     static bool attr_set[64] = {};
     int dev = 0;
