@@ -517,7 +517,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // ------------------------------------------------ MMAs, issued by one thread
             // The run is one stream of tiles, S one tile ahead of O, across the items' ends as well.
             constexpr uint32_t kIdescQK = idesc_f16<T>(kTileKeys, false);
-            constexpr uint32_t kIdescPV = idesc_f16<T>(DP, true);
+            const int steps = (sh.head_dim + 15) / 16;   // of 16 elements: those past the head are zeros in S, unused in O
+            const uint32_t idesc_pv = idesc_f16<T>(steps * 16, true);
             struct Tile {
                 int groups;
                 bool first, last;   // of its item's tiles in this run
@@ -564,6 +565,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 const uint32_t b = sdesc_low(kv_smem + k_ring.stage * Cfg::kStageBytes);
 #pragma unroll
                 for (int ks = 0; ks < DP / 16; ++ks) {
+                    if (ks >= steps) break;
                     const uint32_t off = ((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4;
                     tc_mma_ss(kTmemS + i * 128, sdesc(a + off, 16), sdesc(b + off, 16), kIdescQK, ks > 0 ? 1u : 0u);
                 }
@@ -592,7 +594,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         tc_fence_after();
                     }
                     tc_mma_ts(kTmemO + i * DP, Cfg::kTmemP + i * Cfg::kPStep + ks * 8,
-                              sdesc(b + ((ks * 16 * 128) >> 4), kTileKeys * 128), kIdescPV,
+                              sdesc(b + ((ks * 16 * 128) >> 4), kTileKeys * 128), idesc_pv,
                               ks > 0 || !t.first ? 1u : 0u);
                 }
                 p_parity ^= 1u;
@@ -673,14 +675,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (lane == 0) mbar_arrive(smem_u32(&s_s_free[grp]));
                 }
                 uint32_t dead = 0;   // quarters that no row of the warp sees
-                if (masked) {
+                float top = m;
+                if (!masked) {
+                    top = max3(max3(max32(x[0]), max32(x[1]), max32(x[2])), max32(x[3]), m);
+                } else {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        if (__all_sync(0xffffffffu, hi < q * 32 || lo > q * 32 + 31)) dead |= 1u << q;
-                        if (__any_sync(0xffffffffu, hi < q * 32 + 31 || lo > q * 32)) mask32(x[q], lo - q * 32, hi - q * 32);
+                        if (__all_sync(0xffffffffu, hi < q * 32 || lo > q * 32 + 31)) {
+                            dead |= 1u << q;
+                        } else {
+                            if (__any_sync(0xffffffffu, hi < q * 32 + 31 || lo > q * 32))
+                                mask32(x[q], lo - q * 32, hi - q * 32);
+                            top = fmaxf(top, max32(x[q]));
+                        }
                     }
                 }
-                const float top = max3(max3(max32(x[0]), max32(x[1]), max32(x[2])), max32(x[3]), m);
                 if (Cfg::kOwnP && tile_no > 1) {   // the group's product before this one has been taken: O and P are free
                     ok = warp_wait(smem_u32(&s_o_full[grp]), (tile_no - 2) & 1u, abort_flag);
                     if (!ok) break;
