@@ -28,13 +28,12 @@ namespace kt {
 
 constexpr int kTileKeys = 128;
 constexpr int kTileThreads = 384;
-constexpr int kItemUnits = 3;         // what an item costs besides its key tiles, in key tiles
+constexpr int kItemUnits = 2;         // what an item costs besides its key tiles, in key tiles
 constexpr int kTileMinUnits = kItemUnits + 2;   // least units of a CTA's run
 constexpr int kPlanSeqs = 512;        // sequences planned at a time
 constexpr float kLazyLog2 = 8.0f;     // growth of the maximum (log2) that is let stand
 
-// Tensor memory: the CTA takes all 512 columns, so it starts at 0.  S of the groups, then O.  Heads of up to 64 leave
-// room for P of its own, so that a group's next S is computed while its weights are; else P lies in S's first half.
+// Tensor memory: the CTA takes all 512 columns, so it starts at 0.  S of the groups, P in its first half, then O.
 constexpr uint32_t kTmemS = 0, kTmemO = 256;
 
 template <int DP>
@@ -42,8 +41,6 @@ struct TileCfg {
     static constexpr int kQBytes = 128 * DP * 2;         // one row group
     static constexpr int kStageBytes = kTileKeys * DP * 2;   // one tile of K or V
     static constexpr int kStages = DP == 128 ? 5 : 9;        // odd: K and V alternate in a stage
-    static constexpr bool kOwnP = DP == 64;
-    static constexpr uint32_t kTmemP = kOwnP ? 384 : kTmemS, kPStep = kOwnP ? 64 : 128;   // P of group 0, to group 1's
     static constexpr int kQBufs = DP == 128 ? 1 : 2;
     static constexpr int kQAll = kQBufs * 2 * kQBytes;
     static constexpr int kSmem = kQAll + kStages * kStageBytes + 1024;
@@ -379,7 +376,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_kv_full[Cfg::kStages], s_kv_empty[Cfg::kStages];
     __shared__ __align__(8) uint64_t s_q_full[Cfg::kQBufs][2], s_q_empty[Cfg::kQBufs][2];
-    __shared__ __align__(8) uint64_t s_s_full[2], s_s_free[2], s_p_full[2][2], s_o_full[2], s_done;
+    __shared__ __align__(8) uint64_t s_s_full[2], s_p_full[2][2], s_o_full[2], s_done;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_last[2];
     __shared__ RunPlan s_plan;
@@ -402,9 +399,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 mbar_init(smem_u32(&s_q_full[b][i]), 1);
                 mbar_init(smem_u32(&s_q_empty[b][i]), 1);
             }
-            mbar_init(smem_u32(&s_s_free[i]), 4);   // the group's warps
             mbar_init(smem_u32(&s_s_full[i]), 1);
-            mbar_init(smem_u32(&s_p_full[i][0]), 4);
+            mbar_init(smem_u32(&s_p_full[i][0]), 4);   // the group's warps
             mbar_init(smem_u32(&s_p_full[i][1]), 4);
             mbar_init(smem_u32(&s_o_full[i]), 1);
         }
@@ -535,9 +531,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
             };
             Ring k_ring{0, 0}, v_ring{1, 0};
-            // parities of each group's next query item, weights and (kOwnP) release of S; query buffer
+            // parities of each group's next query item and weights; query buffer
             uint32_t q_parity0 = 0, q_parity1 = 0, q_buf0 = 0, q_buf1 = 0, p_parity0 = 0, p_parity1 = 0;
-            uint32_t free0 = 1, free1 = 1;   // S is free at first: the phase before the first has passed
             auto wait = [&](uint64_t& bar, uint32_t par) { return mbar_wait(smem_u32(&bar), par, abort_flag); };
             auto tile_ahead = [&](Tile& t) {   // false: no more
                 if (ahead == w.t1) {
@@ -553,13 +548,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 constexpr int i = decltype(group)::value;
                 uint32_t& q_parity = i == 0 ? q_parity0 : q_parity1;
                 uint32_t& buf = i == 0 ? q_buf0 : q_buf1;
-                uint32_t& free = i == 0 ? free0 : free1;
                 if (t.first && !wait(s_q_full[buf][i], q_parity)) return false;
                 if (i == 0 && !wait(s_kv_full[k_ring.stage], k_ring.parity)) return false;
-                if (Cfg::kOwnP) {
-                    if (!wait(s_s_free[i], free)) return false;
-                    free ^= 1u;
-                }
                 tc_fence_after();
                 const uint32_t a = sdesc_low(q_smem + (buf * 2 + i) * Cfg::kQBytes);
                 const uint32_t b = sdesc_low(kv_smem + k_ring.stage * Cfg::kStageBytes);
@@ -589,16 +579,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < kTileKeys / 16; ++ks) {
-                    if (ks == kTileKeys / 16 * 3 / 4) {
+                    if (ks == kTileKeys / 32) {
                         if (!wait(s_p_full[i][1], p_parity)) return false;
                         tc_fence_after();
                     }
-                    tc_mma_ts(kTmemO + i * DP, Cfg::kTmemP + i * Cfg::kPStep + ks * 8,
+                    tc_mma_ts(kTmemO + i * DP, kTmemS + i * 128 + ks * 8,
                               sdesc(b + ((ks * 16 * 128) >> 4), kTileKeys * 128), idesc_pv,
                               ks > 0 || !t.first ? 1u : 0u);
                 }
                 p_parity ^= 1u;
-                if (Cfg::kOwnP || t.last) tc_commit(smem_u32(&s_o_full[i]));
+                if (t.last) tc_commit(smem_u32(&s_o_full[i]));
                 if (i + 1 == t.groups) {
                     tc_commit(smem_u32(&s_kv_empty[v_ring.stage]));
                     v_ring.step();
@@ -614,13 +604,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 while (true) {
                     now = next;
                     const bool any = tile_ahead(next);
-                    if (Cfg::kOwnP && any)
-                        if (!qk(group0, next) || (next.groups > 1 && !qk(group1, next))) return false;
                     if (!pv(group0, now)) return false;
-                    if (!Cfg::kOwnP && any && !qk(group0, next)) return false;
+                    if (any && !qk(group0, next)) return false;   // P has been read in that order
                     if (now.groups > 1 && !pv(group1, now)) return false;
                     if (!any) return true;
-                    if (!Cfg::kOwnP && next.groups > 1 && !qk(group1, next)) return false;
+                    if (next.groups > 1 && !qk(group1, next)) return false;
                 }
             };
             if (!run() && !*reinterpret_cast<volatile int*>(&s_abort)) {
@@ -640,7 +628,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = kTmemS + lane_base + grp * 128;
         const uint32_t t_o = kTmemO + lane_base + grp * DP;
-        const uint32_t t_p = Cfg::kTmemP + lane_base + grp * Cfg::kPStep;
         const float c = sh.scale_log2;
         uint32_t tile_no = 0, item_no = 0, loads = 0;   // loads: key and value tiles of the items so far
         bool ok = true;
@@ -669,11 +656,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 tc_wait_ld_of(x[0]);
 #pragma unroll
                 for (int q = 1; q < 4; ++q) pin(x[q]);
-                if (Cfg::kOwnP) {   // S is in registers: the group's next one may come
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&s_s_free[grp]));
-                }
                 uint32_t dead = 0;   // quarters that no row of the warp sees
                 float top = m;
                 if (!masked) {
@@ -689,11 +671,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             top = fmaxf(top, max32(x[q]));
                         }
                     }
-                }
-                if (Cfg::kOwnP && tile_no > 1) {   // the group's product before this one has been taken: O and P are free
-                    ok = warp_wait(smem_u32(&s_o_full[grp]), (tile_no - 2) & 1u, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
                 }
                 // the reference follows the maximum only when that has outgrown it (also from -inf)
                 const bool grown = (top - m) * c > kLazyLog2;
@@ -732,7 +709,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 const float neg = m == -INFINITY ? 0.0f : -m * c;
                 const uint64_t c2 = pair(c, c), neg2 = pair(neg, neg);
                 uint64_t sum_a = 0, sum_b = 0;   // two zeros each
-                auto hand_over = [&](int part) {   // three quarters of the keys, then the rest: the product starts early
+                auto hand_over = [&](int part) {   // keys 0 to 63, then the others: the product starts with the first
                     tc_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -743,16 +720,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     for (int q = 0; q < 4; ++q) {
                         uint32_t pk[16];
                         weights32<T>(x[q], c2, neg2, pk, sum_a, sum_b);
-                        tc_st_16(t_p + q * 16, pk);
-                        if (q >= 2) hand_over(q - 2);
+                        if (q == 2) hand_over(0);   // the first half's stores have landed meanwhile
+                        tc_st_16(t_s + q * 16, pk);
+                        if (q == 3) hand_over(1);
                     }
                 } else {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         uint32_t pk[16] = {};
                         if (!(dead >> q & 1u)) weights32<T>(x[q], c2, neg2, pk, sum_a, sum_b);
-                        tc_st_16(t_p + q * 16, pk);
-                        if (q >= 2) hand_over(q - 2);
+                        if (q == 2) hand_over(0);
+                        tc_st_16(t_s + q * 16, pk);
+                        if (q == 3) hand_over(1);
                     }
                 }
                 float s0, s1;
@@ -761,7 +740,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             if (!ok) break;
             loads += 2 * static_cast<uint32_t>(w.t1 - w.t0);
-            ok = warp_wait(smem_u32(&s_o_full[grp]), (Cfg::kOwnP ? tile_no - 1 : item_no) & 1u, abort_flag);
+            ok = warp_wait(smem_u32(&s_o_full[grp]), item_no & 1u, abort_flag);
             if (!ok) break;
             ++item_no;
             tc_fence_after();
