@@ -747,24 +747,27 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
             // ---- the item's piece is complete: store it, or leave it for the join
             const bool whole = w.t0 == 0 && w.t1 == w.it.tiles;
-            const int head = w.h * sh.group + row % sh.group;
-            T* dst = static_cast<T*>(p.out) + static_cast<long long>(w.sq.first_token + tok) * p.o_token +
-                     static_cast<long long>(head) * p.o_head;
-            auto closing = [&](float mt, float lt, float& scale_o) {   // 1 / sum, the sink's share included
-                scale_o = 1.0f;
-                if (sh.sinks != nullptr && valid) {
-                    const float sk = sh.sinks[head] * kLog2e;
+            const int rows = min(tpg, w.sq.q_len - (w.rt * 2 + grp) * tpg) * sh.group;   // of the group, that hold tokens
+            auto head_of = [&](int r) { return w.h * sh.group + r % sh.group; };
+            auto row_ptr = [&](int r) {
+                const int t = w.sq.first_token + (w.rt * 2 + grp) * tpg + r / sh.group;
+                return reinterpret_cast<uint64_t>(static_cast<T*>(p.out) + static_cast<long long>(t) * p.o_token +
+                                                  static_cast<long long>(head_of(r)) * p.o_head);
+            };
+            auto closing = [&](int head_of, float mt, float lt) {   // 1 / sum, the sink's share included
+                float scale_o = 1.0f;
+                if (sh.sinks != nullptr) {
+                    const float sk = sh.sinks[head_of] * kLog2e;
                     const float mc = mt == -INFINITY ? -INFINITY : mt * c;
                     const float t = fmaxf(mc, sk);
                     const float tb = t == -INFINITY ? 0.0f : t;
                     scale_o = ex2(mc - tb);
                     lt = lt * scale_o + ex2(sk - tb);
                 }
-                scale_o = lt == 0.0f ? 0.0f : scale_o / lt;
+                return lt == 0.0f ? 0.0f : scale_o / lt;
             };
             // A row's 64 bytes lie with one lane; four lanes exchange 16-byte pieces so that they write a row at a time.
-            const uint64_t to = valid ? reinterpret_cast<uint64_t>(dst) : 0;   // 0: not stored
-            auto store_64 = [&](uint32_t(&v)[16], int d) {   // elements [d, d + 32) of the row
+            auto store_64 = [&](uint32_t(&v)[16], int d, uint64_t to) {   // elements [d, d + 32) of the row `to` (0: none)
                 const bool odd = lane & 1, upper = lane & 2;
 #pragma unroll
                 for (int i = 0; i < 16; i += 8)
@@ -789,8 +792,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
             };
             if (whole) {
-                float inv;
-                closing(m, l, inv);
+                const float inv = closing(head_of(row), m, l);
+                const uint64_t to = row < rows ? row_ptr(row) : 0;
 #pragma unroll 1
                 for (int q = 0; q < DP / 32; ++q) {
                     float o[32];
@@ -799,7 +802,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     uint32_t v[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = pack2<T>(o[2 * i] * inv, o[2 * i + 1] * inv);
-                    store_64(v, q * 32);
+                    store_64(v, q * 32, to);
                 }
                 tc_fence_before();
                 continue;
@@ -815,59 +818,64 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 tc_ld_f32(t_o + q * 32, o);
                 tc_wait_ld_of(o);
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
+                for (int i = 0; i < 32 && row < rows; i += 4)
                     p.part_o[(slot * (DP / 4) + (q * 32 + i) / 4) * 256 + prow] =
-                        make_float4(o[i], o[i + 1], o[i + 2],
-                                    o[i + 3]);
+                        make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
             }
             tc_fence_before();
-            p.part_ml[slot * 256 + prow] = make_float2(m, l);
-            __threadfence();
+            if (row < rows) p.part_ml[slot * 256 + prow] = make_float2(m, l);
             asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory");
             if (row == 0) {
+                __threadfence();
                 const unsigned seen = atomicAdd(&p.counters[2 * c0 + grp], 1u);
                 s_last[grp] = seen == static_cast<unsigned>(c1 - c0);
                 if (s_last[grp]) p.counters[2 * c0 + grp] = 0;
+                __threadfence();
             }
             asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory");
             if (!s_last[grp]) continue;
-            __threadfence();
-            float mt = -INFINITY;
-            for (int k = c0; k <= c1; ++k)
-                mt = fmaxf(mt, __ldcg(&p.part_ml[(2 * static_cast<size_t>(k) + (k == c0 ? 1 : 0)) * 256 + prow]).x);
+            // The join's time is that of its loads: few rows are shared out among all threads of the group, a part of
+            // the head each, and eight loads of each of four pieces are under way.
+            const int span = rows > 64 ? 128 : rows > 32 ? 64 : 32;   // rows to a part
+            const int width = DP * span / 128 > 32 ? DP * span / 128 : 32;
+            const int jrow = row % span, d0 = row / span * width;
+            const bool joins = jrow < rows && d0 < DP;
+            const uint64_t to = joins ? row_ptr(jrow) : 0;
+            auto slot_of = [&](int k) { return 2 * static_cast<size_t>(c0 + k) + (k == 0 ? 1 : 0); };
+            const int pieces = c1 - c0 + 1, jp = grp * 128 + (joins ? jrow : 0);
+            float mt = -INFINITY, lt = 0.0f;
+#pragma unroll 8
+            for (int k = 0; k < pieces; ++k) mt = fmaxf(mt, __ldcg(&p.part_ml[slot_of(k) * 256 + jp]).x);
             const float mref = mt == -INFINITY ? 0.0f : mt;
-            float lt = 0.0f;
-            for (int k = c0; k <= c1; ++k) {
-                const float2 ml = __ldcg(&p.part_ml[(2 * static_cast<size_t>(k) + (k == c0 ? 1 : 0)) * 256 + prow]);
+#pragma unroll 8
+            for (int k = 0; k < pieces; ++k) {
+                const float2 ml = __ldcg(&p.part_ml[slot_of(k) * 256 + jp]);
                 lt += ml.y * ex2((ml.x - mref) * c);
             }
-            float inv;
-            closing(mt, lt, inv);
+            const float inv = closing(head_of(joins ? jrow : 0), mt, lt);
 #pragma unroll 1
-            for (int q = 0; q < DP; q += 64) {   // 16 loads under way for each piece
-                float acc[64];
+            for (int q = 0; q < width; q += 32) {
+                float acc[32];
 #pragma unroll
-                for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
-                for (int k = c0; k <= c1; ++k) {
-                    const size_t sl = 2 * static_cast<size_t>(k) + (k == c0 ? 1 : 0);
-                    const float f = ex2((__ldcg(&p.part_ml[sl * 256 + prow]).x - mref) * c);
+                for (int i = 0; i < 32; ++i) acc[i] = 0.0f;
+                if (joins) {
+#pragma unroll 4
+                    for (int k = 0; k < pieces; ++k) {
+                        const float f = ex2((__ldcg(&p.part_ml[slot_of(k) * 256 + jp]).x - mref) * c);
 #pragma unroll
-                    for (int i = 0; i < 64; i += 4) {
-                        const float4 v = __ldcg(&p.part_o[(sl * (DP / 4) + (q + i) / 4) * 256 + prow]);
-                        acc[i] += f * v.x;
-                        acc[i + 1] += f * v.y;
-                        acc[i + 2] += f * v.z;
-                        acc[i + 3] += f * v.w;
+                        for (int i = 0; i < 32; i += 4) {
+                            const float4 v = __ldcg(&p.part_o[(slot_of(k) * (DP / 4) + (d0 + q + i) / 4) * 256 + jp]);
+                            acc[i] += f * v.x;
+                            acc[i + 1] += f * v.y;
+                            acc[i + 2] += f * v.z;
+                            acc[i + 3] += f * v.w;
+                        }
                     }
                 }
+                uint32_t v[16];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t v[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        v[i] = pack2<T>(acc[half * 32 + 2 * i] * inv, acc[half * 32 + 2 * i + 1] * inv);
-                    store_64(v, q + half * 32);
-                }
+                for (int i = 0; i < 16; ++i) v[i] = pack2<T>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+                store_64(v, d0 + q, to);
             }
         }
         if (!ok && !*reinterpret_cast<volatile int*>(&s_abort)) {
