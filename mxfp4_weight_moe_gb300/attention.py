@@ -347,6 +347,8 @@ class PagedKV:
             _written(out, "out")
         if workspace is None:
             workspace = self._workspace(stream)
+        elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous uint8 on {self.device}")
         b = _buffer
         _ATTEND_CALL.pack_into(b.buf, 0, *batch, *hq, *_heads(out, "out", dt, dim, dev, n, heads))
         at = b.at + _BATCH_BYTES

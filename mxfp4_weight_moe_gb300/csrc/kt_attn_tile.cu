@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_kv_full[Cfg::kStages], s_kv_empty[Cfg::kStages];
     __shared__ __align__(8) uint64_t s_q_full[Cfg::kQBufs][2], s_q_empty[Cfg::kQBufs][2];
-    __shared__ __align__(8) uint64_t s_s_full[2], s_p_full[2][2], s_o_full[2], s_done;
+    __shared__ __align__(8) uint64_t s_s_full[2], s_p_full[2][2], s_o_full[2], s_sync[2], s_done;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_last[2];
     __shared__ RunPlan s_plan;
@@ -403,6 +403,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_init(smem_u32(&s_p_full[i][0]), 4);   // the group's warps
             mbar_init(smem_u32(&s_p_full[i][1]), 4);
             mbar_init(smem_u32(&s_o_full[i]), 1);
+            mbar_init(smem_u32(&s_sync[i]), 4);
         }
         mbar_init(smem_u32(&s_done), 1);
         fence_mbar_init();
@@ -629,6 +630,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t t_s = kTmemS + lane_base + grp * 128;
         const uint32_t t_o = kTmemO + lane_base + grp * DP;
         const float c = sh.scale_log2;
+        uint32_t sync_no = 0;
+        auto group_sync = [&]() {   // the group's four warps; bounded, as every wait here
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s_sync[grp]));
+            return warp_wait(smem_u32(&s_sync[grp]), sync_no++ & 1u, abort_flag);
+        };
         uint32_t tile_no = 0, item_no = 0, loads = 0;   // loads: key and value tiles of the items so far
         bool ok = true;
         TileWalk w;
@@ -824,7 +831,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             tc_fence_before();
             if (row < rows) p.part_ml[slot * 256 + prow] = make_float2(m, l);
-            asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory");
+            if (!(ok = group_sync())) break;
             if (row == 0) {
                 __threadfence();
                 const unsigned seen = atomicAdd(&p.counters[2 * c0 + grp], 1u);
@@ -832,7 +839,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (s_last[grp]) p.counters[2 * c0 + grp] = 0;
                 __threadfence();
             }
-            asm volatile("bar.sync %0, 128;" ::"r"(grp + 1) : "memory");
+            if (!(ok = group_sync())) break;
             if (!s_last[grp]) continue;
             // The join's time is that of its loads: few rows are shared out among all threads of the group, a part of
             // the head each, and eight loads of each of four pieces are under way.

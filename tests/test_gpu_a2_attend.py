@@ -1,5 +1,6 @@
 """Attention over a paged cache against the 64-bit statement: head layouts, lengths, masks, pages, streams."""
 import math
+import random
 
 import pytest
 import torch
@@ -61,6 +62,72 @@ def test_pages(dtype, page, layout):
 ])
 def test_chunks(dtype, q_lens, past, hq, hk, d, page):
     _run(q_lens, past, hq, hk, d, dtype, page=page)
+
+
+@pytest.mark.parametrize("d", [8, 16, 24, 40, 56, 72, 104, 120])
+def test_chunks_of_other_head_sizes(d):
+    _run([45, 3], [30, 100], 9, 3, d, torch.float16, page=16)
+
+
+def test_expanded_queries():
+    """Queries of stride zero (one head for all, one token for all)."""
+    n, d = 40, 64
+    kp, vp, table = R.paged([n + 9], 16, 1, d, torch.bfloat16, DEV, 5)
+    one_head = _rand(n, 1, d, dtype=torch.bfloat16, seed=1).expand(n, 4, d)
+    one_token = _rand(1, 4, d, dtype=torch.bfloat16, seed=2).expand(n, 4, d)
+    for q in (one_head, one_token):
+        out = kt.PagedKV(kp, vp).attend(q, table, R.starts([n], DEV),
+                                        torch.tensor([n + 9], dtype=torch.int32, device=DEV), n)
+        want, bound = R.attend(q, kp, vp, table, [n], [n + 9], R.softmax_scale(d))
+        assert bool(((out.double().cpu() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_drawn_batches(seed):
+    """Batches of mixed lengths, pages, heads, windows and sinks."""
+    r = random.Random(seed)
+    seqs = r.choice((1, 2, 5, 9))
+    q_lens = [r.choice((0, 1, 1, r.randint(1, 20), r.randint(1, 90))) for _ in range(seqs)]
+    q_lens[0] = max(q_lens[0], 1)
+    past = [r.choice((0, r.randint(0, 40), r.randint(0, 300))) for _ in range(seqs)]
+    hk = r.choice((1, 2, 3))
+    hq = hk * r.choice((1, 2, 5, 8))
+    sinks = torch.randn(hq, generator=torch.Generator().manual_seed(seed)).to(DEV) if r.random() < 0.5 else None
+    _run(q_lens, past, hq, hk, r.choice((32, 64, 80, 128)), r.choice((torch.bfloat16, torch.float16)),
+         page=r.choice((16, 32, 80, 128)), layout=r.choice(("slots", "heads", "pairs")),
+         window=r.choice((0, 0, r.randint(1, 200))), sinks=sinks, seed=seed, max_q=r.choice((1, max(q_lens))))
+
+
+def test_many_sequences_of_chunks():
+    g = torch.Generator().manual_seed(2)
+    b = 600
+    past = torch.randint(0, 50, (b,), generator=g).tolist()
+    q_lens = torch.randint(0, 4, (b,), generator=g).tolist()
+    _run(q_lens, past, 2, 1, 32, torch.float16, max_q=100)
+
+
+@pytest.mark.parametrize("new", [1, 70])
+def test_calls_that_share_a_workspace(new):
+    """Consecutive calls of different sizes on one workspace, each as if alone; a short workspace is refused."""
+    d, page = 64, 16
+    cases = []
+    for length in (5000, 90, 2000):
+        pages = -(-(length + new) // page)
+        kp, vp = (_rand(pages, page, 1, d, dtype=torch.bfloat16, seed=length + i) for i in (0, 1))
+        table = torch.arange(pages, dtype=torch.int32, device=DEV)[None]
+        args = (_rand(new, 4, d, dtype=torch.bfloat16, seed=7), table, R.starts([new], DEV),
+                torch.tensor([length + new], dtype=torch.int32, device=DEV), new)
+        c = kt.PagedKV(kp, vp)
+        cases.append((c, args, c.attend(*args)))
+    ws = cases[0][0].workspace()
+    outs = [c.attend(*args, workspace=ws) for c, args, _ in cases for _ in range(2)]
+    for i, (_, _, want) in enumerate(cases):
+        assert torch.equal(outs[2 * i], want) and torch.equal(outs[2 * i + 1], want)
+    assert not bool(ws[:A.WORKSPACE_ZEROED].any())
+    with pytest.raises(kt.KTError, match="workspace"):
+        cases[0][0].attend(*cases[0][1], workspace=ws[:4096])
+    with pytest.raises((TypeError, ValueError)):
+        cases[0][0].attend(*cases[0][1], workspace=ws.view(torch.int32))
 
 
 @pytest.mark.parametrize("window", [1, 2, 16, 60, 64, 129, 10_000])
