@@ -630,6 +630,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t t_s = kTmemS + lane_base + grp * 128;
         const uint32_t t_o = kTmemO + lane_base + grp * DP;
         const float c = sh.scale_log2;
+        const int row_tok = row / sh.group, row_head = row - row_tok * sh.group;   // the row's token and head in its group
+        const long long row_off = row_tok * p.o_token + row_head * p.o_head;
         uint32_t sync_no = 0;
         auto group_sync = [&]() {   // the group's four warps; bounded, as every wait here
             __syncwarp();
@@ -641,12 +643,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         TileWalk w;
         for (bool more = w.start(sh, p.geo, plan); more && ok; more = w.next(sh, p.geo)) {
             if (grp >= w.groups(tpg)) continue;
-            const int tok = (w.rt * 2 + grp) * tpg + row / sh.group;
-            const bool valid = row / sh.group < tpg && tok < w.sq.q_len;
+            const int tok0 = (w.rt * 2 + grp) * tpg, tok = tok0 + row_tok;
+            const bool valid = row_tok < tpg && tok < w.sq.q_len;
             const int pos = w.sq.first_pos + tok;
-            // keys [first, last] are seen; rows of no token compute without masks and are not stored
+            // keys [first, last] are seen, and what all or some rows of the warp see; rows of no token compute without
+            // masks and are not stored
             const int last = valid ? min(pos, w.sq.keys - 1) : 0x7fffffff;
             const int first = valid ? window_start(pos, sh.window) : 0;
+            const int last_all = __reduce_min_sync(0xffffffffu, last), first_all = __reduce_max_sync(0xffffffffu, first);
+            const int last_any = __reduce_max_sync(0xffffffffu, valid ? last : -1);
+            const int first_any = __reduce_min_sync(0xffffffffu, valid ? first : 0x7fffffff);
             const int rag = ragged_tile(w, p.geo.box_slots);
             float m = -INFINITY, l = 0.0f;
             for (int j = w.t0; j < w.t1; ++j) {
@@ -655,7 +661,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if (!ok) break;
                 ++tile_no;
                 tc_fence_after();
-                const bool masked = __any_sync(0xffffffffu, last < key0 + kTileKeys - 1 || first > key0);
+                const bool masked = last_all < key0 + kTileKeys - 1 || first_all > key0;
                 const int hi = last - key0, lo = first - key0;
                 float x[4][32];
 #pragma unroll
@@ -670,11 +676,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 } else {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        if (__all_sync(0xffffffffu, hi < q * 32 || lo > q * 32 + 31)) {
+                        const int k0 = key0 + q * 32;
+                        if (last_any < k0 || first_any > k0 + 31) {
                             dead |= 1u << q;
                         } else {
-                            if (__any_sync(0xffffffffu, hi < q * 32 + 31 || lo > q * 32))
-                                mask32(x[q], lo - q * 32, hi - q * 32);
+                            if (last_all < k0 + 31 || first_all > k0) mask32(x[q], lo - q * 32, hi - q * 32);
                             top = fmaxf(top, max32(x[q]));
                         }
                     }
@@ -754,17 +760,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
             // ---- the item's piece is complete: store it, or leave it for the join
             const bool whole = w.t0 == 0 && w.t1 == w.it.tiles;
-            const int rows = min(tpg, w.sq.q_len - (w.rt * 2 + grp) * tpg) * sh.group;   // of the group, that hold tokens
-            auto head_of = [&](int r) { return w.h * sh.group + r % sh.group; };
-            auto row_ptr = [&](int r) {
-                const int t = w.sq.first_token + (w.rt * 2 + grp) * tpg + r / sh.group;
-                return reinterpret_cast<uint64_t>(static_cast<T*>(p.out) + static_cast<long long>(t) * p.o_token +
-                                                  static_cast<long long>(head_of(r)) * p.o_head);
-            };
-            auto closing = [&](int head_of, float mt, float lt) {   // 1 / sum, the sink's share included
+            const int rows = min(tpg, w.sq.q_len - tok0) * sh.group;   // of the group, that hold tokens
+            T* const out0 = static_cast<T*>(p.out) + static_cast<long long>(w.sq.first_token + tok0) * p.o_token +
+                            static_cast<long long>(w.h * sh.group) * p.o_head;   // of the group's first row
+            auto closing = [&](int head, float mt, float lt) {   // 1 / sum, the sink's share included
                 float scale_o = 1.0f;
                 if (sh.sinks != nullptr) {
-                    const float sk = sh.sinks[head_of] * kLog2e;
+                    const float sk = sh.sinks[w.h * sh.group + head] * kLog2e;
                     const float mc = mt == -INFINITY ? -INFINITY : mt * c;
                     const float t = fmaxf(mc, sk);
                     const float tb = t == -INFINITY ? 0.0f : t;
@@ -774,7 +776,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 return lt == 0.0f ? 0.0f : scale_o / lt;
             };
             // A row's 64 bytes lie with one lane; four lanes exchange 16-byte pieces so that they write a row at a time.
-            auto store_64 = [&](uint32_t(&v)[16], int d, uint64_t to) {   // elements [d, d + 32) of the row `to` (0: none)
+            T* four[4];   // the rows of the lane's four (null: not stored), given its own
+            auto meet = [&](T* own) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    four[k] = reinterpret_cast<T*>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(own), (lane & ~3) + k));
+            };
+            auto store_64 = [&](uint32_t(&v)[16], int d) {   // elements [d, d + 32) of the rows
                 const bool odd = lane & 1, upper = lane & 2;
 #pragma unroll
                 for (int i = 0; i < 16; i += 8)
@@ -792,15 +801,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 const int at = d + (lane & 3) * 8;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {   // row k of the four
-                    T* row_k = reinterpret_cast<T*>(__shfl_sync(0xffffffffu, to, (lane & ~3) + k));
-                    if (row_k != nullptr && at < sh.head_dim)
-                        *reinterpret_cast<uint4*>(row_k + at) = make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-                }
+                for (int k = 0; k < 4; ++k)   // row k of the four
+                    if (four[k] != nullptr && at < sh.head_dim)
+                        *reinterpret_cast<uint4*>(four[k] + at) =
+                            make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             };
             if (whole) {
-                const float inv = closing(head_of(row), m, l);
-                const uint64_t to = row < rows ? row_ptr(row) : 0;
+                const float inv = closing(row_head, m, l);
+                meet(row < rows ? out0 + row_off : nullptr);
 #pragma unroll 1
                 for (int q = 0; q < DP / 32; ++q) {
                     float o[32];
@@ -809,7 +817,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     uint32_t v[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = pack2<T>(o[2 * i] * inv, o[2 * i + 1] * inv);
-                    store_64(v, q * 32, to);
+                    store_64(v, q * 32);
                 }
                 tc_fence_before();
                 continue;
@@ -847,7 +855,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int width = DP * span / 128 > 32 ? DP * span / 128 : 32;
             const int jrow = row % span, d0 = row / span * width;
             const bool joins = jrow < rows && d0 < DP;
-            const uint64_t to = joins ? row_ptr(jrow) : 0;
+            const int jtok = joins ? jrow / sh.group : 0, jhead = joins ? jrow - jtok * sh.group : 0;
+            meet(joins ? out0 + jtok * p.o_token + jhead * p.o_head : nullptr);
             auto slot_of = [&](int k) { return 2 * static_cast<size_t>(c0 + k) + (k == 0 ? 1 : 0); };
             const int pieces = c1 - c0 + 1, jp = grp * 128 + (joins ? jrow : 0);
             float mt = -INFINITY, lt = 0.0f;
@@ -859,7 +868,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 const float2 ml = __ldcg(&p.part_ml[slot_of(k) * 256 + jp]);
                 lt += ml.y * ex2((ml.x - mref) * c);
             }
-            const float inv = closing(head_of(joins ? jrow : 0), mt, lt);
+            const float inv = closing(jhead, mt, lt);
 #pragma unroll 1
             for (int q = 0; q < width; q += 32) {
                 float acc[32];
@@ -882,7 +891,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 uint32_t v[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = pack2<T>(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-                store_64(v, d0 + q, to);
+                store_64(v, d0 + q);
             }
         }
         if (!ok && !*reinterpret_cast<volatile int*>(&s_abort)) {
