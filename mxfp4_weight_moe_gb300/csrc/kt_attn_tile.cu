@@ -599,17 +599,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             auto run = [&]() -> bool {
                 const std::integral_constant<int, 0> group0{};
                 const std::integral_constant<int, 1> group1{};
-                Tile now, next;
-                if (!tile_ahead(next)) return true;
-                if (!qk(group0, next) || (next.groups > 1 && !qk(group1, next))) return false;
+                Tile now{0, false, false}, next;   // (no groups before the first)
                 while (true) {
-                    now = next;
                     const bool any = tile_ahead(next);
-                    if (!pv(group0, now)) return false;
+                    if (now.groups > 0 && !pv(group0, now)) return false;
                     if (any && !qk(group0, next)) return false;   // P has been read in that order
                     if (now.groups > 1 && !pv(group1, now)) return false;
                     if (!any) return true;
                     if (next.groups > 1 && !qk(group1, next)) return false;
+                    now = next;
                 }
             };
             if (!run() && !*reinterpret_cast<volatile int*>(&s_abort)) {
@@ -663,31 +661,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 tc_fence_after();
                 const bool masked = last_all < key0 + kTileKeys - 1 || first_all > key0;
                 const int hi = last - key0, lo = first - key0;
-                float x[4][32];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tc_ld_f32(t_s + q * 32, x[q]);
-                tc_wait_ld_of(x[0]);
-#pragma unroll
-                for (int q = 1; q < 4; ++q) pin(x[q]);
-                uint32_t dead = 0;   // quarters that no row of the warp sees
-                float top = m;
-                if (!masked) {
-                    top = max3(max3(max32(x[0]), max32(x[1]), max32(x[2])), max32(x[3]), m);
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int k0 = key0 + q * 32;
-                        if (last_any < k0 || first_any > k0 + 31) {
-                            dead |= 1u << q;
-                        } else {
-                            if (last_all < k0 + 31 || first_all > k0) mask32(x[q], lo - q * 32, hi - q * 32);
-                            top = fmaxf(top, max32(x[q]));
-                        }
-                    }
-                }
                 // the reference follows the maximum only when that has outgrown it (also from -inf)
-                const bool grown = (top - m) * c > kLazyLog2;
-                if (__any_sync(0xffffffffu, grown)) {
+                auto follow = [&](float top) {
+                    const bool grown = (top - m) * c > kLazyLog2;
+                    if (!__any_sync(0xffffffffu, grown)) return;
                     const float f = grown ? ex2((m - top) * c) : 1.0f;
                     if (grown) m = top;
                     l *= f;
@@ -702,7 +679,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                             tc_st_16(t_o + q * 16, reinterpret_cast<const uint32_t(&)[16]>(o));
                         }
                     }
-                }
+                };
+                auto hand_over = [&](int part) {   // keys 0 to 63, then the others: the product starts with the first
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&s_p_full[grp][part]));
+                };
                 if (grp == 0 && j == rag) {
                     // Values past the sequence's end are whatever the page holds, and 0 x NaN is NaN: zeros, before
                     // this group lets the tile be multiplied (group 1's product is issued after it).
@@ -719,16 +702,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     }
                     fence_proxy_async_smem();
                 }
-                const float neg = m == -INFINITY ? 0.0f : -m * c;
-                const uint64_t c2 = pair(c, c), neg2 = pair(neg, neg);
                 uint64_t sum_a = 0, sum_b = 0;   // two zeros each
-                auto hand_over = [&](int part) {   // keys 0 to 63, then the others: the product starts with the first
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&s_p_full[grp][part]));
-                };
-                if (dead == 0) {
+                const uint64_t c2 = pair(c, c);
+                if (!masked) {
+                    float x[4][32];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tc_ld_f32(t_s + q * 32, x[q]);
+                    tc_wait_ld_of(x[0]);
+#pragma unroll
+                    for (int q = 1; q < 4; ++q) pin(x[q]);
+                    follow(max3(max3(max32(x[0]), max32(x[1]), max32(x[2])), max32(x[3]), m));
+                    const float neg = m == -INFINITY ? 0.0f : -m * c;
+                    const uint64_t neg2 = pair(neg, neg);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         uint32_t pk[16];
@@ -738,13 +723,38 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         if (q == 3) hand_over(1);
                     }
                 } else {
-#pragma unroll
+                    // The same by quarters, each read twice: what no row of the warp sees is skipped.  One copy of the
+                    // code for the four, for a window's or a short prompt's tiles are all of this kind and straight
+                    // code for them would not stay in the instruction cache.  (P of quarter q lies in S's columns of
+                    // quarter q / 2, which have been read by then.)
+                    auto dead = [&](int q) { return last_any < key0 + q * 32 || first_any > key0 + q * 32 + 31; };
+                    auto load = [&](int q, float(&x)[32]) {
+                        tc_ld_f32(t_s + q * 32, x);
+                        tc_wait_ld_of(x);
+                        if (last_all < key0 + q * 32 + 31 || first_all > key0 + q * 32)
+                            mask32(x, lo - q * 32, hi - q * 32);
+                    };
+                    float top = m;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        if (dead(q)) continue;
+                        float x[32];
+                        load(q, x);
+                        top = fmaxf(top, max32(x));
+                    }
+                    follow(top);
+                    const float neg = m == -INFINITY ? 0.0f : -m * c;
+                    const uint64_t neg2 = pair(neg, neg);
+#pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         uint32_t pk[16] = {};
-                        if (!(dead >> q & 1u)) weights32<T>(x[q], c2, neg2, pk, sum_a, sum_b);
-                        if (q == 2) hand_over(0);
+                        if (!dead(q)) {
+                            float x[32];
+                            load(q, x);
+                            weights32<T>(x, c2, neg2, pk, sum_a, sum_b);
+                        }
                         tc_st_16(t_s + q * 16, pk);
-                        if (q == 3) hand_over(1);
+                        if (q & 1) hand_over(q >> 1);
                     }
                 }
                 float s0, s1;
