@@ -3,13 +3,28 @@
 //
 // An item is (sequence, cache head, 16 query rows): row r of a sequence is its
 // new token r / group under query head r % group of the cache head's group, so
-// the heads that share a cache head share its loads.  The keys an item sees are
-// cut into units of 64 keys; all items' units form one line that is dealt to
-// the CTAs in equal contiguous runs, so that one long sequence and many short
-// ones keep the GPU equally busy.  An item inside one run is finished by its
-// CTA; one that is cut leaves partial sums (maximum, sum, unnormalised output)
-// in the workspace, and the CTA that finishes last joins them in order, so the
-// result does not depend on which one that was.
+// the heads that share a cache head share its loads.  A warp takes blocks of 16
+// keys (32 for heads of up to 64: the same bytes), through a ring of TMA loads
+// of its own: no barrier among warps until the item's end.  S = Q K^T and P V
+// are mma.sync products of 16 rows: the operator is bound by reading the cache
+// (16 flops a byte for 8 heads a cache head), which they keep up with, and their
+// latency is a warp's, where a tensor-memory tile's would be a CTA's.  P is
+// rounded to the element type for the product with V; the sum that divides the
+// result is of the unrounded weights.
+//
+// Few items are cut into pieces that each have a CTA of their own; many lie on a
+// line that is cut into equal runs, so that one long sequence and many short ones
+// keep the GPU equally busy.  A cut item leaves partial sums (maximum, sum,
+// unnormalised output) in the workspace, and the CTA that finishes last joins
+// them in order, so the result does not depend on which one that was.
+//
+// Measured on GB300 (bf16): 64 single tokens after up to 8191, 64 / 8 heads of
+// 128 (1.31 GB of cache), 211 us, 6.23 TB/s (92 % of the measured copy rate); 4
+// after up to 131071, heads of 64 (0.59 GB), 109 us, 5.39 TB/s, of which about 10
+// us are the launch, the plan and the join.  One token after 500 keys: 10 us, of
+// which 0.5 launch, 1.7 plan, 1.7 first look-ups and loads, 2 the keys, 3.5 the
+// pieces' join; after 60 (no join) 6 us.  L2 promotion past a head's row (256
+// bytes for rows of 128) read 1.39 times the cache.
 #include <algorithm>
 #include <type_traits>
 

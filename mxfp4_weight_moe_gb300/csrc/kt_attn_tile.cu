@@ -12,13 +12,32 @@
 // work on the other's products.  m is the running maximum as of its last change;
 // it follows the true maximum only when that has grown by more than 2^8, so the
 // rescaling of O (by the row's own thread) is rare, and the sums stay exact in
-// fp32 (P up to 2^8 rounds with the same relative error).
+// fp32 (P up to 2^8 rounds with the same relative error, and fp16 holds it).
+// P is rounded to the element type because the tensor cores multiply it with V
+// in that type; the sum that divides O is of the unrounded weights.
 //
-// Work is dealt as in the split kernel: all items' key tiles form one line, cut
-// into equal runs; the last CTA of a cut item joins its partial sums in order.
+// Work is dealt to one CTA per SM: all items' key tiles (and two more each, what
+// an item costs besides: 1 to 5 measured, 2 fastest) form one line that is cut
+// into equal runs, so causal items of any length keep the SMs equally busy; a
+// cut item leaves partial sums in the workspace and the CTA that finishes it
+// last joins them in order, so the result does not depend on which that was.
 //
-// Warps: 0-3 softmax of group 0, 4-7 of group 1, 8 issues the MMAs, 9 to 11 the TMA loads of
-// keys, values and queries.
+// Warps: 0-3 softmax of group 0, 4-7 of group 1, 8 issues the MMAs, 9 to 11 the
+// TMA loads of keys, values and queries.
+//
+// Bound: for heads of 128 the tensor cores (2630 of 3000 cycles of a tile pair),
+// for smaller heads the softmax (128 exponentials a row and tile: 1370 cycles of
+// issue and exponential unit for the two warps of a scheduler, measured alone).
+// Measured on GB300 (bf16): an 8192-token prompt, 64 / 8 heads of 128, 670 us,
+// 1640 TFLOP/s (85 % of the measured burst matmul rate, 96 % of the sustained
+// one); heads of 64, 600 us, 916 TFLOP/s; 2048 tokens after 30001 on 16-slot
+// pages (fp16, 32 / 8 heads of 128) 683 us, 1525 TFLOP/s.
+//
+// Tried and left out (8192-token prompt): P beside S so that the next S comes
+// early (heads of 64: 636 against 614 us, both groups then contend for the
+// exponential unit); the maximum of the second half under the first half's
+// weights (738 against 677 us, registers spill); 224 registers for the softmax
+// warps (694 against 674 us); the weights handed over at once (705 against 674).
 #include <algorithm>
 #include <type_traits>
 
@@ -714,14 +733,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     follow(max3(max3(max32(x[0]), max32(x[1]), max32(x[2])), max32(x[3]), m));
                     const float neg = m == -INFINITY ? 0.0f : -m * c;
                     const uint64_t neg2 = pair(neg, neg);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t pk[16];
-                        weights32<T>(x[q], c2, neg2, pk, sum_a, sum_b);
-                        if (q == 2) hand_over(0);   // the first half's stores have landed meanwhile
-                        tc_st_16(t_s + q * 16, pk);
-                        if (q == 3) hand_over(1);
-                    }
+                    uint32_t pa[16], pb[16];
+                    weights32<T>(x[0], c2, neg2, pa, sum_a, sum_b);
+                    tc_st_16(t_s, pa);
+                    weights32<T>(x[1], c2, neg2, pb, sum_a, sum_b);
+                    tc_st_16(t_s + 16, pb);
+                    weights32<T>(x[2], c2, neg2, pa, sum_a, sum_b);
+                    weights32<T>(x[3], c2, neg2, pb, sum_a, sum_b);
+                    hand_over(0);   // the first half's stores have landed meanwhile: no wait among the weights
+                    tc_st_16(t_s + 32, pa);
+                    tc_st_16(t_s + 48, pb);
+                    hand_over(1);
                 } else {
                     // The same by quarters, each read twice: what no row of the warp sees is skipped.  One copy of the
                     // code for the four, for a window's or a short prompt's tiles are all of this kind and straight
