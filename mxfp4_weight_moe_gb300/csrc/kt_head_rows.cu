@@ -145,7 +145,8 @@ __device__ __forceinline__ TokenPlace place_of(const HeadRowsParams& p, int toke
 }
 
 // Four heads a group and six blocks of 128 threads on an SM: measured on 8192 tokens of 64 + 8 heads of 128 (302 MB of
-// rows) with norms, 54.1 us, 5.66 TB/s; two heads 58 to 62 us, fewer blocks 57.6 us, without norms 6.45 TB/s.
+// rows) with norms, 54.1 us (49.4 us, 6.2 TB/s, with the rows marked to leave L2); two heads 58 to 62 us, three 56.3, six
+// 56.7, fewer blocks 57.6.
 constexpr int kRowThreads = 128, kRowBlocks = 6, kRowHeads = 4;
 constexpr int kNoNorm = 0, kWeightsTyped = 1, kWeightsF32 = 2;
 
@@ -161,7 +162,7 @@ constexpr int kNoNorm = 0, kWeightsTyped = 1, kWeightsF32 = 2;
 // A group of lanes takes R consecutive heads of one token and one of q, k, v:
 // it issues the 2R loads at once, before it looks up the position and the page,
 // and reads the cosines and the weights once for the R heads.
-template <typename T, int VEC, int R, int NORM>
+template <typename T, int VEC, int R, int NORM, bool STREAM>
 __global__ void __launch_bounds__(kRowThreads, kRowBlocks) head_rows_kernel(const HeadRowsParams p) {
     using Raw = typename RawVec<VEC>::type;
     constexpr int kPairs = VEC / 2;
@@ -190,8 +191,8 @@ __global__ void __launch_bounds__(kRowThreads, kRowBlocks) head_rows_kernel(cons
         for (int r = 0; r < R; ++r) {
             x[r][0] = x[r][1] = Raw{};
             if (r < nh) {
-                x[r][0] = *reinterpret_cast<const Raw*>(src + e0);
-                x[r][1] = *reinterpret_cast<const Raw*>(src + e1);
+                x[r][0] = STREAM ? __ldcs(reinterpret_cast<const Raw*>(src + e0)) : *reinterpret_cast<const Raw*>(src + e0);
+                x[r][1] = STREAM ? __ldcs(reinterpret_cast<const Raw*>(src + e1)) : *reinterpret_cast<const Raw*>(src + e1);
             }
             src += sg.src_head;
         }
@@ -275,13 +276,18 @@ __global__ void __launch_bounds__(kRowThreads, kRowBlocks) head_rows_kernel(cons
             x[r][0] = narrow<T, VEC>(a);
             x[r][1] = narrow<T, VEC>(b);
         }
-        *reinterpret_cast<Raw*>(dst + e0) = x[r][0];
-        *reinterpret_cast<Raw*>(dst + e1) = x[r][1];
+        if (STREAM) {
+            __stcs(reinterpret_cast<Raw*>(dst + e0), x[r][0]);
+            __stcs(reinterpret_cast<Raw*>(dst + e1), x[r][1]);
+        } else {
+            *reinterpret_cast<Raw*>(dst + e0) = x[r][0];
+            *reinterpret_cast<Raw*>(dst + e1) = x[r][1];
+        }
         dst += sg.dst_head;
     }
 }
 
-template <typename T, int VEC, int R>
+template <typename T, int VEC, int R, bool STREAM>
 static cudaError_t launch_rows(HeadRowsParams& p, cudaStream_t s) {
     int units = 0;
     for (HeadSegment& sg : p.seg) {
@@ -299,18 +305,23 @@ static cudaError_t launch_rows(HeadRowsParams& p, cudaStream_t s) {
     const dim3 grid(static_cast<unsigned>((threads + kRowThreads - 1) / kRowThreads));
     count_launches(1);
     const bool norm = p.seg[0].weight != nullptr || p.seg[1].weight != nullptr;
-    return launch_chained(!norm            ? head_rows_kernel<T, VEC, R, kNoNorm>
-                          : p.weight_f32   ? head_rows_kernel<T, VEC, R, kWeightsF32>
-                                           : head_rows_kernel<T, VEC, R, kWeightsTyped>,
+    return launch_chained(!norm            ? head_rows_kernel<T, VEC, R, kNoNorm, STREAM>
+                          : p.weight_f32   ? head_rows_kernel<T, VEC, R, kWeightsF32, STREAM>
+                                           : head_rows_kernel<T, VEC, R, kWeightsTyped, STREAM>,
                           grid, dim3(kRowThreads), 0, s, static_cast<const HeadRowsParams&>(p));
 }
 
 template <typename T>
 static cudaError_t launch_typed(HeadRowsParams& p, bool wide, cudaStream_t s) {
     const long long rows = static_cast<long long>(p.tokens) * (p.seg[0].heads + p.seg[1].heads + p.seg[2].heads);
-    if (!wide) return launch_rows<T, 4, 1>(p, s);
+    if (!wide) return launch_rows<T, 4, 1, false>(p, s);
     // few rows: one per group, so that they spread over the GPU; many: several, for the loads in flight
-    return rows < 16384 ? launch_rows<T, 8, 1>(p, s) : launch_rows<T, 8, kRowHeads>(p, s);
+    if (rows < 16384) return launch_rows<T, 8, 1, false>(p, s);
+    // Rows that pass through L2 (in and out, 128 MB of it) are marked to leave it first: 8192 tokens of 64 + 8 heads of
+    // 128 in 49.4 us against 54.1.  What fits stays as it is: the projection has left it there, and attention reads it
+    // next (2000 such tokens read and written in place of themselves: 11.4 us against 13.8 marked).
+    if (rows * p.head_dim * 4 > (128ll << 20)) return launch_rows<T, 8, kRowHeads, true>(p, s);
+    return launch_rows<T, 8, kRowHeads, false>(p, s);
 }
 
 cudaError_t launch_head_rows(HeadRowsParams& p, int dtype, bool wide, cudaStream_t s) {

@@ -53,6 +53,31 @@ def test_norm_and_rotation(dtype, n, hq, hk, d, rot, style):
     assert torch.equal(qkv[:, hq:], kept[:, hq:])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_large_steps_are_their_parts(dtype):
+    """Steps beyond L2 take another path through it: the same bits as in parts that do not, dense and paged."""
+    n, hq, hk, d, page = 6001, 40, 8, 128, 64
+    qkv = torch.randn(n, hq + 2 * hk, d, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).to(dtype)
+    q, k, v = qkv.split((hq, hk, hk), dim=1)
+    table, pos = kt.rope_table(n, d), torch.arange(n, dtype=torch.int32, device=DEV)
+    w = _rand(d, dtype=dtype, seed=2)
+    whole_q, whole_k = kt.qk_norm_rope(q, k, pos, table, w, w)
+    pages = -(-n // page)
+    bt = torch.arange(pages, dtype=torch.int32, device=DEV).flip(0)[None].contiguous()
+    whole = kt.PagedKV(*(torch.zeros(pages, page, hk, d, dtype=dtype, device=DEV) for _ in range(2)))
+    parts = kt.PagedKV(*(torch.zeros(pages, page, hk, d, dtype=dtype, device=DEV) for _ in range(2)))
+    got = whole.append(k, v, bt, R.starts([n], DEV), torch.tensor([n], dtype=torch.int32, device=DEV), table, q=q,
+                       q_weight=w, k_weight=w)
+    assert torch.equal(got, whole_q)
+    for lo, hi in ((0, 2000), (2000, 4001), (4001, n)):
+        pq, pk = kt.qk_norm_rope(q[lo:hi], k[lo:hi], pos[lo:hi], table, w, w)
+        assert torch.equal(pq, whole_q[lo:hi]) and torch.equal(pk, whole_k[lo:hi])
+        parts.append(k[lo:hi], v[lo:hi], bt, R.starts([hi - lo], DEV), torch.tensor([hi], dtype=torch.int32, device=DEV),
+                     table, k_weight=w)
+    assert torch.equal(whole.k_pages, parts.k_pages) and torch.equal(whole.v_pages, parts.v_pages)
+    _near(whole_k[::500], *R.head_rows(k[::500], w, 1e-6, table, pos[::500], "halves"))
+
+
 def test_unaligned_heads():
     """Heads that start 8 bytes into a 16-byte word, and outputs of another order of dimensions."""
     d, n, h = 64, 11, 4
