@@ -263,8 +263,12 @@ class PagedKV:
         self._err = self._error.data_ptr()
         self._workspaces = {}
 
-    def read_error(self, clear: bool = True) -> int:
-        """The error bits since the last clearing (waits for the current stream)."""
+    def read_error(self, clear: bool = True, stream=None) -> int:
+        """The error bits since the last clearing; waits for `stream` (default: the current one), on which the calls in
+        question were made."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.read_error(clear)
         code = int(self._error.item())
         if clear and code:
             self._error.zero_()

@@ -180,7 +180,7 @@ struct TileWalk {
 };
 
 // Deals all sequences' units in equal runs.  A warp sums a sequence: a long chunk has many items.
-__device__ __forceinline__ RunPlan plan_tiles(const AttnShape& s, const TileGeometry& g, unsigned* costs, RunPlan* shared) {
+__device__ __forceinline__ RunPlan plan_tiles(const AttnShape& s, const TileGeometry& g, unsigned long long* costs, RunPlan* shared) {
     constexpr int kWarps = kTileThreads / 32;
     __shared__ long long s_sum[kWarps];
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
@@ -188,9 +188,10 @@ __device__ __forceinline__ RunPlan plan_tiles(const AttnShape& s, const TileGeom
         for (int b = b0 + warp; b < min(s.seqs, b0 + kPlanSeqs); b += kWarps) {
             const SeqInfo q = seq_info(s, b);
             const int tiles = (q.q_len + 2 * g.tokens - 1) / (2 * g.tokens);
-            unsigned n = 0;
-            for (int r = lane; r < tiles; r += 32) n += static_cast<unsigned>(item_units(tile_item(s, q, g, r)));
-            n = __reduce_add_sync(0xffffffffu, n);
+            unsigned long long n = 0;
+            for (int r = lane; r < tiles; r += 32) n += static_cast<unsigned long long>(item_units(tile_item(s, q, g, r)));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
             if (lane == 0) costs[b - b0] = n;
         }
         __syncthreads();
@@ -199,7 +200,7 @@ __device__ __forceinline__ RunPlan plan_tiles(const AttnShape& s, const TileGeom
     for (int b0 = 0; b0 < s.seqs; b0 += kPlanSeqs) {
         if (b0 > 0) __syncthreads();
         fill(b0);
-        for (int i = tid; i < min(s.seqs - b0, kPlanSeqs); i += kTileThreads) mine += costs[i];
+        for (int i = tid; i < min(s.seqs - b0, kPlanSeqs); i += kTileThreads) mine += static_cast<long long>(costs[i]);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     griddep_wait();
     griddep_launch_dependents();
-    const RunPlan plan = plan_tiles(sh, p.geo, reinterpret_cast<unsigned*>(kv_ptr), &s_plan);
+    const RunPlan plan = plan_tiles(sh, p.geo, reinterpret_cast<unsigned long long*>(kv_ptr), &s_plan);
     tc_fence_before();
     fence_proxy_async_smem();   // the plan's and the zeros' generic writes before the first loads
     __syncthreads();
