@@ -33,7 +33,7 @@ KT_DEVERR_BAD_POSITION = 0x40
 # GPU, so a call packs its descriptors into one buffer of the thread's and passes addresses in it.
 HEADS = "Pqqixxxx"                    # kt_heads: ptr, token_stride, head_stride, heads
 PAGED_KV = "PPqqqqqqiiiiixxxx"        # kt_paged_kv: k, v, strides, num_pages, page_size, heads, head_dim, dtype
-PAGED_BATCH = "PqixxxxPPii"           # kt_paged_batch: block_table, table_stride, max_pages, cu_q, seq_lens, seqs, tokens
+PAGED_BATCH = "PqixxxxPPii"           # kt_paged_batch: block_table, table_stride, max_pages, cu_q, seq_lens, sizes
 HEAD_TRANSFORM = "PiiixxxxPPif"       # kt_head_transform: table, positions, rotary_dim, style, weights, dtype, eps
 _HEADS_BYTES, _BATCH_BYTES = struct.calcsize(HEADS), struct.calcsize(PAGED_BATCH)
 _NORM_CALL = struct.Struct(HEAD_TRANSFORM + 4 * HEADS)

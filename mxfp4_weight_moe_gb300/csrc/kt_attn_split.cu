@@ -50,7 +50,7 @@ struct SplitCfg {
     static constexpr int kStages = 3;
     static constexpr int kRing = kStages * 2 * kBlockBytes;          // per warp
     static constexpr int kSmem = kSplitWarps * kRing + 1024;
-    static constexpr int kMergeRow = DP + 8;                         // floats of a row, so that rows start 8 banks apart
+    static constexpr int kMergeRow = DP + 8;                         // floats of a row: rows start 8 banks apart
     static constexpr int kMergeBytes = kSplitWarps * kSplitRows * kMergeRow * 4;
     static constexpr int kParts = kSplitRows * DP / 4 / kSplitThreads;   // float4 per thread of 16 rows
 };
@@ -575,7 +575,8 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                         if (part_row(k) < rows) store(part_row(k), acc[k], ml[k]);
                 };
                 if (rows * (DP / 4) <= kSplitThreads) join(std::integral_constant<int, 1>());
-                else if (Cfg::kParts > 2 && rows * (DP / 4) <= 2 * kSplitThreads) join(std::integral_constant<int, 2>());
+                else if (Cfg::kParts > 2 && rows * (DP / 4) <= 2 * kSplitThreads)
+                    join(std::integral_constant<int, 2>());
                 else join(std::integral_constant<int, Cfg::kParts>());
             }
         }

@@ -145,8 +145,8 @@ __device__ __forceinline__ TokenPlace place_of(const HeadRowsParams& p, int toke
 }
 
 // Four heads a group and six blocks of 128 threads on an SM: measured on 8192 tokens of 64 + 8 heads of 128 (302 MB of
-// rows) with norms, 54.1 us (49.4 us, 6.2 TB/s, with the rows marked to leave L2); two heads 58 to 62 us, three 56.3, six
-// 56.7, fewer blocks 57.6.
+// rows) with norms, 54.1 us (49.9 us, 6.1 TB/s, with the rows marked to leave L2); two heads 58 to 62 us, three 56.3,
+// six 56.7, fewer blocks 57.6.
 constexpr int kRowThreads = 128, kRowBlocks = 6, kRowHeads = 4;
 constexpr int kNoNorm = 0, kWeightsTyped = 1, kWeightsF32 = 2;
 
@@ -191,8 +191,10 @@ __global__ void __launch_bounds__(kRowThreads, kRowBlocks) head_rows_kernel(cons
         for (int r = 0; r < R; ++r) {
             x[r][0] = x[r][1] = Raw{};
             if (r < nh) {
-                x[r][0] = STREAM ? __ldcs(reinterpret_cast<const Raw*>(src + e0)) : *reinterpret_cast<const Raw*>(src + e0);
-                x[r][1] = STREAM ? __ldcs(reinterpret_cast<const Raw*>(src + e1)) : *reinterpret_cast<const Raw*>(src + e1);
+                const Raw* s0 = reinterpret_cast<const Raw*>(src + e0);
+                const Raw* s1 = reinterpret_cast<const Raw*>(src + e1);
+                x[r][0] = STREAM ? __ldcs(s0) : *s0;
+                x[r][1] = STREAM ? __ldcs(s1) : *s1;
             }
             src += sg.src_head;
         }

@@ -72,8 +72,8 @@ def test_large_steps_are_their_parts(dtype):
     for lo, hi in ((0, 2000), (2000, 4001), (4001, n)):
         pq, pk = kt.qk_norm_rope(q[lo:hi], k[lo:hi], pos[lo:hi], table, w, w)
         assert torch.equal(pq, whole_q[lo:hi]) and torch.equal(pk, whole_k[lo:hi])
-        parts.append(k[lo:hi], v[lo:hi], bt, R.starts([hi - lo], DEV), torch.tensor([hi], dtype=torch.int32, device=DEV),
-                     table, k_weight=w)
+        parts.append(k[lo:hi], v[lo:hi], bt, R.starts([hi - lo], DEV),
+                     torch.tensor([hi], dtype=torch.int32, device=DEV), table, k_weight=w)
     assert torch.equal(whole.k_pages, parts.k_pages) and torch.equal(whole.v_pages, parts.v_pages)
     _near(whole_k[::500], *R.head_rows(k[::500], w, 1e-6, table, pos[::500], "halves"))
 
@@ -164,7 +164,7 @@ def test_append(dtype, layout, q_lens, past, hq, hk, d, rot, style, page, norm):
 
 
 def test_append_bad_pages_and_positions():
-    """A page outside the cache, a length outside the table, a position outside the rotation table: told, not written."""
+    """A page outside the cache, a length outside the table, a position outside the rotation: told, not written."""
     d, page = 64, 16
     kp = torch.zeros(4, page, 1, d, dtype=torch.bfloat16, device=DEV)
     vp = torch.zeros_like(kp)
@@ -172,7 +172,7 @@ def test_append_bad_pages_and_positions():
     k = torch.ones(4, 1, d, dtype=torch.bfloat16, device=DEV)
     cu = R.starts([1, 1, 1, 1], DEV)
     bt = torch.tensor([[4, 0], [-1, 0], [1, 2], [3, 3]], dtype=torch.int32, device=DEV)
-    lens = torch.tensor([1, 1, 33, 0], dtype=torch.int32, device=DEV)       # no such page twice, past the table, before 0
+    lens = torch.tensor([1, 1, 33, 0], dtype=torch.int32, device=DEV)       # no page twice, past the table, before 0
     cache.append(k, k, bt, cu, lens)
     assert cache.read_error() == A.KT_DEVERR_BAD_PAGE and cache.read_error() == 0
     assert not bool(kp.any()) and not bool(vp.any())
