@@ -28,10 +28,11 @@
 // Bound: for heads of 128 the tensor cores (2630 of 3000 cycles of a tile pair),
 // for smaller heads the softmax (128 exponentials a row and tile: 1370 cycles of
 // issue and exponential unit for the two warps of a scheduler, measured alone).
-// Measured on GB300 (bf16): an 8192-token prompt, 64 / 8 heads of 128, 670 us,
-// 1640 TFLOP/s (85 % of the measured burst matmul rate, 96 % of the sustained
-// one); heads of 64, 600 us, 916 TFLOP/s; 2048 tokens after 30001 on 16-slot
-// pages (fp16, 32 / 8 heads of 128) 683 us, 1525 TFLOP/s.
+// Measured on GB300 (bf16): an 8192-token prompt, 64 / 8 heads of 128, 670 us on
+// the fastest machine (1640 TFLOP/s, 85 % of the measured burst matmul rate, 96 %
+// of the sustained one), up to 790 us on others; heads of 64, 600 us, 916
+// TFLOP/s; 2048 tokens after 30001 on 16-slot pages (fp16, 32 / 8 heads of 128)
+// 652 to 702 us, 1480 to 1600 TFLOP/s.
 //
 // Tried and left out (8192-token prompt): P beside S so that the next S comes
 // early (heads of 64: 636 against 614 us, both groups then contend for the
@@ -823,7 +824,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 return lt == 0.0f ? 0.0f : scale_o / lt;
             };
             // A row's 64 bytes lie with one lane; four lanes exchange 16-byte pieces, so as to write a row at a time
-            // (16 scattered bytes a lane: 7.5 k cycles an item for the output, this 1.7 k).
+            // (16 scattered bytes a lane took 7.5 k cycles an item for the output).
             T* four[4];   // the rows of the lane's four (null: not stored), given its own
             auto meet = [&](T* own) {
 #pragma unroll
