@@ -9,8 +9,10 @@
  * before anything is launched, no device memory allocated, sm_103a only.  The
  * descriptor structs are HOST structs, read during the call.  Element types are
  * KT_DTYPE_BF16 or KT_DTYPE_FP16; all arithmetic is fp32, rounded once to the
- * element type where a result is stored (attention also rounds its softmax
- * weights to the element type for the matrix product with the values).
+ * element type where a result is stored.  For the matrix product with the values,
+ * attention holds its softmax weights in two parts of the element type where a
+ * call has few query rows (max_q_len x group up to 16), and rounds them to the
+ * element type, once, for chunks of more.
  */
 #ifndef KT_ATTN_H
 #define KT_ATTN_H

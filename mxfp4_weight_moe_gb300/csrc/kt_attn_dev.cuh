@@ -5,6 +5,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "kt_attn_internal.h"
 #include "kt_common.cuh"
 
@@ -184,6 +186,32 @@ template <>
 __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// The two halves of such a pair as floats.
+template <typename T>
+__device__ __forceinline__ float low_of(uint32_t v) {
+    if (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(v << 16);
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(v)));
+}
+template <typename T>
+__device__ __forceinline__ float high_of(uint32_t v) {
+    if (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(v & 0xffff0000u);
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(v >> 16)));
+}
+// A pair of T, what is larger than T's largest number (infinity) replaced by that, signs kept.
+template <typename T>
+__device__ __forceinline__ uint32_t finite_pair(uint32_t v);
+template <>
+__device__ __forceinline__ uint32_t finite_pair<__nv_bfloat16>(uint32_t v) {
+    uint32_t r;
+    asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7f7f7f7fu));
+    return r;
+}
+template <>
+__device__ __forceinline__ uint32_t finite_pair<__half>(uint32_t v) {
+    uint32_t r;
+    asm("min.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7bff7bffu));
     return r;
 }
 #endif

@@ -8,9 +8,12 @@
 // of its own: no barrier among warps until the item's end.  S = Q K^T and P V
 // are mma.sync products of 16 rows: the operator is bound by reading the cache
 // (16 flops a byte for 8 heads a cache head), which they keep up with, and their
-// latency is a warp's, where a tensor-memory tile's would be a CTA's.  P is
-// rounded to the element type for the product with V; the sum that divides the
-// result is of the unrounded weights.
+// latency is a warp's, where a tensor-memory tile's would be a CTA's.  P goes into
+// the product with V in two parts of the element type, P rounded to it and the
+// remainder rounded to it (16 bits of P in bf16, 22 in fp16): the tensor cores wait
+// for the cache anyway, so that the second product costs 0 to 1.5 % of a large
+// cache's time and 3 % of a short one's (one part, the other way: 207 against 209
+// us, 10.1 against 10.3), and the error is that of fp32 and the result's rounding.
 //
 // Few items are cut into pieces that each have a CTA of their own; many lie on a
 // line that is cut into equal runs, so that one long sequence and many short ones
@@ -406,10 +409,13 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
             const bool ragged = key0 + Cfg::kBlockKeys > it.hi || key0 < it.lo;
 #pragma unroll
             for (int sub = 0; sub < Cfg::kSub; ++sub) {
-                const uint32_t pa[4] = {pack2<T>(x[0][4 * sub], x[0][4 * sub + 1]),
-                                        pack2<T>(x[1][4 * sub], x[1][4 * sub + 1]),
-                                        pack2<T>(x[0][4 * sub + 2], x[0][4 * sub + 3]),
-                                        pack2<T>(x[1][4 * sub + 2], x[1][4 * sub + 3])};
+                uint32_t pa[4], pb[4];   // the two parts of the weights
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const float lo = x[f & 1][4 * sub + (f >> 1) * 2], hi = x[f & 1][4 * sub + (f >> 1) * 2 + 1];
+                    pa[f] = pack2<T>(lo, hi);
+                    pb[f] = pack2<T>(lo - low_of<T>(pa[f]), hi - high_of<T>(pa[f]));
+                }
 #pragma unroll
                 for (int n = 0; n < DP / 8; n += 2) {
                     uint32_t vf[4];
@@ -426,6 +432,10 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                     }
                     mma_16816<T>(o[n], pa, vf[0], vf[1]);
                     mma_16816<T>(o[n + 1], pa, vf[2], vf[3]);
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) vf[f] = finite_pair<T>(vf[f]);   // (a second part of 0 x infinity)
+                    mma_16816<T>(o[n], pb, vf[0], vf[1]);
+                    mma_16816<T>(o[n + 1], pb, vf[2], vf[3]);
                 }
             }
             __syncwarp();
