@@ -129,7 +129,8 @@ size_t kt_paged_attention_workspace_bytes(void);
  * over the keys j <= position(t), and j > position(t) - window where window > 0;
  * group = q heads / cache heads (a whole number, at most 128).  sinks (f32 [q
  * heads], may be NULL; finite or -inf) adds exp(sinks[h]) to the softmax's sum.
- * A token that sees no key gets zeros.
+ * A token that sees no key gets zeros.  Pages that lie before every token's window
+ * are not read, whatever their entries say.
  *   max_q_len  upper bound of the sequences' new tokens (picks the kernel form
  *              only; results hold for any value)
  *   scale      finite, > 0

@@ -331,7 +331,8 @@ class PagedKV:
 
         max_q_len: an upper bound of the sequences' new tokens (it picks the kernel, not the result).  scale: default
         head_dim ** -0.5.  window > 0: each token sees its last `window` positions, its own among them.  sinks: f32
-        [q heads], logits added to each softmax's sum.  A token that sees no key gets zeros.
+        [q heads], logits added to each softmax's sum.  A token that sees no key gets zeros.  Pages that lie before every
+        token's window are not read, whatever their entries say.
 
         A non-finite value row reaches, besides the tokens that see it, others of the sequence that share a tile with
         those; rows past a sequence's keys reach nothing."""

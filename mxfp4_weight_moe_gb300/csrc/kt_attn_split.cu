@@ -269,7 +269,8 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                 const int key = base + mine * Cfg::kUnit + lane % Cfg::kSub * kSplitKeys;
                 my_page = -1;
                 my_slot = 0;
-                if (mine < i1 && key < it.hi) {   // (past the keys: zeros from outside the cache)
+                // (16 keys that no row sees, past them all or before the window: zeros from outside the cache)
+                if (mine < i1 && key < it.hi && key + kSplitKeys > it.lo) {
                     my_page = checked_page(sh, pages, key);
                     my_slot = key % sh.page_size;
                 }

@@ -75,3 +75,27 @@ def test_infinite_values_that_a_token_sees(dtype, new):
     assert bool((out[..., 5] == float("inf")).all()) and bool((out[..., 50] == float("-inf")).all())
     rest = [i for i in range(d) if i not in (5, 50)]
     assert bool(((out.double().cpu() - want)[..., rest].abs() <= bound[..., rest]).all())
+
+
+@pytest.mark.parametrize("new", [1, 3])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 48])
+def test_pages_behind_the_window_are_free(new, d, page):
+    """A page that no token's window reaches need not be one: its entry says nothing, what it holds reaches nothing.
+
+    33 lengths, so that windows start at every place of a block of keys; single tokens and chunks of three take the
+    kernels for few rows and for many."""
+    window, hq, hk = 40, 8, 1
+    lens = [150 + i for i in range(33)]
+    kp, vp, table = R.paged(lens, page, hk, d, torch.bfloat16, DEV, 21)
+    q = _rand(new * len(lens), hq, d, dtype=torch.bfloat16, seed=22)
+    want, bound = R.attend(q, kp, vp, table, [new] * len(lens), lens, R.softmax_scale(d), window)
+    for b, n in enumerate(lens):
+        behind = (n - new - window + 1) // page              # pages before the first token's first key
+        freed = table[b, :behind].long()
+        kp[freed], vp[freed] = float("nan"), float("nan")
+        table[b, :behind] = _i32([(-1, kp.shape[0], -2 ** 31)[i % 3] for i in range(behind)])
+    cache = kt.PagedKV(kp, vp)
+    out = cache.attend(q, table, R.starts([new] * len(lens), DEV), _i32(lens), new, window=window)
+    assert cache.read_error() == 0
+    assert bool(((out.double().cpu() - want).abs() <= bound).all())
