@@ -110,13 +110,13 @@ __device__ __forceinline__ void load_turn(const float* cos, const float* sin, ui
     }
 }
 
-// Where a token's rows go: rotation position (-1: none such, queries and keys are not written), page and slot of the
-// cache (page -1: keys and values are not written); kNoToken for a token of no sequence.
+// Where a token's rows go: rotation position (negative: nothing of the token is written, for it has none such or, with
+// kNoToken, is of no sequence), page and slot of the cache (page -1: keys and values are not written).
 struct TokenPlace {
     int pos, page, slot;
 };
 constexpr int kNoToken = -2;
-// tells: the caller reports what is wrong; which: segment that asks (2: values, which need no rotation), -1 for all.
+// tells: the caller reports what is wrong (a position, but for values: queries and keys do); which: segment that asks.
 __device__ __forceinline__ TokenPlace place_of(const HeadRowsParams& p, int token, bool tells, int which) {
     TokenPlace t{0, -1, 0};
     if (p.cu_q != nullptr) {
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kRowThreads, kRowBlocks) head_rows_kernel(cons
     uint64_t cs[kPairs], sn[kPairs];
     if (inside) {
         const TokenPlace t = place_of(p, static_cast<int>(token), j == 0, which);
-        ok = ok && t.pos != kNoToken && (which == 2 || t.pos >= 0) && (!sg.paged || t.page >= 0);
+        ok = ok && t.pos >= 0 && (!sg.paged || t.page >= 0);
         dst += sg.paged ? t.page * sg.dst_page + t.slot * sg.dst_token : static_cast<long long>(token) * sg.dst_token;
         turned = ok && rotated && which != 2 && p.table != nullptr;
         if (turned) {
