@@ -32,6 +32,7 @@ extern "C" {
 #define KT_DEVERR_BAD_PAGE 0x20     /* a needed block-table entry was outside [0, num_pages), or a length
                                        outside the block table: nothing is written there; it reads as zeros */
 #define KT_DEVERR_BAD_POSITION 0x40 /* a rotation position outside the table: that token is not written */
+/* KT_DEVERR_TIMEOUT_* (kt_moe.h): a wait inside kt_paged_attention ran out; that call's results are undefined. */
 
 /* [tokens, heads, head_dim]: element (t, h, d) at ptr + t*token_stride + h*head_stride + d (strides in elements). */
 typedef struct kt_heads {

@@ -372,10 +372,11 @@ kt_status kt_moe_profile_enable_stages(uint32_t stage_mask);
 
 /*
  * Test hook for the device-side failure path.  wait_limit_us bounds every
- * barrier wait inside the GEMM kernels (0 restores the default of 2 s).
- * flags = KT_DEBUG_WITHHOLD_STAGE makes each GEMM CTA's producer withhold
- * the first pipeline stage of its first tile (nothing is loaded into it and
- * it is never signalled), so the MMA issuer's wait runs out: the kernel
+ * barrier wait inside the GEMM kernels and those of kt_attn.h (0 restores the
+ * default of 2 s).  flags = KT_DEBUG_WITHHOLD_STAGE makes each GEMM CTA's
+ * producer withhold the first pipeline stage of its first tile, and the first
+ * CTA of an attention kernel its first load of keys (nothing is loaded into it
+ * and it is never signalled), so that the wait for it runs out: the kernel
  * records KT_DEVERR_TIMEOUT_* in the error word, frees its tensor memory
  * and returns; the CUDA context stays usable.  Process-wide; 0 disables.
  */

@@ -400,7 +400,7 @@ def profile_enable(enable: bool = True, stages=None):
 
 
 def debug_configure(wait_limit_us: int = 0, flags: int = 0):
-    """Test hook: bound the GEMM barrier waits and optionally withhold a stage
+    """Test hook: bound the GEMM and attention kernels' barrier waits and optionally withhold a stage
     (see kt_moe_debug_configure); debug_configure() restores the defaults."""
     _check(lib().kt_moe_debug_configure(int(wait_limit_us), int(flags)), "kt_moe_debug_configure")
 

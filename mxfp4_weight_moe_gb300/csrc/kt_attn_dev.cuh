@@ -24,6 +24,8 @@ struct AttnShape {
     int seqs, tokens, max_pages, num_pages, page_size;
     int kv_heads, group, head_dim, window;
     float scale_log2;   // scale * log2(e): the softmax runs on powers of two
+    int withhold;       // test hook: the first CTA withholds its first load
+    unsigned long long wait_limit_ns;
 };
 
 inline AttnShape attn_shape(const AttnArgs& a) {
@@ -44,6 +46,9 @@ inline AttnShape attn_shape(const AttnArgs& a) {
     s.head_dim = a.kv.head_dim;
     s.window = a.window;
     s.scale_log2 = a.scale * kLog2e;
+    const DebugSettings dbg = debug_settings();
+    s.withhold = (dbg.flags & KT_DEBUG_WITHHOLD_STAGE) != 0;
+    s.wait_limit_ns = dbg.wait_limit_ns;
     return s;
 }
 
@@ -83,6 +88,13 @@ __device__ __forceinline__ int checked_page(const AttnShape& s, const int32_t* p
     set_error(s.err, KT_DEVERR_BAD_PAGE);
     return -1;
 }
+
+// mbar_wait with one answer for the whole warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag,
+                                          unsigned long long limit_ns) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, limit_ns)) != 0;
+}
+constexpr uint64_t kDrainLimitNs = 1000000;   // for loads in flight to land, after a wait has run out
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
                                             int w) {

@@ -249,6 +249,8 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
         }
     }
     uint32_t loads = 0;            // blocks this warp has consumed so far
+    bool gave_up = false;          // a wait ran out: the warp loads nothing more, but takes part in joins and counters
+    const bool withhold = sh.withhold != 0 && blockIdx.x == 0 && warp == 0;
     const uint64_t policy = l2_policy_evict_first();   // 64 single tokens: 211 us, 215 without
     while (true) {
         if (u1 > u0) {
@@ -259,8 +261,10 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
         int i0 = 0, i1 = u1 - u0;
         while (i0 < i1 && base + i0 * Cfg::kUnit + Cfg::kBlockKeys <= it.lo) ++i0;
         while (i1 > i0 && base + (i1 - 1) * Cfg::kUnit >= it.hi) --i1;
+        if (gave_up) i1 = i0;
         int page_batch = -1, my_page = -1, my_slot = 0;
         auto issue = [&](int i) {   // whole warp; block i into its stage
+            if (withhold && loads == 0 && i == i0) return;   // test hook
             // lanes look up the pages of the next 32 loads at a time
             const int batch = (i - i0) / (32 / Cfg::kSub);
             if (batch != page_batch) {
@@ -334,9 +338,20 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
         for (int i = i0; i < i1; ++i) {
             const uint32_t seq_no = loads + static_cast<uint32_t>(i - i0);
             const uint32_t st = seq_no % Cfg::kStages;
-            if (!mbar_wait(smem_u32(&s_full[warp][st]), (seq_no / Cfg::kStages) & 1u, &s_abort)) {
-                s_abort = 1;
-                set_error(sh.err, KT_DEVERR_TIMEOUT_LOAD);
+            if (!warp_wait(smem_u32(&s_full[warp][st]), (seq_no / Cfg::kStages) & 1u, &s_abort, sh.wait_limit_ns)) {
+                if (lane == 0 && !*reinterpret_cast<volatile int*>(&s_abort)) {
+                    s_abort = 1;
+                    set_error(sh.err, KT_DEVERR_TIMEOUT_LOAD);
+                }
+                // loads still in flight land before their memory has another use (each wait bounded)
+                int never = 0;
+                for (int k = i; k < min(i + Cfg::kStages, i1); ++k) {
+                    const uint32_t no = loads + static_cast<uint32_t>(k - i0);
+                    mbar_wait(smem_u32(&s_full[warp][no % Cfg::kStages]), (no / Cfg::kStages) & 1u, &never,
+                              kDrainLimitNs);
+                }
+                gave_up = true;
+                break;
             }
             const uint32_t kb = smem_u32(ring + st * 2 * Cfg::kBlockBytes);
             const uint32_t vb = kb + Cfg::kBlockBytes;

@@ -391,11 +391,6 @@ __device__ __forceinline__ void weights32(const float (&x)[32], uint64_t c2, uin
     }
 }
 
-// mbar_wait with one answer for the whole warp.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
-}
-
 // The item's tile whose last rows lie past the sequence's end inside a page, if it is in this run; else -1.
 __device__ __forceinline__ int ragged_tile(const TileWalk& w, int box_slots) {
     const int j = w.sq.keys >= w.it.base ? (w.sq.keys - w.it.base) / kTileKeys : -1;
@@ -461,6 +456,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __syncthreads();
     tc_fence_after();
     const int* abort_flag = &s_abort;
+    const unsigned long long limit = sh.wait_limit_ns;
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -485,7 +481,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (lane < boxes && key < w.it.hi && key + p.geo.box_slots > w.it.lo)
                         page = checked_page(sh, pages, key);
                     page = __shfl_sync(0xffffffffu, page, box);
-                    if (round > 0) ok = warp_wait(smem_u32(&s_kv_empty[stage]), (round - 1) & 1u, abort_flag);
+                    if (round > 0) ok = warp_wait(smem_u32(&s_kv_empty[stage]), (round - 1) & 1u, abort_flag, limit);
                     if (!ok) break;
                     if (lane == 0) mbar_arrive_expect_tx(full, Cfg::kStageBytes);
                     __syncwarp();
@@ -508,7 +504,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 int never = 0;
                 for (int i = 0; i < Cfg::kStages && load >= 2; ++i) {
                     load -= 2;
-                    mbar_wait(smem_u32(&s_kv_full[load % Cfg::kStages]), (load / Cfg::kStages) & 1u, &never, 1000000);
+                    mbar_wait(smem_u32(&s_kv_full[load % Cfg::kStages]), (load / Cfg::kStages) & 1u, &never,
+                              kDrainLimitNs);
                 }
             }
         } else if (warp == 11) {
@@ -519,7 +516,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 const int groups = w.groups(tpg);
                 for (int i = 0; i < groups; ++i) {
                     const uint32_t buf = item_no[i] % Cfg::kQBufs, round = item_no[i] / Cfg::kQBufs;
-                    if (round > 0) ok = warp_wait(smem_u32(&s_q_empty[buf][i]), (round - 1) & 1u, abort_flag);
+                    if (round > 0) ok = warp_wait(smem_u32(&s_q_empty[buf][i]), (round - 1) & 1u, abort_flag, limit);
                     if (!ok) break;
                     ++item_no[i];
                     if (lane == 0) {
@@ -541,7 +538,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 for (int i = 0; i < 2; ++i)
                     for (uint32_t k = 0; k < Cfg::kQBufs && k < item_no[i]; ++k) {
                         const uint32_t n = item_no[i] - 1 - k;
-                        mbar_wait(smem_u32(&s_q_full[n % Cfg::kQBufs][i]), (n / Cfg::kQBufs) & 1u, &never, 1000000);
+                        mbar_wait(smem_u32(&s_q_full[n % Cfg::kQBufs][i]), (n / Cfg::kQBufs) & 1u, &never,
+                                  kDrainLimitNs);
                     }
             }
         } else if (warp == 8 && elect_one()) {
@@ -568,7 +566,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             Ring k_ring{0, 0}, v_ring{1, 0};
             // parities of each group's next query item and weights; query buffer
             uint32_t q_parity0 = 0, q_parity1 = 0, q_buf0 = 0, q_buf1 = 0, p_parity0 = 0, p_parity1 = 0;
-            auto wait = [&](uint64_t& bar, uint32_t par) { return mbar_wait(smem_u32(&bar), par, abort_flag); };
+            auto wait = [&](uint64_t& bar, uint32_t par) { return mbar_wait(smem_u32(&bar), par, abort_flag, limit); };
             auto tile_ahead = [&](Tile& t) {   // false: no more
                 if (ahead == w.t1) {
                     more_items = more_items && w.next(sh, p.geo);
@@ -668,7 +666,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         auto group_sync = [&]() {   // the group's four warps; bounded, as every wait here
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&s_sync[grp]));
-            return warp_wait(smem_u32(&s_sync[grp]), sync_no++ & 1u, abort_flag);
+            return warp_wait(smem_u32(&s_sync[grp]), sync_no++ & 1u, abort_flag, limit);
         };
         uint32_t tile_no = 0, item_no = 0, loads = 0;   // loads: key and value tiles of the items so far
         bool ok = true;
@@ -690,7 +688,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             float m = -INFINITY, l = 0.0f;
             for (int j = w.t0; j < w.t1; ++j) {
                 const int key0 = w.it.base + j * kTileKeys;
-                ok = warp_wait(smem_u32(&s_s_full[grp]), tile_no & 1u, abort_flag);
+                ok = warp_wait(smem_u32(&s_s_full[grp]), tile_no & 1u, abort_flag, limit);
                 if (!ok) break;
                 ++tile_no;
                 tc_fence_after();
@@ -726,7 +724,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     // this group lets the tile be multiplied (group 1's product is issued after it).
                     const uint32_t load = loads + 2 * static_cast<uint32_t>(j - w.t0) + 1;   // K0 V0 K1 V1 ...
                     const uint32_t st = load % Cfg::kStages;
-                    ok = warp_wait(smem_u32(&s_kv_full[st]), (load / Cfg::kStages) & 1u, abort_flag);
+                    ok = warp_wait(smem_u32(&s_kv_full[st]), (load / Cfg::kStages) & 1u, abort_flag, limit);
                     if (!ok) break;
                     const int past = w.sq.keys - key0;
                     const int end = (past / p.geo.box_slots + 1) * p.geo.box_slots;   // the rest was loaded as zeros
@@ -801,7 +799,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             if (!ok) break;
             loads += 2 * static_cast<uint32_t>(w.t1 - w.t0);
-            ok = warp_wait(smem_u32(&s_o_full[grp]), item_no & 1u, abort_flag);
+            ok = warp_wait(smem_u32(&s_o_full[grp]), item_no & 1u, abort_flag, limit);
             if (!ok) break;
             ++item_no;
             tc_fence_after();

@@ -122,7 +122,7 @@ struct GemmArgs {
     float alpha = 1.0f, limit = 0.0f;
 };
 
-// Test-hook settings (kt_moe_debug_configure), read at each GEMM launch.
+// Test-hook settings (kt_moe_debug_configure), read at each GEMM and attention launch.
 struct DebugSettings {
     uint64_t wait_limit_ns;
     int flags;
