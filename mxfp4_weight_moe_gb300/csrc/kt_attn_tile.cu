@@ -408,6 +408,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     __shared__ __align__(8) uint64_t s_s_full[2], s_p_full[2][2], s_o_full[2], s_sync[2], s_done;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_last[2];
+    __shared__ long long s_counted[2];   // first tile of the last item that a group has counted
     __shared__ RunPlan s_plan;
     const AttnShape& sh = p.sh;
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
@@ -419,6 +420,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
     if (tid == 0) {
         s_abort = 0;
+        s_counted[0] = s_counted[1] = -1;
         for (int i = 0; i < Cfg::kStages; ++i) {
             mbar_init(smem_u32(&s_kv_full[i]), 1);
             mbar_init(smem_u32(&s_kv_empty[i]), 1);
@@ -483,6 +485,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     page = __shfl_sync(0xffffffffu, page, box);
                     if (round > 0) ok = warp_wait(smem_u32(&s_kv_empty[stage]), (round - 1) & 1u, abort_flag, limit);
                     if (!ok) break;
+                    if (sh.withhold != 0 && blockIdx.x == 0 && load == 0) {   // test hook: the first keys
+                        load += 2;
+                        continue;
+                    }
                     if (lane == 0) mbar_arrive_expect_tx(full, Cfg::kStageBytes);
                     __syncwarp();
                     if (lane < boxes * (DP / 64)) {
@@ -671,7 +677,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint32_t tile_no = 0, item_no = 0, loads = 0;   // loads: key and value tiles of the items so far
         bool ok = true;
         TileWalk w;
-        for (bool more = w.start(sh, p.geo, plan); more && ok; more = w.next(sh, p.geo)) {
+        bool more = w.start(sh, p.geo, plan);
+        // The pieces of a cut item lie with the CTA of its first tile (that CTA's slot 1) and the following ones (slot
+        // 0); whoever counts last, as this says, clears the count for the next call.
+        auto first_piece = [&]() { return static_cast<int>(w.first / plan.per); };
+        auto last_piece = [&]() { return static_cast<int>((w.first + w.it.tiles - 1) / plan.per); };
+        auto count_piece = [&]() -> bool {
+            const int c0 = first_piece();
+            const bool last = atomicAdd(&p.counters[2 * c0 + grp], 1u) == static_cast<unsigned>(last_piece() - c0);
+            if (last) p.counters[2 * c0 + grp] = 0;
+            return last;
+        };
+        for (; more && ok; more = w.next(sh, p.geo)) {
             if (grp >= w.groups(tpg)) continue;
             const int tok0 = (w.rt * 2 + grp) * tpg, tok = tok0 + row_tok;
             const bool valid = row_tok < tpg && tok < w.sq.q_len;
@@ -869,9 +886,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 tc_fence_before();
                 continue;
             }
-            // pieces of the item: the run of its first tile (that CTA's slot 1), then the following ones (slot 0)
-            const int c0 = static_cast<int>(w.first / plan.per);
-            const int c1 = static_cast<int>((w.first + w.it.tiles - 1) / plan.per);
+            const int c0 = first_piece();
             const size_t slot = 2 * blockIdx.x + (w.t0 == 0 ? 1 : 0);
             const int prow = grp * 128 + row;
 #pragma unroll 1
@@ -889,9 +904,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (!(ok = group_sync())) break;
             if (row == 0) {
                 __threadfence();
-                const unsigned seen = atomicAdd(&p.counters[2 * c0 + grp], 1u);
-                s_last[grp] = seen == static_cast<unsigned>(c1 - c0);
-                if (s_last[grp]) p.counters[2 * c0 + grp] = 0;
+                s_last[grp] = count_piece();
+                s_counted[grp] = w.first;
                 __threadfence();
             }
             if (!(ok = group_sync())) break;
@@ -905,7 +919,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int jtok = joins ? jrow / sh.group : 0, jhead = joins ? jrow - jtok * sh.group : 0;
             meet(joins ? out0 + jtok * p.o_token + jhead * p.o_head : nullptr);
             auto slot_of = [&](int k) { return 2 * static_cast<size_t>(c0 + k) + (k == 0 ? 1 : 0); };
-            const int pieces = c1 - c0 + 1, jp = grp * 128 + (joins ? jrow : 0);
+            const int pieces = last_piece() - c0 + 1, jp = grp * 128 + (joins ? jrow : 0);
             float mt = -INFINITY, lt = 0.0f;
 #pragma unroll 8
             for (int k = 0; k < pieces; ++k) mt = fmaxf(mt, __ldcg(&p.part_ml[slot_of(k) * 256 + jp]).x);
@@ -941,9 +955,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 store_64(v, d0 + q);
             }
         }
-        if (!ok && !*reinterpret_cast<volatile int*>(&s_abort)) {
-            s_abort = 1;
-            set_error(sh.err, KT_DEVERR_TIMEOUT_EPI);
+        if (!ok) {
+            if (!*reinterpret_cast<volatile int*>(&s_abort)) {
+                s_abort = 1;
+                set_error(sh.err, KT_DEVERR_TIMEOUT_EPI);
+            }
+            // the run's pieces that have not been counted are, so that the counters are zero after the call
+            if (row == 0)
+                for (; more; more = w.next(sh, p.geo))
+                    if (grp < w.groups(tpg) && !(w.t0 == 0 && w.t1 == w.it.tiles) && s_counted[grp] != w.first)
+                        count_piece();
         }
         tc_fence_before();
     }

@@ -44,3 +44,10 @@ def _withheld_call_between_two(seqs, new, past, hq, hk, d, dtype):
 def test_few_rows(seqs, past, dtype, d):
     """One sequence cut over many CTAs, one that one CTA has, and more than there are CTAs, some cut."""
     _withheld_call_between_two(seqs, 1, past, 8, 1, d, dtype)
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 64), (torch.float16, 128)])
+@pytest.mark.parametrize("seqs,new,past,hq", [(1, 40, 20000, 8), (1, 20, 40, 8), (3, 500, 300, 8), (20, 300, 0, 5)])
+def test_chunks(seqs, new, past, hq, dtype, d):
+    """Items that many CTAs share, that one has, and runs of several items, the last ones cut."""
+    _withheld_call_between_two(seqs, new, past, hq, 1, d, dtype)
