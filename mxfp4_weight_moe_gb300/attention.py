@@ -233,8 +233,9 @@ class PagedKV:
     any strides with contiguous heads, page_size a multiple of 16, head_dim a multiple of 8 up to 128.
 
     The tensors are checked once and stay the caller's.  `append` and `attend` report device-side conditions in an
-    error word (`read_error`): KT_DEVERR_BAD_PAGE, KT_DEVERR_BAD_POSITION.  `attend` keeps one workspace per stream
-    that it is called on (while a CUDA graph is captured, one of the graph's own)."""
+    error word (`read_error`): KT_DEVERR_BAD_PAGE, KT_DEVERR_BAD_POSITION, of `attend` also KT_DEVERR_TIMEOUT_*; making
+    the object waits for the current stream, so that the word is clear for calls on any.  `attend` keeps one workspace
+    per stream that it is called on (while a CUDA graph is captured, one of the graph's own)."""
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor):
         for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
@@ -259,19 +260,23 @@ class PagedKV:
             PAGED_KV, k_pages.data_ptr(), v_pages.data_ptr(), *strides, self.num_pages, self.page_size, self.heads,
             self.head_dim, DTYPE_CODES[self.dtype]))
         self._desc_at = ctypes.addressof(self._desc)
-        self._error = torch.zeros(1, dtype=torch.int32, device=self.device)
+        with torch.cuda.device(self.device):
+            self._error = torch.zeros(1, dtype=torch.int32, device=self.device)
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()   # calls may come on any stream: it is zero before the first
         self._err = self._error.data_ptr()
         self._workspaces = {}
 
     def read_error(self, clear: bool = True, stream=None) -> int:
         """The error bits since the last clearing; waits for `stream` (default: the current one), on which the calls in
-        question were made."""
+        question were made, and clears the bits that it returns."""
         if stream is not None:
             with torch.cuda.stream(stream):
                 return self.read_error(clear)
         code = int(self._error.item())
         if clear and code:
-            self._error.zero_()
+            self._error.bitwise_and_(~code)
+            torch.cuda.current_stream(self.device).synchronize()   # before calls on other streams set them again
         return code
 
     def workspace(self) -> torch.Tensor:
