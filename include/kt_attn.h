@@ -101,7 +101,7 @@ typedef struct kt_head_transform {
 /*
  * Norm and rotation of q and k (k may be NULL) in one pass and one launch:
  * q_out = transform(q), k_out = transform(k).  An output may be its input (same
- * pointer and strides).  positions: i32 [tokens], required with a table.
+ * pointer and strides) and shares no memory otherwise.  positions: i32 [tokens], required with a table.
  * head_dim: multiple of 8 up to 256; pointers 8-byte aligned, strides multiples
  * of 4 elements.  tokens == 0 is a no-op.
  * Errors: KT_ERR_INVALID_ARG, KT_ERR_UNSUPPORTED_SHAPE, KT_ERR_ALIGNMENT, KT_ERR_CUDA.
@@ -113,7 +113,8 @@ kt_status kt_qk_norm_rope(const kt_heads* q, const kt_heads* k, const kt_heads* 
 /*
  * Append the step's keys (transformed; transform may be NULL) and values to the
  * cache, and, where q is not NULL, write q_out = transform(q), all in one
- * launch.  The rotation position is the position in the sequence.
+ * launch.  The rotation position is the position in the sequence.  q_out may be q
+ * and shares no memory otherwise.
  */
 kt_status kt_kv_append(const kt_paged_kv* cache, const kt_paged_batch* batch, const kt_heads* k, const kt_heads* v,
                        const kt_heads* q, const kt_heads* q_out, const kt_head_transform* transform, int* err,
@@ -138,7 +139,8 @@ size_t kt_paged_attention_workspace_bytes(void);
  *   ws         >= kt_paged_attention_workspace_bytes() bytes, 256-byte aligned,
  *              its first KT_PAGED_ATTENTION_ZEROED bytes zeroed before the first
  *              use; every call leaves them zero
- * q and out: 16-byte aligned, strides multiples of 8 elements.
+ * q and out: 16-byte aligned, strides multiples of 8 elements.  out may be q (same
+ * pointer and strides) and shares no memory otherwise.
  */
 kt_status kt_paged_attention(const kt_paged_kv* cache, const kt_paged_batch* batch, const kt_heads* q,
                              const kt_heads* out, int max_q_len, float scale, int window, const float* sinks, int* err,

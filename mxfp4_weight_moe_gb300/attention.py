@@ -93,6 +93,42 @@ def _written(t, name: str):
         raise ValueError(f"{name}: its rows overlap, strides are {st}")
 
 
+def _rows_meet(a, b, n: int, dim: int) -> bool:
+    """Whether a row of a and one of b (n tokens each, as _heads describes them) share an element."""
+    between = (b[0] - a[0]) // 2
+    (_, ta, ha, na), (_, tb, hb, nb) = a, b
+    if ta == tb and (na - 1) * ha + dim <= between % ta <= ta - (nb - 1) * hb - dim:
+        return False                                     # side by side in every token: slices of one projection
+    if ta == tb and ha == hb and ta % ha == 0 and dim <= between % ha <= ha - dim:
+        return False                                     # side by side in every head
+    first = (torch.arange(n)[:, None] * ta + torch.arange(na) * ha).flatten().sort().values
+    other = (torch.arange(n)[:, None] * tb + torch.arange(nb) * hb).flatten() + between
+    after = torch.searchsorted(first, other, right=True)     # the first row that starts after each of the others
+    return bool(((after > 0) & (first[(after - 1).clamp(min=0)] + dim > other)).any()
+                or ((after < len(first)) & (first[after.clamp(max=len(first) - 1)] < other + dim)).any())
+
+
+def _span(a, n: int, dim: int):
+    return a[0], a[0] + 2 * ((n - 1) * a[1] + (a[3] - 1) * a[2] + dim)
+
+
+def _apart(name: str, out, n: int, dim: int, own, others=(), spans=()):
+    """Refuse an output that shares memory with an input or another output, where threads would write what others read.
+
+    out, own and the `others` are as _heads describes them; out may be `own`, the input of the same rows.  spans: from
+    one end to the other of a cache's pages; out lies outside them."""
+    if n == 0 or dim == 0 or out[3] == 0:
+        return
+    lo, hi = _span(out, n, dim)
+    for x in (own, *others) if out != own else others:
+        a, b = _span(x, n, dim)
+        if a < hi and lo < b and _rows_meet(out, x, n, dim):
+            raise ValueError(f"{name} shares memory with another tensor of the call")
+    for a, b in spans:
+        if a < hi and lo < b:
+            raise ValueError(f"{name} lies among the cache's pages")
+
+
 def _ints(t, name: str, ndim: int, device: int):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -188,7 +224,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     """RMS norm of each head (where its weight is given) and rotation by position (where a table is given) of
     q [tokens, q heads, head_dim] and k [tokens, k heads, head_dim] (or None) in one launch; returns (q_out, k_out).
 
-    bf16 or fp16; heads may be slices of a packed projection, outputs may be the inputs.  positions: int32 [tokens];
+    bf16 or fp16; heads may be slices of a packed projection.  q_out may be q and k_out k; they share no memory
+    otherwise.  positions: int32 [tokens];
     table: rope_table's; style "halves" (pairs i, i + rotary_dim/2) or "interleaved" (2i, 2i+1).  error: an int32
     [1] tensor that gets KT_DEVERR_BAD_POSITION for a position outside the table (that token is not written)."""
     if not isinstance(q, torch.Tensor) or q.dtype not in DTYPE_CODES or q.dim() != 3:
@@ -208,17 +245,22 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     tf = _transform(table, q_weight, k_weight, eps, style, dt, dim, dev)
     if error is not None:
         _ints(error, "error", 1, dev)
-    if q_out is None:
-        q_out = _output(q, stream)
-    else:
+    q_given, k_given = q_out is not None, k is not None and k_out is not None
+    if q_given:
         _written(q_out, "q_out")
+    else:
+        q_out = _output(q, stream)
     hqo, hko = _heads(q_out, "q_out", dt, dim, dev, n, heads), _NO_HEADS
     if k is not None:
-        if k_out is None:
-            k_out = _output(k, stream)
-        else:
+        if k_given:
             _written(k_out, "k_out")
+        else:
+            k_out = _output(k, stream)
         hko = _heads(k_out, "k_out", dt, dim, dev, n, hk[3])
+    if q_given:
+        _apart("q_out", hqo, n, dim, hq, () if k is None else (hk, hko))
+    if k_given:
+        _apart("k_out", hko, n, dim, hk, (hq, hqo))
     b = _buffer
     _NORM_CALL.pack_into(b.buf, 0, *tf, *hq, *hk, *hqo, *hko)
     at = b.at + _TRANSFORM_BYTES
@@ -256,6 +298,9 @@ class PagedKV:
         strides = [st if size > 1 else d for t in (k_pages, v_pages)
                    for st, size, d in zip(t.stride(), t.shape[:3], dense)]
         self._index = k_pages.get_device()
+        self._spans = tuple((t.data_ptr(), t.data_ptr() + 2 * (1 + sum((size - 1) * st for size, st in
+                                                                      zip(t.shape, t.stride()))))
+                            for t in (k_pages, v_pages))
         self._desc = ctypes.create_string_buffer(struct.pack(
             PAGED_KV, k_pages.data_ptr(), v_pages.data_ptr(), *strides, self.num_pages, self.page_size, self.heads,
             self.head_dim, DTYPE_CODES[self.dtype]))
@@ -305,7 +350,7 @@ class PagedKV:
                style: str = "halves", q_out: torch.Tensor | None = None, stream=None):
         """Write the step's keys k and values v [tokens, heads, head_dim] to their pages, the keys normed (k_weight)
         and rotated (table) on the way; with q [tokens, q heads, head_dim], also return it normed (q_weight) and
-        rotated.  One launch.  Tokens past cu_q[B] are left alone; options as qk_norm_rope's."""
+        rotated (q_out may be q).  One launch.  Tokens past cu_q[B] are left alone; options as qk_norm_rope's."""
         dt, dev, dim = self.dtype, self._index, self.head_dim
         hk = _heads(k, "k", dt, dim, dev, -1, self.heads)
         n = k.shape[0]
@@ -315,9 +360,11 @@ class PagedKV:
             hq = _heads(q, "q", dt, dim, dev, n, -1)
             if q_out is None:
                 q_out = _output(q, stream)
+                hqo = _heads(q_out, "q_out", dt, dim, dev, n, hq[3])
             else:
                 _written(q_out, "q_out")
-            hqo = _heads(q_out, "q_out", dt, dim, dev, n, hq[3])
+                hqo = _heads(q_out, "q_out", dt, dim, dev, n, hq[3])
+                _apart("q_out", hqo, n, dim, hq, (hk, hv), self._spans)
         tf = _transform(table, q_weight, k_weight, eps, style, dt, dim, dev)
         b = _buffer
         _APPEND_CALL.pack_into(b.buf, 0, *tf, *_batch(block_table, cu_q, seq_lens, n, dev), *hk, *hv, *hq, *hqo)
@@ -332,12 +379,12 @@ class PagedKV:
                max_q_len: int, scale: float | None = None, window: int = 0, sinks: torch.Tensor | None = None,
                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         """Attention of the step's queries q [tokens, q heads, head_dim] over their sequences' pages, causal (the
-        step's own keys are appended before); returns out of q's shape.
+        step's own keys are appended before); returns out, of q's shape and possibly q itself.
 
         max_q_len: an upper bound of the sequences' new tokens (it picks the kernel, not the result).  scale: default
         head_dim ** -0.5.  window > 0: each token sees its last `window` positions, its own among them.  sinks: f32
-        [q heads], logits added to each softmax's sum.  A token that sees no key gets zeros.  Pages that lie before every
-        token's window are not read, whatever their entries say.
+        [q heads], logits added to each softmax's sum.  A token that sees no key gets zeros.  Pages that lie before
+        every token's window are not read, whatever their entries say.
 
         A non-finite value row reaches, besides the tokens that see it, others of the sequence that share a tile with
         those; rows past a sequence's keys reach nothing."""
@@ -353,14 +400,17 @@ class PagedKV:
             sink = sinks.data_ptr()
         if out is None:
             out = _output(q, stream)
+            ho = _heads(out, "out", dt, dim, dev, n, heads)
         else:
             _written(out, "out")
+            ho = _heads(out, "out", dt, dim, dev, n, heads)
+            _apart("out", ho, n, dim, hq, (), self._spans)
         if workspace is None:
             workspace = self._workspace(stream)
         elif workspace.dtype is not torch.uint8 or workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous uint8 on {self.device}")
         b = _buffer
-        _ATTEND_CALL.pack_into(b.buf, 0, *batch, *hq, *_heads(out, "out", dt, dim, dev, n, heads))
+        _ATTEND_CALL.pack_into(b.buf, 0, *batch, *hq, *ho)
         at = b.at + _BATCH_BYTES
         _call(dev, stream, "kt_paged_attention", self._desc_at, b.at, at, at + _HEADS_BYTES, int(max_q_len),
               dim ** -0.5 if scale is None else float(scale), int(window), sink, self._err, workspace.data_ptr(),

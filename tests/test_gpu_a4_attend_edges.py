@@ -55,7 +55,7 @@ def test_weights_of_few_rows_keep_two_parts(dtype, d):
     bound = 1.01 * (R.ROUND[dtype] * want.abs() + (R.ROUND[dtype] ** 2 + 2 * off) * by_weight
                     + 2 * R.TINY[dtype] * plain) + R.TINY[dtype]
     over = (out.double().cpu() - want).abs() - bound
-    assert float(over.max()) <= 0, f"{int((over > 0).sum())} of {over.numel()} over the bound, by {float(over.max()):.2e}"
+    assert float(over.max()) <= 0, f"{int((over > 0).sum())} of {over.numel()} over the bound, {float(over.max()):.2e}"
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])

@@ -36,3 +36,48 @@ def test_error_word_is_clear_before_any_stream_uses_it():
     torch.cuda.synchronize()
     assert cache.read_error() == A.KT_DEVERR_BAD_PAGE
     assert cache.read_error() == 0
+
+
+def test_outputs_that_share_memory_are_refused():
+    """Before anything is launched: nothing is written."""
+    n, hq, hk, d, page = 6, 4, 2, 64, 16
+    qkv = torch.randn(n, hq + 2 * hk, d, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    q, k, v = qkv.split((hq, hk, hk), dim=1)
+    before, w = qkv.clone(), torch.ones(d, device=DEV)
+    kp, vp = (torch.zeros(2, page, hk, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    cache = kt.PagedKV(kp, vp)
+    step = (torch.zeros(1, 1, dtype=torch.int32, device=DEV), R.starts([n], DEV),
+            torch.full((1,), n, dtype=torch.int32, device=DEV))
+    inside = kp.view(-1, hq, d)[:n]
+    for out in (qkv[:, 1:1 + hq], qkv[:, hk:hk + hq], qkv.view(-1, hq, d)[:n]):
+        with pytest.raises(ValueError, match="q_out"):
+            kt.qk_norm_rope(q, k, q_weight=w, q_out=out)
+        with pytest.raises(ValueError, match="q_out"):
+            cache.append(k, v, *step, q=q, q_out=out)
+        with pytest.raises(ValueError, match="out"):
+            cache.attend(q, *step, n, out=out)
+    with pytest.raises(ValueError, match="k_out"):
+        kt.qk_norm_rope(q, k, q_weight=w, k_out=q[:, :hk])
+    with pytest.raises(ValueError, match="q_out"):
+        cache.append(k, v, *step, q=q, q_out=inside)
+    with pytest.raises(ValueError, match="out"):
+        cache.attend(q, *step, n, out=inside)
+    torch.cuda.synchronize()
+    assert torch.equal(qkv, before) and not bool(kp.any())
+
+
+@pytest.mark.parametrize("new,past,seqs", [(1, 5000, 1), (1, 70, 400), (90, 3000, 1), (300, 0, 9)])
+def test_attention_in_place_of_the_queries(new, past, seqs):
+    """The same bits as into another tensor, pieces of sequences joined or not."""
+    hq, hk, d, page, n = 8, 2, 64, 32, new + past
+    pages = -(-n // page)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    kp, vp = (torch.randn(seqs * pages, page, hk, d, generator=g, device=DEV).to(torch.float16) for _ in range(2))
+    qkv = torch.randn(seqs * new, hq + 2 * hk, d, generator=g, device=DEV).to(torch.float16)
+    q, rest = qkv[:, :hq], qkv[:, hq:].clone()
+    args = (torch.arange(seqs * pages, dtype=torch.int32, device=DEV).view(seqs, pages), R.starts([new] * seqs, DEV),
+            torch.full((seqs,), n, dtype=torch.int32, device=DEV), new)
+    cache = kt.PagedKV(kp, vp)
+    want = cache.attend(q, *args)
+    assert cache.attend(q, *args, out=q) is q
+    assert torch.equal(q, want) and torch.equal(qkv[:, hq:], rest) and cache.read_error() == 0
