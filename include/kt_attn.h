@@ -120,8 +120,10 @@ kt_status kt_kv_append(const kt_paged_kv* cache, const kt_paged_batch* batch, co
                        const kt_heads* q, const kt_heads* q_out, const kt_head_transform* transform, int* err,
                        void* stream);
 
-/* Workspace bytes of kt_paged_attention on the current device.  Its first
- * KT_PAGED_ATTENTION_ZEROED bytes are counters. */
+/* Workspace bytes of kt_paged_attention on the current device (40 MB on 152 SMs:
+ * partial results of two pieces of 256 query rows for each; the same for every
+ * call).  Its first KT_PAGED_ATTENTION_ZEROED bytes are counters.  Calls of one
+ * stream can share one. */
 #define KT_PAGED_ATTENTION_ZEROED 4096
 size_t kt_paged_attention_workspace_bytes(void);
 

@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import struct
 import threading
+import weakref
 
 import torch
 
@@ -276,8 +277,12 @@ class PagedKV:
 
     The tensors are checked once and stay the caller's.  `append` and `attend` report device-side conditions in an
     error word (`read_error`): KT_DEVERR_BAD_PAGE, KT_DEVERR_BAD_POSITION, of `attend` also KT_DEVERR_TIMEOUT_*; making
-    the object waits for the current stream, so that the word is clear for calls on any.  `attend` keeps one workspace
-    per stream that it is called on (while a CUDA graph is captured, one of the graph's own)."""
+    the object waits for the current stream, so that the word is clear for calls on any.  `attend` needs a workspace
+    (`workspace`): it keeps one for each stream that it is called on, which all cache objects share there.  While a CUDA
+    graph is captured, each call takes one of the graph's own and clears its counters; passing one `workspace()` to all
+    of a graph's calls leaves that out."""
+
+    _shared = weakref.WeakValueDictionary()   # (device, stream) -> workspace, kept by the objects that use it
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor):
         for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
@@ -325,7 +330,8 @@ class PagedKV:
         return code
 
     def workspace(self) -> torch.Tensor:
-        """A workspace for `attend`; calls that share one must not overlap."""
+        """A workspace for `attend` (some 40 MB: partial results of two pieces of 256 query rows for each SM, whatever
+        the cache's size); calls that share one must not overlap."""
         with torch.cuda.device(self.device):
             n = int(kt.lib().kt_paged_attention_workspace_bytes())
             ws = torch.empty(n, dtype=torch.uint8, device=self.device)
@@ -341,7 +347,10 @@ class PagedKV:
         ptr = torch._C._cuda_getCurrentRawStream(self._index)
         ws = self._workspaces.get(ptr)
         if ws is None:
-            ws = self._workspaces[ptr] = self.workspace()
+            ws = self._shared.get((self._index, ptr))   # calls on one stream do not overlap
+            if ws is None:
+                ws = self._shared[self._index, ptr] = self.workspace()
+            self._workspaces[ptr] = ws
         return ws
 
     def append(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor, cu_q: torch.Tensor,

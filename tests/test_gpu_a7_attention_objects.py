@@ -81,3 +81,33 @@ def test_attention_in_place_of_the_queries(new, past, seqs):
     want = cache.attend(q, *args)
     assert cache.attend(q, *args, out=q) is q
     assert torch.equal(q, want) and torch.equal(qkv[:, hq:], rest) and cache.read_error() == 0
+
+
+def test_caches_share_a_stream_s_workspace():
+    """One for all the layers of a model; another stream has its own; the last cache takes it along."""
+    d, page, n = 64, 16, 3000
+    pages = -(-n // page)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    made = [[torch.randn(pages, page, 1, d, generator=g, device=DEV).to(torch.bfloat16) for _ in range(2)]
+            for _ in range(4)]
+    q = torch.randn(70, 4, d, generator=g, device=DEV).to(torch.bfloat16)
+    step = (torch.arange(pages, dtype=torch.int32, device=DEV)[None], R.starts([70], DEV),
+            torch.full((1,), n, dtype=torch.int32, device=DEV), 70)
+    ws = kt.PagedKV(*made[0]).workspace()
+    want = [kt.PagedKV(*kv).attend(q, *step, workspace=ws) for kv in made]
+    size = ws.numel()
+    torch.cuda.synchronize()
+    start = torch.cuda.memory_allocated()
+    caches = [kt.PagedKV(*kv) for kv in made]
+    out = torch.empty_like(q)
+    for _ in range(2):
+        for cache, w in zip(caches, want):
+            assert torch.equal(cache.attend(q, *step, out=out), w)
+    assert size <= torch.cuda.memory_allocated() - start < 2 * size
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    caches[0].attend(q, *step, out=out, stream=side)
+    side.synchronize()
+    assert torch.equal(out, want[0]) and torch.cuda.memory_allocated() - start >= 2 * size
+    del caches, cache
+    assert torch.cuda.memory_allocated() - start < size
