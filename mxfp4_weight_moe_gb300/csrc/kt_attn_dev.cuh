@@ -78,8 +78,10 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnShape& s, int b) {
     return q;
 }
 
-// First key that a row at position pos sees.
-__device__ __forceinline__ int window_start(int pos, int window) { return window > 0 ? max(0, pos - window + 1) : 0; }
+// First key that a row at position pos sees (no difference that an int may not hold: pos can be negative).
+__device__ __forceinline__ int window_start(int pos, int window) {
+    return window > 0 && pos >= window ? pos - window + 1 : 0;
+}
 
 // Page of key `key`, -1 (reads as zeros, and says so in the error word) when the table has none there.
 __device__ __forceinline__ int checked_page(const AttnShape& s, const int32_t* pages, int key) {

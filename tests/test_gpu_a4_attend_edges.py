@@ -99,3 +99,17 @@ def test_pages_behind_the_window_are_free(new, d, page):
     out = cache.attend(q, table, R.starts([new] * len(lens), DEV), _i32(lens), new, window=window)
     assert cache.read_error() == 0
     assert bool(((out.double().cpu() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("q_lens,lens", [([8, 2], [3, 9]), ([60, 40], [30, 90])])
+def test_the_widest_window_is_none(q_lens, lens):
+    """Windows as large as an int allows, also for tokens before position 0, which see nothing."""
+    d, page = 64, 16
+    kp, vp, table = R.paged(lens, page, 1, d, torch.bfloat16, DEV, 41)
+    q = _rand(sum(q_lens), 4, d, dtype=torch.bfloat16, seed=42)
+    args = (q, table, R.starts(q_lens, DEV), _i32(lens), max(q_lens))
+    cache = kt.PagedKV(kp, vp)
+    want, bound = R.attend(q, kp, vp, table, q_lens, lens, R.softmax_scale(d))
+    for window in (2 ** 31 - 1, 2 ** 31 - 2):
+        out = cache.attend(*args, window=window)
+        assert bool(((out.double().cpu() - want).abs() <= bound).all())
