@@ -182,6 +182,11 @@ def _transform(table, q_weight, k_weight, eps: float, style: str, dtype, dim: in
     return t, positions, rot, code, qw, kw, weight_dtype, eps
 
 
+def _int(x) -> int:
+    """A count as the library's int, which wraps: the largest one for larger counts, -1 (which is refused) below 0."""
+    return min(max(int(x), -1), 0x7FFFFFFF)
+
+
 def _output(like, stream):
     """A contiguous output of like's shape that belongs to `stream` (None: the current one)."""
     if stream is None:
@@ -421,7 +426,7 @@ class PagedKV:
         b = _buffer
         _ATTEND_CALL.pack_into(b.buf, 0, *batch, *hq, *ho)
         at = b.at + _BATCH_BYTES
-        _call(dev, stream, "kt_paged_attention", self._desc_at, b.at, at, at + _HEADS_BYTES, int(max_q_len),
-              dim ** -0.5 if scale is None else float(scale), int(window), sink, self._err, workspace.data_ptr(),
+        _call(dev, stream, "kt_paged_attention", self._desc_at, b.at, at, at + _HEADS_BYTES, _int(max_q_len),
+              dim ** -0.5 if scale is None else float(scale), _int(window), sink, self._err, workspace.data_ptr(),
               workspace.numel())
         return out

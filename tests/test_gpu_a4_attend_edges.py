@@ -113,3 +113,24 @@ def test_the_widest_window_is_none(q_lens, lens):
     for window in (2 ** 31 - 1, 2 ** 31 - 2):
         out = cache.attend(*args, window=window)
         assert bool(((out.double().cpu() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_numbers_beyond_an_int(new):
+    """A window or a bound on new tokens that no int holds means what it says; negative ones are refused."""
+    d, page, n = 64, 16, 200
+    kp, vp, table = R.paged([n], page, 1, d, torch.bfloat16, DEV, 51)
+    q = _rand(new, 4, d, dtype=torch.bfloat16, seed=52)
+    args = (q, table, R.starts([new], DEV), _i32([n]))
+    cache = kt.PagedKV(kp, vp)
+    want = cache.attend(*args, new)
+    for window in (2 ** 31, 2 ** 32 + 5, 2 ** 63):
+        assert torch.equal(cache.attend(*args, new, window=window), want)
+    chunk = cache.attend(*args, 2 ** 31 - 1)
+    for most in (2 ** 31, 2 ** 32 + 1, 2 ** 63):
+        assert torch.equal(cache.attend(*args, most), chunk)
+    for wrong in (-1, -2 ** 32 + 5, -2 ** 31 - 1):
+        with pytest.raises(kt.KTError):
+            cache.attend(*args, new, window=wrong)
+        with pytest.raises(kt.KTError):
+            cache.attend(*args, wrong)
