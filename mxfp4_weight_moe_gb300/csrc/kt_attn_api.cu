@@ -5,6 +5,8 @@
 #include <cstdarg>
 #include <cstdio>
 
+#include <cudaTypedefs.h>
+
 #include "kt_attn_dev.cuh"
 
 namespace kt {
@@ -22,6 +24,36 @@ static kt_status refuse(kt_status st, const char* fmt, ...) {
 static bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 static bool is_16bit(int dtype) { return dtype == KT_DTYPE_BF16 || dtype == KT_DTYPE_FP16; }
 
+// cuTensorMapEncodeTiled by way of the runtime, so that the library needs no link to the driver's; NULL without one.
+static PFN_cuTensorMapEncodeTiled_v12000 find_encode() {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e =
+        cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+    return e == cudaSuccess && found == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p)
+               : nullptr;
+}
+
+bool encode_tiled_map(CUtensorMap* m, int dtype, const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box, CUtensorMapL2promotion promotion) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = find_encode();
+    if (!encode) return false;
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    cuuint64_t size[4] = {}, pitch[3] = {};
+    cuuint32_t part[4] = {};
+    for (int i = 0; i < rank; ++i) {
+        size[i] = dims[i];
+        part[i] = box[i];
+        if (i > 0) pitch[i - 1] = strides[i - 1];
+    }
+    const CUtensorMapDataType type =
+        dtype == KT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return encode(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), size, pitch, part, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_kv_map(CUtensorMap* m, const kt_paged_kv& kv, bool values, int box_slots) {
     const uint64_t dims[4] = {static_cast<uint64_t>(kv.head_dim), static_cast<uint64_t>(kv.page_size),
                               static_cast<uint64_t>(kv.heads), static_cast<uint64_t>(kv.num_pages)};
@@ -35,9 +67,7 @@ bool encode_kv_map(CUtensorMap* m, const kt_paged_kv& kv, bool values, int box_s
                                              : row % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
                                              : row % 64 == 0  ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
                                                               : CU_TENSOR_MAP_L2_PROMOTION_NONE;
-    return encode_tiled_map(m, kv.dtype == KT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                            values ? kv.v : kv.k, 4, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, promotion);
+    return encode_tiled_map(m, kv.dtype, values ? kv.v : kv.k, 4, dims, strides, box, promotion);
 }
 
 static kt_status check_heads(const kt_heads* h, const char* name, size_t align, int64_t step) {

@@ -52,6 +52,12 @@ inline AttnShape attn_shape(const AttnArgs& a) {
     return s;
 }
 
+// Tiled tensor map of 16-bit elements (dims and box innermost first; strides in
+// bytes for dims 1..rank-1, rank up to 4) in the 128-byte swizzle; false when it
+// cannot be encoded.
+bool encode_tiled_map(CUtensorMap* m, int dtype, const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box, CUtensorMapL2promotion promotion);
+
 // 4-D map (element, slot, head, page) of the cache's keys or values; a box is
 // 64 elements x box_slots slots of one head and page in the 128-byte swizzle.
 // Elements past head_dim and pages outside the cache read as zeros.

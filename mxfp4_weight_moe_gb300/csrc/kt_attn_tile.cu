@@ -998,9 +998,7 @@ static kt_status launch_tile_typed(const AttnArgs& a, cudaStream_t s) {
                             static_cast<uint64_t>(a.batch.tokens)};
     const uint64_t qs[2] = {2 * static_cast<uint64_t>(a.q.head_stride), 2 * static_cast<uint64_t>(a.q.token_stride)};
     const uint32_t qb[3] = {64, static_cast<uint32_t>(p.sh.group), static_cast<uint32_t>(p.geo.tokens)};
-    if (!encode_tiled_map(&qmap, a.kv.dtype == KT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                          a.q.ptr, 3, qd, qs, qb, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+    if (!encode_tiled_map(&qmap, a.kv.dtype, a.q.ptr, 3, qd, qs, qb, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
         !encode_kv_map(&kmap, a.kv, false, p.geo.box_slots) || !encode_kv_map(&vmap, a.kv, true, p.geo.box_slots))
         return report(KT_ERR_CUDA, "tensor map encoding failed");
     static bool attr_set[64] = {};

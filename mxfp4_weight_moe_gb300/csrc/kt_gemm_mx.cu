@@ -1364,8 +1364,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // tiled map of rank 2-5 (dims/box innermost first; strides in bytes for dims 1..rank-1)
 constexpr int kMaxMapRank = 5;
 static bool encode(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
-                   const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw,
-                   CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
+                   const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw) {
     auto fn = encode_fn();
     if (!fn || rank < 1 || rank > kMaxMapRank) return false;
     cuuint64_t d[kMaxMapRank], st[kMaxMapRank - 1];
@@ -1376,13 +1375,8 @@ static bool encode(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int
     }
     for (int i = 0; i < rank - 1; ++i) st[i] = strides[i];
     return fn(m, dt, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, st, b, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, sw, promotion,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-bool encode_tiled_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
-                      const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw,
-                      CUtensorMapL2promotion promotion) {
-    return encode(m, dt, base, rank, dims, strides, box, sw, promotion);
 }
 
 // Largest cluster size (up to `want`) whose co-resident clusters of one CTA

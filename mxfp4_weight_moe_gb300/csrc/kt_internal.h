@@ -156,12 +156,6 @@ struct DecodeInputs {
 };
 kt_status launch_decode(const GemmArgs& fc1, const GemmArgs& fc2, const DecodeInputs& in, cudaStream_t s);
 
-// Tiled tensor map of rank 2-5 (dims and box innermost first; strides in bytes
-// for dims 1..rank-1); false when it cannot be encoded.
-bool encode_tiled_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
-                      const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle sw,
-                      CUtensorMapL2promotion promotion);
-
 // Device properties cached per device.
 int sm_count();
 
