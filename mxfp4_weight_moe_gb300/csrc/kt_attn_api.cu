@@ -180,7 +180,7 @@ static bool wide_rows(const HeadRowsParams& p) {
 }
 
 static bool too_many_rows(const HeadRowsParams& p) {
-    // 32 lanes at most per row, 256 threads a block, 31 bits of blocks and of units
+    // 32 lanes at most a row, and 31 bits of threads
     return static_cast<long long>(p.tokens) * (p.seg[0].heads + p.seg[1].heads + p.seg[2].heads) > INT_MAX / 32;
 }
 

@@ -21,13 +21,14 @@
 // unnormalised output) in the workspace, and the CTA that finishes last joins
 // them in order, so the result does not depend on which one that was.
 //
-// Measured on GB300 (bf16): 64 single tokens after up to 8191, 64 / 8 heads of
-// 128 (1.31 GB of cache), 211 us, 6.23 TB/s (92 % of the measured copy rate); 4
-// after up to 131071, heads of 64 (0.59 GB), 109 us, 5.39 TB/s, of which about 10
-// us are the launch, the plan and the join.  One token after 500 keys: 10 us, of
-// which 0.5 launch, 1.7 plan, 1.7 first look-ups and loads, 2 the keys, 3.5 the
-// pieces' join; after 60 (no join) 6 us.  L2 promotion past a head's row (256
-// bytes for rows of 128) read 1.39 times the cache.
+// Measured on GB300, machines differing: 64 single tokens after up to 8191, bf16,
+// 64 / 8 heads of 128 (1.31 GB of cache), 208 to 216 us, 6.1 to 6.3 TB/s (90 to 93 %
+// of the measured copy rate); 4 after up to 131071, fp16, heads of 64 (0.59 GB), 109
+// to 119 us, 4.9 to 5.4 TB/s, of which about 10 us are the launch, the plan and the
+// join.  One token after 500 keys: 10.3 us, of which 0.5 launch, 1.7 plan, 1.7 first
+// look-ups and loads, 2 the keys, 3.5 the pieces' join (timed when it took 10.0);
+// after 60 (no join) 6.1 us.  L2 promotion past a head's row (256 bytes for rows of
+// 128) read 1.39 times the cache.
 #include <algorithm>
 #include <type_traits>
 

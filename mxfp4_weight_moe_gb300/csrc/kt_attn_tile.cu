@@ -14,7 +14,10 @@
 // rescaling of O (by the row's own thread) is rare, and the sums stay exact in
 // fp32 (P up to 2^8 rounds with the same relative error, and fp16 holds it).
 // P is rounded to the element type because the tensor cores multiply it with V
-// in that type; the sum that divides O is of the unrounded weights.
+// in that type (once: a second product with what the rounding left would add half
+// of their work again, and they are what heads of 128 wait for); the sum that
+// divides O is of the unrounded weights.  Error against 64 bits: 1.1 to 1.4 times
+// that of rounding the exact result once.
 //
 // Work is dealt to one CTA per SM: all items' key tiles (and two more each, what
 // an item costs besides: 1 to 5 measured, 2 fastest) form one line that is cut
@@ -30,9 +33,10 @@
 // issue and exponential unit for the two warps of a scheduler, measured alone).
 // Measured on GB300 (bf16): an 8192-token prompt, 64 / 8 heads of 128, 670 us on
 // the fastest machine (1640 TFLOP/s, 85 % of the measured burst matmul rate, 96 %
-// of the sustained one), up to 790 us on others; heads of 64, 600 us, 916
-// TFLOP/s; 2048 tokens after 30001 on 16-slot pages (fp16, 32 / 8 heads of 128)
-// 652 to 702 us, 1480 to 1600 TFLOP/s.
+// of the sustained one), up to 790 us on others; heads of 64, 600 to 652 us, 842 to
+// 916 TFLOP/s; 2048 tokens after 30001 on 16-slot pages (fp16, 32 / 8 heads of 128)
+// 652 to 702 us, 1480 to 1600 TFLOP/s (757 us in seconds of calls, under the power
+// cap at 1537 MHz).
 //
 // Tried and left out (8192-token prompt): P beside S so that the next S comes
 // early (heads of 64: 636 against 614 us, both groups then contend for the

@@ -146,7 +146,7 @@ __device__ __forceinline__ TokenPlace place_of(const HeadRowsParams& p, int toke
 
 // Four heads a group and six blocks of 128 threads on an SM: measured on 8192 tokens of 64 + 8 heads of 128 (302 MB of
 // rows) with norms, 54.1 us (49.9 us, 6.1 TB/s, with the rows marked to leave L2); two heads 58 to 62 us, three 56.3,
-// six 56.7, fewer blocks 57.6.
+// six 56.7, fewer blocks 57.6.  (With norms, six blocks cost 44 bytes of spills a thread.)
 constexpr int kRowThreads = 128, kRowBlocks = 6, kRowHeads = 4;
 constexpr int kNoNorm = 0, kWeightsTyped = 1, kWeightsF32 = 2;
 
