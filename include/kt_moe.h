@@ -253,6 +253,26 @@ kt_status kt_mxfp4_moe_forward_routed(const uint16_t* hidden, int T, int H,
                                       const kt_moe_options* opts, void* stream);
 
 /*
+ * The forward on tokens that are MXFP8 already, as kt_add_rms_norm (kt_norm.h)
+ * writes them or an 8-bit dispatch delivers them: codes e4m3 [T, H] (16-byte
+ * aligned) and scales e8m0 [T, H/32] (4-byte aligned) in place of hidden.  They
+ * are used as they are (the layer's own quantisation becomes a copy to the
+ * permuted rows), so results are bit-identical to kt_mxfp4_moe_forward_ex on
+ * bf16 tokens whose quantisation these are.  expert_offsets, perm and inv_perm:
+ * all three as for kt_mxfp4_moe_forward_routed, or all NULL (derived from
+ * topk_ids).  Other arguments, limits, ownership and errors as
+ * kt_mxfp4_moe_forward_ex.
+ */
+kt_status kt_mxfp4_moe_forward_mx(const uint8_t* codes, const uint8_t* scales, int T, int H,
+                                  const int32_t* topk_ids, const float* topk_w, int k,
+                                  const int32_t* expert_offsets, const int32_t* perm,
+                                  const int32_t* inv_perm,
+                                  const uint8_t* w13, const uint8_t* w13_sf,
+                                  const uint8_t* w2, const uint8_t* w2_sf, int E, int I,
+                                  uint16_t* out, void* ws, size_t ws_bytes,
+                                  const kt_moe_options* opts, void* stream);
+
+/*
  * Single-launch decode: routing, permutation and the layer forward in ONE
  * kernel launch, for decode-sized batches (T * k <= KT_DECODE_MAX_SLOTS).
  * It computes exactly what kt_moe_route_permute followed by

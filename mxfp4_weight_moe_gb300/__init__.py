@@ -1,7 +1,8 @@
 """GB300 (sm_103a) fused MXFP4-weight mixture-of-experts layer.
 
 Thin Python binding over the C ABI in ``include/kt_moe.h`` and, for the attention
-operators in front of the layer (``attention.py``), ``include/kt_attn.h`` (library
+operators in front of the layer (``attention.py``), ``include/kt_attn.h``, for
+the norm between the two (``norm.py``), ``include/kt_norm.h`` (library
 ``_build/libkt_moe.so``, built by ``build_ext.build``).  Every step of the
 layer runs in the library's CUDA kernels; this module only checks shapes,
 allocates outputs/workspaces with torch and passes raw device pointers and
@@ -26,7 +27,7 @@ __all__ = [
     "KTError", "lib", "route_permute", "forward", "workspace_bytes", "workspace_layout", "read_device_error",
     "grouped_gemm_f32", "Layerwise", "status_string", "check_fc_shapes", "kernel_launches", "profile_enable",
     "profile_read", "STAGES", "route_permute_noalloc", "decode", "DECODE_MAX_SLOTS", "MoeLayer",
-    "PagedKV", "qk_norm_rope", "rope_table",
+    "PagedKV", "qk_norm_rope", "rope_table", "add_rms_norm",
 ]
 
 KT_OK = 0
@@ -72,6 +73,8 @@ _SIGNATURES = {
                                  ctypes.POINTER(MoeOptions), _VP], _I),
     "kt_mxfp4_moe_forward_routed": ([_VP, _I, _I, _VP, _VP, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _VP,
                                      _VP, _SZ, ctypes.POINTER(MoeOptions), _VP], _I),
+    "kt_mxfp4_moe_forward_mx": ([_VP, _VP, _I, _I, _VP, _VP, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _VP,
+                                 _VP, _SZ, ctypes.POINTER(MoeOptions), _VP], _I),
     "kt_mxfp4_moe_decode": ([_VP, _VP, _I, _I, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ,
                              ctypes.POINTER(MoeOptions), _VP], _I),
     "kt_moe_workspace_layout": ([_I, _I, _I, _I, _I, ctypes.POINTER(WsLayout)], _I),
@@ -114,7 +117,7 @@ def lib(build_if_missing: bool = True):
         if _lib is None:
             path = build_ext.build() if build_if_missing else build_ext.LIB_PATH
             L = ctypes.CDLL(path)
-            for name, (args, res) in {**_SIGNATURES, **attention.SIGNATURES}.items():
+            for name, (args, res) in {**_SIGNATURES, **attention.SIGNATURES, **norm.SIGNATURES}.items():
                 fn = getattr(L, name)
                 fn.argtypes = args
                 fn.restype = res
@@ -250,20 +253,42 @@ def route_permute(logits: torch.Tensor, k: int, renormalize: bool = True, stream
     return ids, w, offsets, perm, inv
 
 
-def forward(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, w13: torch.Tensor,
+def _mx_tokens(tokens, H: int, T: int, device=None):
+    """(codes, scales) of MXFP8 tokens, checked against T tokens of hidden size H (T < 0: any)."""
+    if len(tokens) != 2:
+        raise TypeError("MXFP8 tokens are a pair (codes, scales)")
+    codes, scales = tokens
+    _need(codes, "codes", torch.uint8, 2, device)
+    _need(scales, "scales", torch.uint8, 2, codes.device)
+    if T < 0:
+        T = codes.shape[0]
+    if codes.shape != (T, H) or scales.shape != (T, H // 32):
+        raise ValueError(f"codes {tuple(codes.shape)} and scales {tuple(scales.shape)} must be [{T}, {H}] and "
+                         f"[{T}, {H // 32}]")
+    return codes, scales
+
+
+def forward(hidden: torch.Tensor | tuple, topk_ids: torch.Tensor, topk_w: torch.Tensor, w13: torch.Tensor,
             w13_sf: torch.Tensor, w2: torch.Tensor, w2_sf: torch.Tensor, out: torch.Tensor | None = None,
             workspace: torch.Tensor | None = None, stream=None, gate_up: str = "halves",
             activation: str = "swiglu", alpha: float = 1.702, limit: float = 7.0,
             routing: tuple | None = None) -> torch.Tensor:
     """One fused MoE layer forward; returns out (bf16 [T, H]).
 
+    hidden: bf16 [T, H], or tokens that are MXFP8 already, as a pair (codes
+    uint8 e4m3 [T, H], scales uint8 e8m0 [T, H/32]), which are used as they
+    are (kt_mxfp4_moe_forward_mx; add_rms_norm writes them).
     gate_up "halves" (w13 rows [0, I) gate, [I, 2I) up) or "interleaved"
     (row 2i gate i, row 2i+1 up i); activation "swiglu" (silu(g) * u) or
     "swiglu_clamped" (the clamped SwiGLU of GPT-OSS-format checkpoints, with
     alpha and limit; see kt_moe_options in kt_moe.h).  routing: the
     (expert_offsets, perm, inv_perm) that route_permute returned for these
     topk_ids, reused instead of re-derived (kt_mxfp4_moe_forward_routed)."""
-    _need(hidden, "hidden", torch.bfloat16, 2)
+    mx = isinstance(hidden, (tuple, list))
+    if mx:
+        hidden, scales = _mx_tokens(hidden, 2 * w13.shape[-1], -1)
+    else:
+        _need(hidden, "hidden", torch.bfloat16, 2)
     dev = hidden.device
     _need(topk_ids, "topk_ids", torch.int32, 2, dev)
     _need(topk_w, "topk_w", torch.float32, 2, dev)
@@ -291,6 +316,9 @@ def forward(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, 
         if gate_up not in GATE_UP_LAYOUTS or activation not in ACTIVATIONS:
             raise ValueError(f"gate_up must be one of {GATE_UP_LAYOUTS} and activation one of {ACTIVATIONS}")
         opts = MoeOptions(GATE_UP_LAYOUTS.index(gate_up), ACTIVATIONS.index(activation), float(alpha), float(limit))
+        if mx:
+            return _forward_mx(hidden, scales, topk_ids, topk_w, (offsets, perm, inv_perm), w13, w13_sf, w2, w2_sf, out,
+                               workspace, opts, stream)
         with _on_device(dev):
             _check(lib().kt_mxfp4_moe_forward_routed(_ptr(hidden), T, H, _ptr(topk_ids), _ptr(topk_w), k,
                                                      _ptr(offsets), _ptr(perm), _ptr(inv_perm), _ptr(w13),
@@ -299,7 +327,7 @@ def forward(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, 
                                                      _stream_ptr(stream, dev)),
                    "kt_mxfp4_moe_forward_routed")
         return out
-    if gate_up == "halves" and activation == "swiglu":
+    if gate_up == "halves" and activation == "swiglu" and not mx:
         with _on_device(dev):
             _check(lib().kt_mxfp4_moe_forward(_ptr(hidden), T, H, _ptr(topk_ids), _ptr(topk_w), k, _ptr(w13),
                                               _ptr(w13_sf), _ptr(w2), _ptr(w2_sf), E, I, _ptr(out),
@@ -309,11 +337,26 @@ def forward(hidden: torch.Tensor, topk_ids: torch.Tensor, topk_w: torch.Tensor, 
     if gate_up not in GATE_UP_LAYOUTS or activation not in ACTIVATIONS:
         raise ValueError(f"gate_up must be one of {GATE_UP_LAYOUTS} and activation one of {ACTIVATIONS}")
     opts = MoeOptions(GATE_UP_LAYOUTS.index(gate_up), ACTIVATIONS.index(activation), float(alpha), float(limit))
+    if mx:
+        return _forward_mx(hidden, scales, topk_ids, topk_w, (None, None, None), w13, w13_sf, w2, w2_sf, out, workspace,
+                           opts, stream)
     with _on_device(dev):
         _check(lib().kt_mxfp4_moe_forward_ex(_ptr(hidden), T, H, _ptr(topk_ids), _ptr(topk_w), k, _ptr(w13),
                                              _ptr(w13_sf), _ptr(w2), _ptr(w2_sf), E, I, _ptr(out), _ptr(workspace),
                                              workspace.numel(), ctypes.byref(opts), _stream_ptr(stream, dev)),
                "kt_mxfp4_moe_forward_ex")
+    return out
+
+
+def _forward_mx(codes, scales, topk_ids, topk_w, routing, w13, w13_sf, w2, w2_sf, out, workspace, opts, stream):
+    E, I, H = check_fc_shapes(w13, w2)
+    T, k = topk_ids.shape
+    dev = codes.device
+    with _on_device(dev):
+        _check(lib().kt_mxfp4_moe_forward_mx(_ptr(codes), _ptr(scales), T, H, _ptr(topk_ids), _ptr(topk_w), k,
+                                             *[_ptr(t) for t in routing], _ptr(w13), _ptr(w13_sf), _ptr(w2),
+                                             _ptr(w2_sf), E, I, _ptr(out), _ptr(workspace), workspace.numel(),
+                                             ctypes.byref(opts), _stream_ptr(stream, dev)), "kt_mxfp4_moe_forward_mx")
     return out
 
 
@@ -422,7 +465,7 @@ class MoeLayer:
     only the step's own tensors are
     checked and marshalled; workspaces and routing buffers are kept per T.
     Results are those of route_permute + forward (or decode) with the same
-    options.  Returns (out, topk_ids, topk_w); the three are reused by the
+    options.  hidden: as forward's (MXFP8 pairs: not with single_launch).  Returns (out, topk_ids, topk_w); the three are reused by the
     next call with the same T unless `out` is given."""
 
     def __init__(self, w13: torch.Tensor, w13_sf: torch.Tensor, w2: torch.Tensor, w2_sf: torch.Tensor, k: int,
@@ -464,11 +507,16 @@ class MoeLayer:
             self._per_T[T] = b
         return b
 
-    def __call__(self, hidden: torch.Tensor, logits: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+    def __call__(self, hidden: torch.Tensor | tuple, logits: torch.Tensor, out: torch.Tensor | None = None, stream=None):
+        scales = None
+        if isinstance(hidden, (tuple, list)):
+            if self._single_launch:
+                raise ValueError("a single launch quantises its tokens itself: hidden must be bf16")
+            hidden, scales = _mx_tokens(hidden, self.H, -1, self.device)
         T = hidden.shape[0]
-        if (hidden.dtype != torch.bfloat16 or logits.dtype != torch.float32 or hidden.shape != (T, self.H)
+        if ((scales is None and hidden.dtype != torch.bfloat16) or (logits.dtype != torch.float32 or hidden.shape != (T, self.H)
                 or logits.shape != (T, self.E) or hidden.get_device() != self._dev_idx
-                or logits.get_device() != self._dev_idx or not hidden.is_contiguous() or not logits.is_contiguous()):
+                or logits.get_device() != self._dev_idx or not hidden.is_contiguous() or not logits.is_contiguous())):
             raise ValueError(f"hidden must be contiguous bf16 [T, {self.H}] and logits contiguous f32 [T, {self.E}] "
                              f"on {self.device}")
         decode, ws, route, rws, own_out = self._buffers(T)
@@ -480,10 +528,10 @@ class MoeLayer:
         ids, w, offs, perm, inv = route
         with _on_device(self.device):
             self._launch(T, hidden, logits, out, decode, ws, ids, w, offs, perm, inv, rws,
-                         _stream_ptr(stream, self.device))
+                         _stream_ptr(stream, self.device), scales)
         return out, ids, w
 
-    def _launch(self, T, hidden, logits, out, decode, ws, ids, w, offs, perm, inv, rws, sp):
+    def _launch(self, T, hidden, logits, out, decode, ws, ids, w, offs, perm, inv, rws, sp, scales=None):
         w13, w13_sf, w2, w2_sf = self._wp
         L = lib()
         if decode:
@@ -495,6 +543,13 @@ class MoeLayer:
             _check(L.kt_moe_route_permute(logits.data_ptr(), T, self.E, self.k, self.renormalize, ids.data_ptr(),
                                           w.data_ptr(), offs.data_ptr(), perm.data_ptr(), inv.data_ptr(),
                                           rws.data_ptr(), rws.numel(), sp), "kt_moe_route_permute")
+            if scales is not None:
+                _check(L.kt_mxfp4_moe_forward_mx(hidden.data_ptr(), scales.data_ptr(), T, self.H, ids.data_ptr(),
+                                                 w.data_ptr(), self.k, offs.data_ptr(), perm.data_ptr(),
+                                                 inv.data_ptr(), w13, w13_sf, w2, w2_sf, self.E, self.I,
+                                                 out.data_ptr(), ws.data_ptr(), ws.numel(), self._optsref, sp),
+                       "kt_mxfp4_moe_forward_mx")
+                return
             _check(L.kt_mxfp4_moe_forward_routed(hidden.data_ptr(), T, self.H, ids.data_ptr(), w.data_ptr(), self.k,
                                                  offs.data_ptr(), perm.data_ptr(), inv.data_ptr(), w13, w13_sf, w2,
                                                  w2_sf, self.E, self.I, out.data_ptr(), ws.data_ptr(), ws.numel(),
@@ -586,5 +641,6 @@ class Layerwise:
             pass
 
 
-from . import attention  # noqa: E402 - needs the helpers above
+from . import attention, norm  # noqa: E402 - need the helpers above
 from .attention import PagedKV, qk_norm_rope, rope_table  # noqa: E402
+from .norm import add_rms_norm  # noqa: E402

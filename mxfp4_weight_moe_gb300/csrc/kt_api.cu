@@ -193,10 +193,17 @@ kt_status kt_mxfp4_moe_forward(const uint16_t* hidden, int T, int H, const int32
                                    nullptr, stream);
 }
 
+// Tokens of a forward: bf16 rows, or (bf16 == NULL) MXFP8 codes and scales.
+struct ForwardTokens {
+    const uint16_t* bf16;
+    const uint8_t* codes;
+    const uint8_t* scales;
+};
+
 // The forward behind kt_mxfp4_moe_forward_ex (routed == false: the permutation is derived here from
-// topk_ids) and kt_mxfp4_moe_forward_routed (routed == true: r_offsets / r_perm / r_inv_perm are the
-// routing call's outputs).
-static kt_status forward_impl(const uint16_t* hidden, int T, int H, const int32_t* topk_ids, const float* topk_w,
+// topk_ids), kt_mxfp4_moe_forward_routed (routed == true: r_offsets / r_perm / r_inv_perm are the
+// routing call's outputs) and kt_mxfp4_moe_forward_mx.
+static kt_status forward_impl(const ForwardTokens& tokens, int T, int H, const int32_t* topk_ids, const float* topk_w,
                               int k, bool routed, const int32_t* r_offsets, const int32_t* r_perm,
                               const int32_t* r_inv_perm, const uint8_t* w13, const uint8_t* w13_sf,
                               const uint8_t* w2, const uint8_t* w2_sf, int E, int I, uint16_t* out, void* ws,
@@ -219,12 +226,16 @@ static kt_status forward_impl(const uint16_t* hidden, int T, int H, const int32_
     if (static_cast<long long>(E) * 2 * I > INT_MAX / 2 || static_cast<long long>(E) * H > INT_MAX / 2)
         return fail(KT_ERR_UNSUPPORTED_SHAPE, "E*2I or E*H too large");
     if (T == 0) return KT_OK;
-    if (!hidden || !topk_ids || !topk_w || !w13 || !w13_sf || !w2 || !w2_sf || !out || !ws)
+    const uint16_t* hidden = tokens.bf16;
+    if ((!hidden && (!tokens.codes || !tokens.scales)) || !topk_ids || !topk_w || !w13 || !w13_sf || !w2 || !w2_sf ||
+        !out || !ws)
         return fail(KT_ERR_INVALID_ARG, "null pointer argument");
     if (routed && (!r_offsets || !r_perm || !r_inv_perm))
         return fail(KT_ERR_INVALID_ARG, "null routing array (expert_offsets, perm, inv_perm)");
     if (!aligned(hidden, 16) || !aligned(out, 16) || !aligned(topk_ids, 16) || !aligned(topk_w, 16))
         return fail(KT_ERR_ALIGNMENT, "hidden, out, topk_ids and topk_w must be 16-byte aligned");
+    if (!aligned(tokens.codes, 16) || !aligned(tokens.scales, 4))
+        return fail(KT_ERR_ALIGNMENT, "codes must be 16-byte and scales 4-byte aligned");
     if (routed && (!aligned(r_offsets, 16) || !aligned(r_perm, 16) || !aligned(r_inv_perm, 16)))
         return fail(KT_ERR_ALIGNMENT, "expert_offsets, perm and inv_perm must be 16-byte aligned");
     if (!aligned(w13, 32) || !aligned(w2, 32))
@@ -262,9 +273,12 @@ static kt_status forward_impl(const uint16_t* hidden, int T, int H, const int32_
     {
         // on a given routing, the quantiser's launch also derives the per-expert chunk counts
         StageTimer timer(KT_STAGE_QUANT, s);
-        if ((st = cuda_status(launch_quant_scatter(hidden, T, H, k, inv_perm, a1, a1_sf, sf_rows(S), s,
-                                                   routed ? offsets : nullptr, E, chunk_prefix))) != KT_OK)
-            return st;
+        const int32_t* counted = routed ? offsets : nullptr;
+        const cudaError_t e = hidden ? launch_quant_scatter(hidden, T, H, k, inv_perm, a1, a1_sf, sf_rows(S), s,
+                                                            counted, E, chunk_prefix)
+                                     : launch_scatter_mx(tokens.codes, tokens.scales, T, H, k, inv_perm, a1, a1_sf,
+                                                         sf_rows(S), s, counted, E, chunk_prefix);
+        if ((st = cuda_status(e)) != KT_OK) return st;
     }
 
     GemmArgs fc1{};
@@ -323,7 +337,7 @@ kt_status kt_mxfp4_moe_forward_ex(const uint16_t* hidden, int T, int H, const in
                                   const float* topk_w, int k, const uint8_t* w13, const uint8_t* w13_sf,
                                   const uint8_t* w2, const uint8_t* w2_sf, int E, int I, uint16_t* out, void* ws,
                                   size_t ws_bytes, const kt_moe_options* opts, void* stream) {
-    return forward_impl(hidden, T, H, topk_ids, topk_w, k, false, nullptr, nullptr, nullptr, w13, w13_sf, w2, w2_sf,
+    return forward_impl({hidden, nullptr, nullptr}, T, H, topk_ids, topk_w, k, false, nullptr, nullptr, nullptr, w13, w13_sf, w2, w2_sf,
                         E, I, out, ws, ws_bytes, opts, stream);
 }
 
@@ -332,8 +346,18 @@ kt_status kt_mxfp4_moe_forward_routed(const uint16_t* hidden, int T, int H, cons
                                       const int32_t* inv_perm, const uint8_t* w13, const uint8_t* w13_sf,
                                       const uint8_t* w2, const uint8_t* w2_sf, int E, int I, uint16_t* out, void* ws,
                                       size_t ws_bytes, const kt_moe_options* opts, void* stream) {
-    return forward_impl(hidden, T, H, topk_ids, topk_w, k, true, expert_offsets, perm, inv_perm, w13, w13_sf, w2,
-                        w2_sf, E, I, out, ws, ws_bytes, opts, stream);
+    return forward_impl({hidden, nullptr, nullptr}, T, H, topk_ids, topk_w, k, true, expert_offsets, perm, inv_perm,
+                        w13, w13_sf, w2, w2_sf, E, I, out, ws, ws_bytes, opts, stream);
+}
+
+kt_status kt_mxfp4_moe_forward_mx(const uint8_t* codes, const uint8_t* scales, int T, int H, const int32_t* topk_ids,
+                                  const float* topk_w, int k, const int32_t* expert_offsets, const int32_t* perm,
+                                  const int32_t* inv_perm, const uint8_t* w13, const uint8_t* w13_sf,
+                                  const uint8_t* w2, const uint8_t* w2_sf, int E, int I, uint16_t* out, void* ws,
+                                  size_t ws_bytes, const kt_moe_options* opts, void* stream) {
+    const bool routed = expert_offsets || perm || inv_perm;
+    return forward_impl({nullptr, codes, scales}, T, H, topk_ids, topk_w, k, routed, expert_offsets, perm, inv_perm,
+                        w13, w13_sf, w2, w2_sf, E, I, out, ws, ws_bytes, opts, stream);
 }
 
 kt_status kt_mxfp4_moe_decode(const float* logits, const uint16_t* hidden, int T, int H, int E, int k, int I,

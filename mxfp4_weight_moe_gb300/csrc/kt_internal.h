@@ -84,6 +84,10 @@ cudaError_t launch_chunk_prefix(const int32_t* expert_offsets, int E, int32_t* c
 cudaError_t launch_quant_scatter(const uint16_t* hidden, int T, int H, int k, const int32_t* inv_perm, uint8_t* a1,
                                  uint8_t* a1_sf, int S4, cudaStream_t s, const int32_t* offsets = nullptr, int E = 0,
                                  int32_t* chunk_prefix = nullptr);
+// The same for tokens that are MXFP8 already (codes [T, H], scales [T, H/32]).
+cudaError_t launch_scatter_mx(const uint8_t* codes, const uint8_t* scales, int T, int H, int k,
+                              const int32_t* inv_perm, uint8_t* a1, uint8_t* a1_sf, int S4, cudaStream_t s,
+                              const int32_t* offsets, int E, int32_t* chunk_prefix);
 // Plain [S, K/32] scale bytes -> K-step-major layout (diagnostic GEMM entry).
 cudaError_t launch_sf_to_kstep_major(const uint8_t* plain, int S, int K, uint8_t* out, int S4, cudaStream_t s);
 // out[t] = sum over valid slots of y[t*k + j] (y already weighted).
