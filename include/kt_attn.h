@@ -58,6 +58,30 @@ typedef struct kt_paged_kv {
 } kt_paged_kv;
 
 /*
+ * The same in 8 bits: e4m3 numbers with a power of two for each block of
+ * KT_KV8_BLOCK slots and head.  Slot s of page p of head h is the row of bytes
+ * k + p*k_page_stride + s*k_slot_stride + h*k_head_stride; an element stands for
+ * e4m3(code) * 2^(scale - 127) with scale = k_scales[(p * page_size / KT_KV8_BLOCK +
+ * s / KT_KV8_BLOCK) * heads + h] (e8m0; dense); a scale of 255 makes the whole block
+ * NaN, the codes 0x7f and 0xff are not used otherwise.  page_size is a multiple of 16, head_dim a multiple of 16 up to 128; rows are 16-byte aligned,
+ * strides positive multiples of 16 bytes.  dtype: the type of the keys, values and
+ * queries that come in and of the output; kt_kv8_append keeps exponents with which
+ * every element is a number of that type and attention's fp32 sums are finite
+ * (2^-117 to 2^87 for bf16, 2^-14 to 2^7 for fp16): larger numbers saturate.
+ */
+#define KT_KV8_BLOCK 16
+typedef struct kt_paged_kv8 {
+    uint8_t* k;
+    uint8_t* v;
+    uint8_t* k_scales;
+    uint8_t* v_scales;
+    int64_t k_page_stride, k_slot_stride, k_head_stride;
+    int64_t v_page_stride, v_slot_stride, v_head_stride;
+    int num_pages, page_size, heads, head_dim;
+    int dtype;
+} kt_paged_kv8;
+
+/*
  * One step's sequences.  Sequence b has the tokens [cu_q[b], cu_q[b+1]) of the
  * step (possibly none) and seq_lens[b] keys in all, the step's own included:
  * its token t has position seq_lens[b] - cu_q[b+1] + t.  Position p lies in slot
@@ -120,6 +144,23 @@ kt_status kt_kv_append(const kt_paged_kv* cache, const kt_paged_batch* batch, co
                        const kt_heads* q, const kt_heads* q_out, const kt_head_transform* transform, int* err,
                        void* stream);
 
+/*
+ * kt_kv_append to an 8-bit cache.  A block is KT_KV8_BLOCK consecutive positions
+ * of a sequence from a multiple of it.  Of each block that gets new tokens, and
+ * each head, keys and values by themselves, the exponent X is the least with
+ * amax <= 448 * 2^X over the new tokens (fp32 keys after norm and rotation), within
+ * the cache dtype's range; codes are x * 2^-X rounded once to nearest even,
+ * saturating.  A block that has older tokens keeps its exponent if that is larger;
+ * if X is, its older codes are rescaled (exact but for numbers that become e4m3
+ * subnormals, which round).  An element that is not finite makes its block NaN (scale
+ * 255), until the block is begun anew.  No two sequences of a step append to one block.
+ * rotary_dim is a multiple of 16; k, v: 16-byte aligned, strides multiples of 8
+ * elements; otherwise as kt_kv_append.
+ */
+kt_status kt_kv8_append(const kt_paged_kv8* cache, const kt_paged_batch* batch, const kt_heads* k, const kt_heads* v,
+                        const kt_heads* q, const kt_heads* q_out, const kt_head_transform* transform, int* err,
+                        void* stream);
+
 /* Workspace bytes of kt_paged_attention on the current device (40 MB on 152 SMs:
  * partial results of two pieces of 256 query rows for each; the same for every
  * call).  Its first KT_PAGED_ATTENTION_ZEROED bytes are counters.  Calls of one
@@ -147,6 +188,15 @@ size_t kt_paged_attention_workspace_bytes(void);
 kt_status kt_paged_attention(const kt_paged_kv* cache, const kt_paged_batch* batch, const kt_heads* q,
                              const kt_heads* out, int max_q_len, float scale, int window, const float* sinks, int* err,
                              void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * kt_paged_attention over an 8-bit cache: keys and values are the numbers that the
+ * codes and scales stand for, exact in the element type where kt_kv8_append wrote
+ * them; the same workspace, arguments and results otherwise.
+ */
+kt_status kt_paged_attention8(const kt_paged_kv8* cache, const kt_paged_batch* batch, const kt_heads* q,
+                              const kt_heads* out, int max_q_len, float scale, int window, const float* sinks,
+                              int* err, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

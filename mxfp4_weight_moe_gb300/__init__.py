@@ -27,7 +27,7 @@ __all__ = [
     "KTError", "lib", "route_permute", "forward", "workspace_bytes", "workspace_layout", "read_device_error",
     "grouped_gemm_f32", "Layerwise", "status_string", "check_fc_shapes", "kernel_launches", "profile_enable",
     "profile_read", "STAGES", "route_permute_noalloc", "decode", "DECODE_MAX_SLOTS", "MoeLayer",
-    "PagedKV", "qk_norm_rope", "rope_table", "add_rms_norm",
+    "PagedKV", "PagedKV8", "qk_norm_rope", "rope_table", "add_rms_norm",
 ]
 
 KT_OK = 0
@@ -642,5 +642,5 @@ class Layerwise:
 
 
 from . import attention, norm  # noqa: E402 - need the helpers above
-from .attention import PagedKV, qk_norm_rope, rope_table  # noqa: E402
+from .attention import PagedKV, PagedKV8, qk_norm_rope, rope_table  # noqa: E402
 from .norm import add_rms_norm  # noqa: E402

@@ -3,9 +3,9 @@
 ``qk_norm_rope`` norms and rotates query and key heads; ``PagedKV`` is a cache
 in pages, whose ``append`` writes a step's keys (normed and rotated on the way)
 and values and whose ``attend`` computes the attention of the step's tokens
-over it.  As everywhere in the package, the arithmetic runs in the library's
-CUDA kernels: this module checks tensors, allocates outputs and passes pointers
-and the CUDA stream.
+over it; ``PagedKV8`` is one that holds 8 bits an element.  As everywhere in the
+package, the arithmetic runs in the library's CUDA kernels: this module checks
+tensors, allocates outputs and passes pointers and the CUDA stream.
 
 A step's batch is three int32 tensors: ``block_table`` [B, max_pages] (the pages
 of each sequence in order), ``cu_q`` [B + 1] (sequence b has the step's tokens
@@ -34,6 +34,7 @@ KT_DEVERR_BAD_POSITION = 0x40
 # GPU, so a call packs its descriptors into one buffer of the thread's and passes addresses in it.
 HEADS = "Pqqixxxx"                    # kt_heads: ptr, token_stride, head_stride, heads
 PAGED_KV = "PPqqqqqqiiiiixxxx"        # kt_paged_kv: k, v, strides, num_pages, page_size, heads, head_dim, dtype
+PAGED_KV8 = "PPPPqqqqqqiiiiixxxx"     # kt_paged_kv8: k, v, their scales, strides, sizes, dtype
 PAGED_BATCH = "PqixxxxPPii"           # kt_paged_batch: block_table, table_stride, max_pages, cu_q, seq_lens, sizes
 HEAD_TRANSFORM = "PiiixxxxPPif"       # kt_head_transform: table, positions, rotary_dim, style, weights, dtype, eps
 _HEADS_BYTES, _BATCH_BYTES = struct.calcsize(HEADS), struct.calcsize(PAGED_BATCH)
@@ -59,6 +60,8 @@ SIGNATURES = {
     "kt_qk_norm_rope": ([_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _VP, _VP, _VP], _I),
     "kt_kv_append": ([_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], _I),
     "kt_paged_attention_workspace_bytes": ([], ctypes.c_size_t),
+    "kt_kv8_append": ([_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP], _I),
+    "kt_paged_attention8": ([_VP, _VP, _VP, _VP, _I, _F, _I, _VP, _VP, _VP, ctypes.c_size_t, _VP], _I),
     "kt_paged_attention": ([_VP, _VP, _VP, _VP, _I, _F, _I, _VP, _VP, _VP, ctypes.c_size_t, _VP], _I),
 }
 
@@ -288,6 +291,7 @@ class PagedKV:
     of a graph's calls leaves that out."""
 
     _shared = weakref.WeakValueDictionary()   # (device, stream) -> workspace, kept by the objects that use it
+    _append, _attend = "kt_kv_append", "kt_paged_attention"
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor):
         for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
@@ -304,16 +308,27 @@ class PagedKV:
                              "multiple of 8 up to 128")
         self.dtype, self.device = k_pages.dtype, k_pages.device
         self.k_pages, self.v_pages = k_pages, v_pages   # keep them alive
-        dense = (self.page_size * self.heads * self.head_dim, self.heads * self.head_dim, self.head_dim)
-        strides = [st if size > 1 else d for t in (k_pages, v_pages)
-                   for st, size, d in zip(t.stride(), t.shape[:3], dense)]
-        self._index = k_pages.get_device()
-        self._spans = tuple((t.data_ptr(), t.data_ptr() + 2 * (1 + sum((size - 1) * st for size, st in
-                                                                      zip(t.shape, t.stride()))))
-                            for t in (k_pages, v_pages))
-        self._desc = ctypes.create_string_buffer(struct.pack(
-            PAGED_KV, k_pages.data_ptr(), v_pages.data_ptr(), *strides, self.num_pages, self.page_size, self.heads,
-            self.head_dim, DTYPE_CODES[self.dtype]))
+        self._spans = self._spans_of(k_pages, v_pages)
+        self._describe(struct.pack(PAGED_KV, k_pages.data_ptr(), v_pages.data_ptr(), *self._strides_of(k_pages, v_pages),
+                                   self.num_pages, self.page_size, self.heads, self.head_dim, DTYPE_CODES[self.dtype]))
+
+    @staticmethod
+    def _strides_of(*pages):
+        """Page, slot and head strides of each (the stride of a dimension of one entry says nothing: a dense one)."""
+        _, page_size, heads, dim = pages[0].shape
+        return [st if size > 1 else d for t in pages
+                for st, size, d in zip(t.stride(), t.shape[:3], (page_size * heads * dim, heads * dim, dim))]
+
+    @staticmethod
+    def _spans_of(*tensors):
+        """From one end to the other of each tensor's memory."""
+        return tuple((t.data_ptr(), t.data_ptr() + t.element_size() * (1 + sum((size - 1) * st for size, st in
+                                                                              zip(t.shape, t.stride()))))
+                     for t in tensors)
+
+    def _describe(self, desc: bytes):
+        self._index = self.device.index
+        self._desc = ctypes.create_string_buffer(desc)
         self._desc_at = ctypes.addressof(self._desc)
         with torch.cuda.device(self.device):
             self._error = torch.zeros(1, dtype=torch.int32, device=self.device)
@@ -384,7 +399,7 @@ class PagedKV:
         _APPEND_CALL.pack_into(b.buf, 0, *tf, *_batch(block_table, cu_q, seq_lens, n, dev), *hk, *hv, *hq, *hqo)
         at = b.at + _TRANSFORM_BYTES
         heads = at + _BATCH_BYTES
-        _call(dev, stream, "kt_kv_append", self._desc_at, at, heads, heads + _HEADS_BYTES,
+        _call(dev, stream, self._append, self._desc_at, at, heads, heads + _HEADS_BYTES,
               heads + 2 * _HEADS_BYTES if q is not None else None, heads + 3 * _HEADS_BYTES if q is not None else None,
               b.at, self._err)
         return q_out if q is not None else None
@@ -426,7 +441,53 @@ class PagedKV:
         b = _buffer
         _ATTEND_CALL.pack_into(b.buf, 0, *batch, *hq, *ho)
         at = b.at + _BATCH_BYTES
-        _call(dev, stream, "kt_paged_attention", self._desc_at, b.at, at, at + _HEADS_BYTES, _int(max_q_len),
+        _call(dev, stream, self._attend, self._desc_at, b.at, at, at + _HEADS_BYTES, _int(max_q_len),
               dim ** -0.5 if scale is None else float(scale), _int(window), sink, self._err, workspace.data_ptr(),
               workspace.numel())
         return out
+
+
+class PagedKV8(PagedKV):
+    """A key/value cache in pages of 8 bits an element: k_pages and v_pages are [num_pages, page_size, heads, head_dim]
+    (float8_e4m3fn or uint8 codes) by any strides that are multiples of 16 with contiguous heads, page_size and head_dim
+    multiples of 16, head_dim up to 128; k_scales and v_scales are contiguous uint8 (e8m0) [num_pages, page_size / 16,
+    heads].  An element stands for e4m3(code) * 2^(scale - 127): a power of two for each 16 positions and head.
+
+    dtype: of the keys, values and queries that come in and of the attention's output (bf16 or fp16).  `append` and
+    `attend` are PagedKV's: `append` picks the powers (the least that hold the 16 positions' values, from 2^-117 to
+    2^87 for bf16 and from 2^-14 to 2^7 for fp16, past which values saturate at 448 times that; a block that has older tokens keeps its power or rescales their codes to a larger
+    one), and `attend` computes with the numbers that the cache stands for.  A rotation table's width is a multiple of
+    16, k and v are 16-byte aligned with strides that are multiples of 8.  A key or value element that is not finite
+    makes its 16 positions of that head NaN."""
+
+    BLOCK = 16   # KT_KV8_BLOCK
+    _append, _attend = "kt_kv8_append", "kt_paged_attention8"
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                 dtype: torch.dtype = torch.bfloat16):
+        if dtype not in DTYPE_CODES:
+            raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+        for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+            if not isinstance(t, torch.Tensor) or t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+                raise TypeError(f"{name} must be a float8_e4m3fn or uint8 tensor")
+            if t.dim() != 4 or not t.is_cuda or (t.stride(3) != 1 and t.shape[3] != 1):
+                raise ValueError(f"{name} must be a CUDA tensor [num_pages, page_size, heads, head_dim] with "
+                                 f"contiguous heads, got {tuple(t.shape)} on {t.device}")
+        if k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype or k_pages.device != v_pages.device:
+            raise ValueError("k_pages and v_pages must have one shape, dtype and device")
+        self.num_pages, self.page_size, self.heads, self.head_dim = k_pages.shape
+        if self.page_size % self.BLOCK or self.head_dim % 16 or self.head_dim > 128 or k_pages.numel() == 0:
+            raise ValueError(f"page_size={self.page_size} must be a multiple of {self.BLOCK} and head_dim="
+                             f"{self.head_dim} a multiple of 16 up to 128")
+        shape = (self.num_pages, self.page_size // self.BLOCK, self.heads)
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            if not isinstance(t, torch.Tensor) or t.dtype is not torch.uint8:
+                raise TypeError(f"{name} must be a uint8 tensor")
+            if t.shape != shape or t.device != k_pages.device or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous {list(shape)} on {k_pages.device}")
+        self.dtype, self.device = dtype, k_pages.device
+        self.k_pages, self.v_pages, self.k_scales, self.v_scales = k_pages, v_pages, k_scales, v_scales
+        self._spans = self._spans_of(k_pages, v_pages, k_scales, v_scales)
+        self._describe(struct.pack(PAGED_KV8, k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(),
+                                   v_scales.data_ptr(), *self._strides_of(k_pages, v_pages), *k_pages.shape,
+                                   DTYPE_CODES[dtype]))

@@ -35,8 +35,9 @@ static PFN_cuTensorMapEncodeTiled_v12000 find_encode() {
                : nullptr;
 }
 
-bool encode_tiled_map(CUtensorMap* m, int dtype, const void* base, int rank, const uint64_t* dims,
-                      const uint64_t* strides, const uint32_t* box, CUtensorMapL2promotion promotion) {
+static bool encode_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle,
+                       CUtensorMapL2promotion promotion) {
     static const PFN_cuTensorMapEncodeTiled_v12000 encode = find_encode();
     if (!encode) return false;
     const cuuint32_t steps[4] = {1, 1, 1, 1};
@@ -47,11 +48,14 @@ bool encode_tiled_map(CUtensorMap* m, int dtype, const void* base, int rank, con
         part[i] = box[i];
         if (i > 0) pitch[i - 1] = strides[i - 1];
     }
-    const CUtensorMapDataType type =
-        dtype == KT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     return encode(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), size, pitch, part, steps,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tiled_map(CUtensorMap* m, int dtype, const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box, CUtensorMapL2promotion promotion) {
+    return encode_map(m, dtype == KT_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                      base, rank, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B, promotion);
 }
 
 bool encode_kv_map(CUtensorMap* m, const kt_paged_kv& kv, bool values, int box_slots) {
@@ -68,6 +72,21 @@ bool encode_kv_map(CUtensorMap* m, const kt_paged_kv& kv, bool values, int box_s
                                              : row % 64 == 0  ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
                                                               : CU_TENSOR_MAP_L2_PROMOTION_NONE;
     return encode_tiled_map(m, kv.dtype, values ? kv.v : kv.k, 4, dims, strides, box, promotion);
+}
+
+bool encode_kv8_map(CUtensorMap* m, const kt_paged_kv& kv, bool values, int width, int box_slots,
+                    CUtensorMapSwizzle swizzle) {
+    const uint64_t dims[4] = {static_cast<uint64_t>(kv.head_dim), static_cast<uint64_t>(kv.page_size),
+                              static_cast<uint64_t>(kv.heads), static_cast<uint64_t>(kv.num_pages)};
+    const uint64_t strides[3] = {static_cast<uint64_t>(values ? kv.v_slot_stride : kv.k_slot_stride),
+                                 static_cast<uint64_t>(values ? kv.v_head_stride : kv.k_head_stride),
+                                 static_cast<uint64_t>(values ? kv.v_page_stride : kv.k_page_stride)};
+    const uint32_t box[4] = {static_cast<uint32_t>(width), static_cast<uint32_t>(box_slots), 1, 1};
+    const int row = kv.head_dim;   // L2 fetches as in encode_kv_map
+    const CUtensorMapL2promotion promotion = row % 128 == 0  ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                             : row % 64 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B
+                                                             : CU_TENSOR_MAP_L2_PROMOTION_NONE;
+    return encode_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, values ? kv.v : kv.k, 4, dims, strides, box, swizzle, promotion);
 }
 
 static kt_status check_heads(const kt_heads* h, const char* name, size_t align, int64_t step) {
@@ -96,6 +115,29 @@ static kt_status check_cache(const kt_paged_kv* c) {
         if (x <= 0) return refuse(KT_ERR_INVALID_ARG, "cache strides must be positive");
         if (x % 8) return refuse(KT_ERR_ALIGNMENT, "cache strides must be multiples of 8 elements");
         if (x >= (int64_t(1) << 38)) return refuse(KT_ERR_UNSUPPORTED_SHAPE, "cache stride too large");
+    }
+    if (!aligned(c->k, 16) || !aligned(c->v, 16))
+        return refuse(KT_ERR_ALIGNMENT, "cache pointers must be 16-byte aligned");
+    return KT_OK;
+}
+
+static kt_status check_cache8(const kt_paged_kv8* c) {
+    if (!c) return refuse(KT_ERR_INVALID_ARG, "null cache descriptor");
+    if (!is_16bit(c->dtype)) return refuse(KT_ERR_INVALID_ARG, "cache dtype %d is not bf16 or fp16", c->dtype);
+    if (c->num_pages <= 0 || c->page_size <= 0 || c->heads <= 0 || c->head_dim <= 0)
+        return refuse(KT_ERR_INVALID_ARG, "cache sizes must be positive");
+    if (c->page_size % KT_KV8_BLOCK || c->page_size > 65536 || c->head_dim % 16 || c->head_dim > 128 ||
+        c->heads > 65535)
+        return refuse(KT_ERR_UNSUPPORTED_SHAPE,
+                      "page_size=%d must be a multiple of %d, head_dim=%d a multiple of 16 up to 128", c->page_size,
+                      KT_KV8_BLOCK, c->head_dim);
+    if (!c->k || !c->v || !c->k_scales || !c->v_scales) return refuse(KT_ERR_INVALID_ARG, "null cache pointer");
+    const int64_t st[6] = {c->k_page_stride, c->k_slot_stride, c->k_head_stride,
+                           c->v_page_stride, c->v_slot_stride, c->v_head_stride};
+    for (int64_t x : st) {
+        if (x <= 0) return refuse(KT_ERR_INVALID_ARG, "cache strides must be positive");
+        if (x % 16) return refuse(KT_ERR_ALIGNMENT, "cache strides must be multiples of 16 bytes");
+        if (x >= (int64_t(1) << 39)) return refuse(KT_ERR_UNSUPPORTED_SHAPE, "cache stride too large");
     }
     if (!aligned(c->k, 16) || !aligned(c->v, 16))
         return refuse(KT_ERR_ALIGNMENT, "cache pointers must be 16-byte aligned");
@@ -264,17 +306,88 @@ kt_status kt_kv_append(const kt_paged_kv* cache, const kt_paged_batch* batch, co
     return cuda_status(launch_head_rows(p, cache->dtype, wide_rows(p), static_cast<cudaStream_t>(stream)));
 }
 
+kt_status kt_kv8_append(const kt_paged_kv8* cache, const kt_paged_batch* batch, const kt_heads* k, const kt_heads* v,
+                        const kt_heads* q, const kt_heads* q_out, const kt_head_transform* transform, int* err,
+                        void* stream) {
+    report(KT_OK, "");
+    kt_status st;
+    if ((st = check_cache8(cache)) != KT_OK || (st = check_batch(batch)) != KT_OK) return st;
+    if (!k || !v || (q && !q_out)) return refuse(KT_ERR_INVALID_ARG, "null descriptor");
+    if ((st = check_transform(transform, cache->head_dim, cache->dtype)) != KT_OK) return st;
+    if (transform && transform->table && transform->rotary_dim % 16)
+        return refuse(KT_ERR_UNSUPPORTED_SHAPE, "rotary_dim=%d must be a multiple of 16", transform->rotary_dim);
+    if (batch->seqs == 0 || batch->tokens == 0) return KT_OK;
+    if ((st = check_heads(k, "k", 16, 8)) != KT_OK || (st = check_heads(v, "v", 16, 8)) != KT_OK) return st;
+    if (q && ((st = check_heads(q, "q", 8, 4)) != KT_OK || (st = check_heads(q_out, "q_out", 8, 4)) != KT_OK))
+        return st;
+    if (k->heads != cache->heads || v->heads != cache->heads || (q && q_out->heads != q->heads))
+        return refuse(KT_ERR_INVALID_ARG, "k and v must have the cache's heads, q_out q's");
+    if (!aligned(err, 4)) return refuse(KT_ERR_ALIGNMENT, "err must be 4-byte aligned");
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Kv8AppendParams p{};
+    p.side[0] = Kv8Side{k->ptr, k->token_stride, k->head_stride, cache->k, cache->k_scales, cache->k_page_stride,
+                        cache->k_slot_stride, cache->k_head_stride};
+    p.side[1] = Kv8Side{v->ptr, v->token_stride, v->head_stride, cache->v, cache->v_scales, cache->v_page_stride,
+                        cache->v_slot_stride, cache->v_head_stride};
+    p.tokens = batch->tokens;
+    p.head_dim = cache->head_dim;
+    p.heads = cache->heads;
+    p.inv_dim = 1.0f / static_cast<float>(cache->head_dim);
+    if (transform) {
+        p.eps = transform->eps;
+        p.weight = transform->k_weight;
+        p.weight_f32 = transform->weight_dtype == KT_DTYPE_F32;
+        p.weight_vector = aligned(transform->k_weight, 16);
+        if (transform->table) {
+            p.table = transform->table;
+            p.positions_end = transform->positions;
+            p.rot = transform->rotary_dim;
+            p.style = transform->style;
+        }
+    }
+    p.cu_q = batch->cu_q;
+    p.seq_lens = batch->seq_lens;
+    p.block_table = batch->block_table;
+    p.table_stride = batch->table_stride;
+    p.seqs = batch->seqs;
+    p.max_pages = batch->max_pages;
+    p.page_size = cache->page_size;
+    p.num_pages = cache->num_pages;
+    p.least = cache->dtype == KT_DTYPE_BF16 ? -117 : -14;
+    // bf16: attention's fp32 sums hold 2^24 keys of 448 * 2^87 under weights of up to 2^8
+    p.most = cache->dtype == KT_DTYPE_BF16 ? 87 : 7;
+    p.err = err;
+    HeadRowsParams h{};
+    if (q) {
+        dense(h.seg[0], q, q_out);
+        fill_transform(h, transform, cache->head_dim);
+        h.seg[1].weight = nullptr;
+        h.tokens = batch->tokens;
+        h.cu_q = batch->cu_q;
+        h.seq_lens = batch->seq_lens;
+        h.seqs = batch->seqs;
+        h.max_pages = batch->max_pages;
+        h.page_size = cache->page_size;
+        h.num_pages = cache->num_pages;
+        h.err = err;
+        if (too_many_rows(h)) return refuse(KT_ERR_UNSUPPORTED_SHAPE, "too many head rows");
+    }
+    if ((st = cuda_status(launch_kv8_append(p, cache->dtype, s))) != KT_OK || !q) return st;
+    return cuda_status(launch_head_rows(h, cache->dtype, wide_rows(h), s));
+}
+
 size_t kt_paged_attention_workspace_bytes(void) {
     const size_t a = attn_split_workspace_bytes(), b = attn_tile_workspace_bytes();
     return KT_PAGED_ATTENTION_ZEROED + (a > b ? a : b);
 }
 
-kt_status kt_paged_attention(const kt_paged_kv* cache, const kt_paged_batch* batch, const kt_heads* q,
-                             const kt_heads* out, int max_q_len, float scale, int window, const float* sinks, int* err,
-                             void* ws, size_t ws_bytes, void* stream) {
-    report(KT_OK, "");
+// kt_paged_attention and kt_paged_attention8 after the checks of the cache (an 8-bit one has scales).
+static kt_status attention_impl(const kt_paged_kv* cache, const uint8_t* k_scales, const uint8_t* v_scales,
+                                const kt_paged_batch* batch, const kt_heads* q, const kt_heads* out, int max_q_len,
+                                float scale, int window, const float* sinks, int* err, void* ws, size_t ws_bytes,
+                                void* stream) {
     kt_status st;
-    if ((st = check_cache(cache)) != KT_OK || (st = check_batch(batch)) != KT_OK) return st;
+    if ((st = check_batch(batch)) != KT_OK) return st;
     if (!q || !out) return refuse(KT_ERR_INVALID_ARG, "null descriptor");
     if (max_q_len < 0 || window < 0)
         return refuse(KT_ERR_INVALID_ARG, "max_q_len=%d and window=%d must be >= 0", max_q_len, window);
@@ -295,14 +408,38 @@ kt_status kt_paged_attention(const kt_paged_kv* cache, const kt_paged_batch* bat
     if (ws_bytes < kt_paged_attention_workspace_bytes())
         return refuse(KT_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes,
                       kt_paged_attention_workspace_bytes());
-    AttnArgs a{*cache, *batch, *q, *out, scale, window, sinks, err, static_cast<unsigned*>(ws),
+    AttnArgs a{*cache, k_scales, v_scales, *batch, *q, *out, scale, window, sinks, err, static_cast<unsigned*>(ws),
                static_cast<uint8_t*>(ws) + KT_PAGED_ATTENTION_ZEROED};
     // The split kernel's tiles hold 16 query rows: it reads the keys once for chunks of up to so many.  The tile
     // kernel loads its queries by TMA, which needs strides.
     const long long rows = static_cast<long long>(max_q_len) * (q->heads / cache->heads);
-    if (rows <= 16 || q->token_stride == 0 || q->head_stride == 0)
+    if (rows <= 16 || q->token_stride == 0 || q->head_stride == 0 || k_scales != nullptr)
         return launch_attn_split(a, static_cast<cudaStream_t>(stream));
     return launch_attn_tile(a, static_cast<cudaStream_t>(stream));
+}
+
+kt_status kt_paged_attention(const kt_paged_kv* cache, const kt_paged_batch* batch, const kt_heads* q,
+                             const kt_heads* out, int max_q_len, float scale, int window, const float* sinks, int* err,
+                             void* ws, size_t ws_bytes, void* stream) {
+    report(KT_OK, "");
+    const kt_status st = check_cache(cache);
+    if (st != KT_OK) return st;
+    return attention_impl(cache, nullptr, nullptr, batch, q, out, max_q_len, scale, window, sinks, err, ws, ws_bytes,
+                          stream);
+}
+
+kt_status kt_paged_attention8(const kt_paged_kv8* cache, const kt_paged_batch* batch, const kt_heads* q,
+                              const kt_heads* out, int max_q_len, float scale, int window, const float* sinks,
+                              int* err, void* ws, size_t ws_bytes, void* stream) {
+    report(KT_OK, "");
+    const kt_status st = check_cache8(cache);
+    if (st != KT_OK) return st;
+    const kt_paged_kv kv{cache->k,             cache->v,             cache->k_page_stride, cache->k_slot_stride,
+                         cache->k_head_stride, cache->v_page_stride, cache->v_slot_stride, cache->v_head_stride,
+                         cache->num_pages,     cache->page_size,     cache->heads,         cache->head_dim,
+                         cache->dtype};
+    return attention_impl(&kv, cache->k_scales, cache->v_scales, batch, q, out, max_q_len, scale, window, sinks, err, ws,
+                          ws_bytes, stream);
 }
 
 }  // extern "C"

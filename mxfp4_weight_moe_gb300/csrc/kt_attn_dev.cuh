@@ -23,6 +23,8 @@ struct AttnShape {
     int* err;
     int seqs, tokens, max_pages, num_pages, page_size;
     int kv_heads, group, head_dim, window;
+    const uint8_t* k_scales;   // of an 8-bit cache
+    const uint8_t* v_scales;
     float scale_log2;   // scale * log2(e): the softmax runs on powers of two
     int withhold;       // test hook: the first CTA withholds its first load
     unsigned long long wait_limit_ns;
@@ -45,6 +47,8 @@ inline AttnShape attn_shape(const AttnArgs& a) {
     s.group = a.q.heads / a.kv.heads;
     s.head_dim = a.kv.head_dim;
     s.window = a.window;
+    s.k_scales = a.k_scales;
+    s.v_scales = a.v_scales;
     s.scale_log2 = a.scale * kLog2e;
     const DebugSettings dbg = debug_settings();
     s.withhold = (dbg.flags & KT_DEBUG_WITHHOLD_STAGE) != 0;
@@ -62,6 +66,10 @@ bool encode_tiled_map(CUtensorMap* m, int dtype, const void* base, int rank, con
 // 64 elements x box_slots slots of one head and page in the 128-byte swizzle.
 // Elements past head_dim and pages outside the cache read as zeros.
 bool encode_kv_map(CUtensorMap* m, const kt_paged_kv& kv, bool values, int box_slots);
+
+// The same of an 8-bit cache: a box is `width` codes (64 or 128) x box_slots slots.
+bool encode_kv8_map(CUtensorMap* m, const kt_paged_kv& kv, bool values, int width, int box_slots,
+                    CUtensorMapSwizzle swizzle);
 
 #ifdef __CUDACC__
 // Sequence b of the step.  Nothing here goes past the step's tokens or the
@@ -219,6 +227,35 @@ __device__ __forceinline__ float high_of(uint32_t v) {
     if (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(v & 0xffff0000u);
     return __half2float(__ushort_as_half(static_cast<unsigned short>(v >> 16)));
 }
+// Four e4m3 codes as two pairs of T: bytes 0 and 2, bytes 1 and 3, times `factor` (a pair of T).  For bf16, which has
+// no conversion from e4m3, the code's bits are put where bf16 has them (an e4m3 exponent of 7 means 0, a bf16 exponent
+// of 127 does, and subnormal codes become subnormal numbers): what stands there is 2^-120 of the value, so that the
+// factor holds 2^120 besides.  NaN codes do not come out as NaN.
+template <typename T>
+__device__ __forceinline__ void widen_e4m3(uint32_t w, uint32_t factor, uint32_t& even, uint32_t& odd);
+template <>
+__device__ __forceinline__ void widen_e4m3<__nv_bfloat16>(uint32_t w, uint32_t factor, uint32_t& even, uint32_t& odd) {
+    const uint32_t e = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
+    const uint32_t o = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(even) : "r"(e), "r"(factor));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"(o), "r"(factor));
+}
+template <>
+__device__ __forceinline__ void widen_e4m3<__half>(uint32_t w, uint32_t factor, uint32_t& even, uint32_t& odd) {
+    const uint32_t s = __byte_perm(w, 0, 0x3120);
+    uint32_t e, o;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(e) : "h"(static_cast<unsigned short>(s)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o) : "h"(static_cast<unsigned short>(s >> 16)));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(even) : "r"(e), "r"(factor));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(odd) : "r"(o), "r"(factor));
+}
+constexpr uint32_t kBf16Widen = 0x7b807b80u;   // 2^120 twice
+
+// 2^(byte - 127) of a scale byte, NaN for 255 (byte 0 as 2^-126: no subnormals, which a product might flush).
+__device__ __forceinline__ float e8m0_power(int byte) {
+    return __uint_as_float(byte == 255 ? 0x7fc00000u : static_cast<uint32_t>(max(byte, 1)) << 23);
+}
+
 // A pair of T, what is larger than T's largest number (infinity) replaced by that, signs kept.
 template <typename T>
 __device__ __forceinline__ uint32_t finite_pair(uint32_t v);

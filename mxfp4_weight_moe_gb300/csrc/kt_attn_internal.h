@@ -40,9 +40,37 @@ struct HeadRowsParams {
 // wide: every pointer is 16-byte aligned, every stride a multiple of 8 and head_dim and rotary_dim multiples of 16.
 cudaError_t launch_head_rows(HeadRowsParams& p, int dtype, bool wide, cudaStream_t s);
 
+// ------------------------------------------------------------- append to an 8-bit cache
+struct Kv8Side {   // keys or values
+    const void* src;
+    long long src_token, src_head;
+    uint8_t* codes;
+    uint8_t* scales;
+    long long page, slot, head;   // strides of the codes in bytes
+};
+struct Kv8AppendParams {
+    Kv8Side side[2];
+    int tokens, head_dim, heads;
+    float inv_dim, eps;
+    const float* table;
+    int positions_end, rot, style;
+    const void* weight;   // of the keys
+    int weight_f32, weight_vector;
+    const int32_t* cu_q;
+    const int32_t* seq_lens;
+    const int32_t* block_table;
+    long long table_stride;
+    int seqs, max_pages, page_size, num_pages;
+    int least, most;      // scale exponents
+    int* err;
+};
+cudaError_t launch_kv8_append(const Kv8AppendParams& p, int dtype, cudaStream_t s);
+
 // ------------------------------------------------------------- attention
 struct AttnArgs {
-    kt_paged_kv kv;
+    kt_paged_kv kv;       // of an 8-bit cache: strides in bytes, which are its elements
+    const uint8_t* k_scales;   // NULL for a 16-bit cache
+    const uint8_t* v_scales;
     kt_paged_batch batch;
     kt_heads q, out;
     float scale;

@@ -45,13 +45,14 @@ constexpr int kSplitMinUnits = 2;                       // least units of a piec
 constexpr int kSplitItemUnits = 3;                      // what an item costs besides its units, in units
 constexpr int kSplitJoinUnits = 4;                      // what cutting an item costs its last CTA, in units
 
-template <int DP>
+template <int DP, bool KV8>
 struct SplitCfg {
-    static constexpr int kSub = DP == 128 ? 1 : 2;                   // loads of K and of V that make a warp's block
+    static constexpr int kSub = DP == 128 && !KV8 ? 1 : 2;           // loads of K and of V that make a warp's block
     static constexpr int kBlockKeys = kSub * kSplitKeys;
     static constexpr int kUnit = kSplitWarps * kBlockKeys;           // keys of one unit
-    static constexpr int kBlockBytes = kBlockKeys * DP * 2;          // one of K, V
-    static constexpr int kStages = 3;
+    static constexpr int kRowBytes = DP * (KV8 ? 1 : 2);             // of a key in a block
+    static constexpr int kBlockBytes = kBlockKeys * kRowBytes;       // one of K, V
+    static constexpr int kStages = KV8 && DP == 64 ? 6 : 3;          // 24 KB a warp
     static constexpr int kRing = kStages * 2 * kBlockBytes;          // per warp
     static constexpr int kSmem = kSplitWarps * kRing + 1024;
     static constexpr int kMergeRow = DP + 8;                         // floats of a row: rows start 8 banks apart
@@ -193,16 +194,28 @@ __device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, int unit, Sp
     return plan;
 }
 
-template <typename T, int DP>
+// Address of 16-byte piece `piece` of key `row` in 16 keys of an 8-bit block at `base`, as TMA's swizzle leaves it.
+template <int DP>
+__device__ __forceinline__ uint32_t piece8(uint32_t base, int row, int piece) {
+    return DP == 128 ? base + row * 128 + ((piece ^ (row & 7)) << 4) : base + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+}
+
+// KV8: the cache's elements are e4m3 codes with a power of two for 16 keys of a head.  Codes go through ldmatrix as
+// pairs and are widened to T (exactly) in registers.  Of four codes that a lane gets, the products take bytes 0 and 2,
+// and 1 and 3: for S that is another order of the head's elements, which the queries follow; for O the lane's columns
+// are four neighbours.  The keys' power multiplies the scores, the values' the softmax weights (bf16) or the codes
+// (fp16, where a weight would leave the type's range).
+template <typename T, int DP, bool KV8>
 __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     attn_split_kernel(const SplitParams p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
-    using Cfg = SplitCfg<DP>;
+    using Cfg = SplitCfg<DP, KV8>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[kSplitWarps][Cfg::kStages];
     __shared__ int s_abort, s_last;
     __shared__ float2 s_ml[kSplitWarps][kSplitRows];
     __shared__ SplitPlan s_plan;
+    __shared__ uint32_t s_scales[KV8 ? kSplitWarps : 1][Cfg::kStages][Cfg::kSub];   // of keys, of values << 8
     const AttnShape& sh = p.sh;
     const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     uint8_t* ring_base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -264,6 +277,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
         while (i1 > i0 && base + (i1 - 1) * Cfg::kUnit >= it.hi) --i1;
         if (gave_up) i1 = i0;
         int page_batch = -1, my_page = -1, my_slot = 0;
+        uint32_t my_scales = 127u << 8 | 127u;
         auto issue = [&](int i) {   // whole warp; block i into its stage
             if (withhold && loads == 0 && i == i0) return;   // test hook
             // lanes look up the pages of the next 32 loads at a time
@@ -274,10 +288,16 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                 const int key = base + mine * Cfg::kUnit + lane % Cfg::kSub * kSplitKeys;
                 my_page = -1;
                 my_slot = 0;
+                my_scales = 127u << 8 | 127u;
                 // (16 keys that no row sees, past them all or before the window: zeros from outside the cache)
                 if (mine < i1 && key < it.hi && key + kSplitKeys > it.lo) {
                     my_page = checked_page(sh, pages, key);
                     my_slot = key % sh.page_size;
+                    if (KV8 && my_page >= 0) {
+                        const long long at = (static_cast<long long>(my_page) * (sh.page_size / KT_KV8_BLOCK) +
+                                              my_slot / KT_KV8_BLOCK) * sh.kv_heads + h;
+                        my_scales = sh.k_scales[at] | static_cast<uint32_t>(sh.v_scales[at]) << 8;
+                    }
                 }
             }
             const uint32_t st = (loads + static_cast<uint32_t>(i - i0)) % Cfg::kStages;
@@ -289,7 +309,15 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                 const int src = (i - i0) % (32 / Cfg::kSub) * Cfg::kSub + sub;
                 const int page = __shfl_sync(0xffffffffu, my_page, src);
                 const int slot = __shfl_sync(0xffffffffu, my_slot, src);
-                if (lane == 0) {
+                if constexpr (KV8) {
+                    const uint32_t scales = __shfl_sync(0xffffffffu, my_scales, src);
+                    if (lane == 0) {
+                        s_scales[warp][st][sub] = scales;
+                        const uint32_t at_block = sub * kSplitKeys * DP;
+                        tma_load_4d_once(k + at_block, &kmap, bar, 0, slot, h, page, policy);
+                        tma_load_4d_once(k + Cfg::kBlockBytes + at_block, &vmap, bar, 0, slot, h, page, policy);
+                    }
+                } else if (lane == 0) {
 #pragma unroll
                     for (int x = 0; x < DP; x += 64) {
                         const uint32_t at_block = (x * Cfg::kBlockKeys + sub * kSplitKeys * 64) * 2;
@@ -301,6 +329,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
         };
         const int n_blocks = i1 - i0;
         for (int i = 0; i < min(n_blocks, Cfg::kStages); ++i) issue(i0 + i);
+        if (KV8) __syncwarp();   // the scales of those blocks
 
         // ---- queries: rows g and g + 8 of the tile in the MMA's A layout
         const int g = lane >> 2, t4 = lane & 3;
@@ -323,10 +352,20 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
             for (int ks = 0; ks < DP / 16; ++ks)
 #pragma unroll
                 for (int f = 0; f < 4; ++f) {
-                    const int d = ks * 16 + t4 * 2 + (f >> 1) * 8;
+                    const int d = KV8 ? ks * 16 + t4 * 4 + (f >> 1) * 2 : ks * 16 + t4 * 2 + (f >> 1) * 8;
                     const T* src = qp[f & 1];
                     qa[ks][f] = src != nullptr && d < sh.head_dim ? *reinterpret_cast<const uint32_t*>(src + d) : 0u;
                 }
+            if (KV8) {   // elements 4t and 4t + 2, 4t + 1 and 4t + 3 of the 16
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ++ks)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t lo = qa[ks][e], hi = qa[ks][e + 2];
+                        qa[ks][e] = __byte_perm(lo, hi, 0x5410);
+                        qa[ks][e + 2] = __byte_perm(lo, hi, 0x7632);
+                    }
+            }
         }
 
         float o[DP / 8][4];
@@ -364,17 +403,42 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
 #pragma unroll
             for (int c = 0; c < kChains * kCols * 4; ++c) sc[c / (kCols * 4)][c / 4 % kCols][c % 4] = 0.0f;
             const int krow = (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-            for (int ks = 0; ks < DP / 16; ++ks)
+            float k_scale[Cfg::kSub], v_scale[Cfg::kSub];   // of the scores, of the weights or the codes
+            if constexpr (KV8) {
 #pragma unroll
                 for (int sub = 0; sub < Cfg::kSub; ++sub) {
-                    uint32_t kf[4];
-                    const int chunk = (ks & 3) * 2 + ((lane >> 3) & 1);
-                    ldmatrix_x4(kf, kb + (ks >> 2) * (Cfg::kBlockKeys * 128) + sub * 2048 + krow * 128 +
-                                        ((chunk ^ (krow & 7)) << 4));
-                    mma_16816<T>(sc[ks % kChains][2 * sub], qa[ks], kf[0], kf[1]);
-                    mma_16816<T>(sc[ks % kChains][2 * sub + 1], qa[ks], kf[2], kf[3]);
+                    const uint32_t scales = s_scales[warp][st][sub];
+                    k_scale[sub] = sh.scale_log2 * e8m0_power(scales & 255u);
+                    v_scale[sub] = e8m0_power(scales >> 8);
                 }
+                const uint32_t one = std::is_same<T, __half>::value ? 0x3c003c00u : kBf16Widen;
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ks += 2)
+#pragma unroll
+                    for (int sub = 0; sub < Cfg::kSub; ++sub) {
+                        uint32_t kf[4], b0, b1;   // keys 0-7 and 8-15 of two steps of 16 elements
+                        ldmatrix_x4(kf, piece8<DP>(kb + sub * kSplitKeys * DP, krow, ks + ((lane >> 3) & 1)));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            widen_e4m3<T>(kf[i], one, b0, b1);
+                            mma_16816<T>(sc[0][2 * sub + (i >> 1)], qa[ks + (i & 1)], b0, b1);
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int sub = 0; sub < Cfg::kSub; ++sub) k_scale[sub] = sh.scale_log2, v_scale[sub] = 1.0f;
+#pragma unroll
+                for (int ks = 0; ks < DP / 16; ++ks)
+#pragma unroll
+                    for (int sub = 0; sub < Cfg::kSub; ++sub) {
+                        uint32_t kf[4];
+                        const int chunk = (ks & 3) * 2 + ((lane >> 3) & 1);
+                        ldmatrix_x4(kf, kb + (ks >> 2) * (Cfg::kBlockKeys * 128) + sub * 2048 + krow * 128 +
+                                            ((chunk ^ (krow & 7)) << 4));
+                        mma_16816<T>(sc[ks % kChains][2 * sub], qa[ks], kf[0], kf[1]);
+                        mma_16816<T>(sc[ks % kChains][2 * sub + 1], qa[ks], kf[2], kf[3]);
+                    }
+            }
             // ---- scale, mask, running maximum (base-2 exponents); x[e]: row g + 8 e, keys k0 + 8 c and the next
             float x[2][2 * kCols];
             const int k0 = key0 + t4 * 2;
@@ -388,7 +452,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                     for (int f = 0; f < 2; ++f) {
                         float v = sc[0][c][2 * e + f];
                         if (kChains == 2) v += sc[kChains - 1][c][2 * e + f];
-                        x[e][2 * c + f] = v * sh.scale_log2;
+                        x[e][2 * c + f] = v * k_scale[c >> 1];
                     }
                 if (masked) {
 #pragma unroll
@@ -427,32 +491,55 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
 #pragma unroll
             for (int sub = 0; sub < Cfg::kSub; ++sub) {
                 uint32_t pa[4], pb[4];   // the two parts of the weights
+                constexpr bool kScaledWeights = KV8 && std::is_same<T, __nv_bfloat16>::value;
 #pragma unroll
                 for (int f = 0; f < 4; ++f) {
-                    const float lo = x[f & 1][4 * sub + (f >> 1) * 2], hi = x[f & 1][4 * sub + (f >> 1) * 2 + 1];
+                    float lo = x[f & 1][4 * sub + (f >> 1) * 2], hi = x[f & 1][4 * sub + (f >> 1) * 2 + 1];
+                    if (kScaledWeights) lo *= v_scale[sub], hi *= v_scale[sub];
                     pa[f] = pack2<T>(lo, hi);
                     pb[f] = pack2<T>(lo - low_of<T>(pa[f]), hi - high_of<T>(pa[f]));
                 }
+                auto hide = [&](uint32_t(&vf)[4]) {   // value rows that no token sees
 #pragma unroll
-                for (int n = 0; n < DP / 8; n += 2) {
-                    uint32_t vf[4];
-                    const int chunk = (n & 7) + (lane >> 4);
-                    ldmatrix_x4_trans(vf, vb + (n >> 3) * (Cfg::kBlockKeys * 128) + sub * 2048 + vrow * 128 +
-                                              ((chunk ^ (vrow & 7)) << 4));
-                    if (ragged) {
+                    for (int f = 0; f < 4; ++f) {
+                        const int key = k0 + sub * kSplitKeys + (f & 1) * 8;
+                        if (key >= it.hi || key < it.lo) vf[f] &= 0xffff0000u;
+                        if (key + 1 >= it.hi || key + 1 < it.lo) vf[f] &= 0x0000ffffu;
+                    }
+                };
+                if constexpr (KV8) {
+                    const uint32_t factor = kScaledWeights ? kBf16Widen : pack2<T>(v_scale[sub], v_scale[sub]);
 #pragma unroll
-                        for (int f = 0; f < 4; ++f) {
-                            const int key = k0 + sub * kSplitKeys + (f & 1) * 8;
-                            if (key >= it.hi || key < it.lo) vf[f] &= 0xffff0000u;
-                            if (key + 1 >= it.hi || key + 1 < it.lo) vf[f] &= 0x0000ffffu;
+                    for (int n = 0; n < DP / 8; n += 4) {
+                        uint32_t vf[4];   // keys 0-7 and 8-15 of two times 16 elements
+                        ldmatrix_x4_trans(vf, piece8<DP>(vb + sub * kSplitKeys * DP, vrow, (n >> 1) + (lane >> 4)));
+                        if (ragged) hide(vf);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t even0, odd0, even1, odd1;
+                            widen_e4m3<T>(vf[2 * i], factor, even0, odd0);
+                            widen_e4m3<T>(vf[2 * i + 1], factor, even1, odd1);
+                            mma_16816<T>(o[n + 2 * i], pa, even0, even1);
+                            mma_16816<T>(o[n + 2 * i + 1], pa, odd0, odd1);
+                            mma_16816<T>(o[n + 2 * i], pb, even0, even1);
+                            mma_16816<T>(o[n + 2 * i + 1], pb, odd0, odd1);
                         }
                     }
-                    mma_16816<T>(o[n], pa, vf[0], vf[1]);
-                    mma_16816<T>(o[n + 1], pa, vf[2], vf[3]);
+                } else {
 #pragma unroll
-                    for (int f = 0; f < 4; ++f) vf[f] = finite_pair<T>(vf[f]);   // (a second part of 0 x infinity)
-                    mma_16816<T>(o[n], pb, vf[0], vf[1]);
-                    mma_16816<T>(o[n + 1], pb, vf[2], vf[3]);
+                    for (int n = 0; n < DP / 8; n += 2) {
+                        uint32_t vf[4];
+                        const int chunk = (n & 7) + (lane >> 4);
+                        ldmatrix_x4_trans(vf, vb + (n >> 3) * (Cfg::kBlockKeys * 128) + sub * 2048 + vrow * 128 +
+                                                  ((chunk ^ (vrow & 7)) << 4));
+                        if (ragged) hide(vf);
+                        mma_16816<T>(o[n], pa, vf[0], vf[1]);
+                        mma_16816<T>(o[n + 1], pa, vf[2], vf[3]);
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) vf[f] = finite_pair<T>(vf[f]);   // (a second part of 0 x infinity)
+                        mma_16816<T>(o[n], pb, vf[0], vf[1]);
+                        mma_16816<T>(o[n + 1], pb, vf[2], vf[3]);
+                    }
                 }
             }
             __syncwarp();
@@ -473,10 +560,17 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 if (8 * e >= rows) break;
+                if constexpr (KV8) {   // elements 4t to 4t + 3 of each 16
 #pragma unroll
-                for (int n = 0; n < DP / 8; ++n)
-                    *reinterpret_cast<float2*>(mo + (g + 8 * e) * Cfg::kMergeRow + n * 8 + t4 * 2) =
-                        make_float2(o[n][2 * e], o[n][2 * e + 1]);
+                    for (int n = 0; n < DP / 8; n += 2)
+                        *reinterpret_cast<float4*>(mo + (g + 8 * e) * Cfg::kMergeRow + n * 8 + t4 * 4) =
+                            make_float4(o[n][2 * e], o[n + 1][2 * e], o[n][2 * e + 1], o[n + 1][2 * e + 1]);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < DP / 8; ++n)
+                        *reinterpret_cast<float2*>(mo + (g + 8 * e) * Cfg::kMergeRow + n * 8 + t4 * 2) =
+                            make_float2(o[n][2 * e], o[n][2 * e + 1]);
+                }
                 if (t4 == 0) s_ml[warp][g + 8 * e] = make_float2(m[e], l[e]);
             }
         }
@@ -642,17 +736,21 @@ size_t attn_split_workspace_bytes() {
     return c * 2 * kSplitRows * (128 + 2) * sizeof(float);
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool KV8>
 static kt_status launch_split_typed(const AttnArgs& a, cudaStream_t s) {
-    using Cfg = SplitCfg<DP>;
+    using Cfg = SplitCfg<DP, KV8>;
     CUtensorMap kmap, vmap;
-    if (!encode_kv_map(&kmap, a.kv, false, kSplitKeys) || !encode_kv_map(&vmap, a.kv, true, kSplitKeys))
+    auto encode = [&](CUtensorMap* m, bool values) {
+        const CUtensorMapSwizzle swizzle = DP == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+        return KV8 ? encode_kv8_map(m, a.kv, values, DP, kSplitKeys, swizzle) : encode_kv_map(m, a.kv, values, kSplitKeys);
+    };
+    if (!encode(&kmap, false) || !encode(&vmap, true))
         return report(KT_ERR_CUDA, "tensor map encoding failed");
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<T, DP>,
+        const cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<T, DP, KV8>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
         if (e != cudaSuccess) return cuda_status(e);
         attr_set[dev] = true;
@@ -670,16 +768,20 @@ static kt_status launch_split_typed(const AttnArgs& a, cudaStream_t s) {
     p.part_o = reinterpret_cast<float4*>(a.ws);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + c * 2 * kSplitRows * 32);
     count_launches(1);
-    return cuda_status(launch_chained(attn_split_kernel<T, DP>, dim3(static_cast<unsigned>(c)), dim3(kSplitThreads),
+    return cuda_status(launch_chained(attn_split_kernel<T, DP, KV8>, dim3(static_cast<unsigned>(c)), dim3(kSplitThreads),
                                       Cfg::kSmem, s, static_cast<const SplitParams&>(p),
                                       static_cast<const CUtensorMap&>(kmap), static_cast<const CUtensorMap&>(vmap)));
 }
 
+template <typename T>
+static kt_status launch_split_of(const AttnArgs& a, cudaStream_t s) {
+    if (a.k_scales != nullptr)
+        return a.kv.head_dim > 64 ? launch_split_typed<T, 128, true>(a, s) : launch_split_typed<T, 64, true>(a, s);
+    return a.kv.head_dim > 64 ? launch_split_typed<T, 128, false>(a, s) : launch_split_typed<T, 64, false>(a, s);
+}
+
 kt_status launch_attn_split(const AttnArgs& a, cudaStream_t s) {
-    const bool wide = a.kv.head_dim > 64;
-    if (a.kv.dtype == KT_DTYPE_BF16)
-        return wide ? launch_split_typed<__nv_bfloat16, 128>(a, s) : launch_split_typed<__nv_bfloat16, 64>(a, s);
-    return wide ? launch_split_typed<__half, 128>(a, s) : launch_split_typed<__half, 64>(a, s);
+    return a.kv.dtype == KT_DTYPE_BF16 ? launch_split_of<__nv_bfloat16>(a, s) : launch_split_of<__half>(a, s);
 }
 
 }  // namespace kt
