@@ -413,7 +413,7 @@ static kt_status attention_impl(const kt_paged_kv* cache, const uint8_t* k_scale
     // The split kernel's tiles hold 16 query rows: it reads the keys once for chunks of up to so many.  The tile
     // kernel loads its queries by TMA, which needs strides.
     const long long rows = static_cast<long long>(max_q_len) * (q->heads / cache->heads);
-    if (rows <= 16 || q->token_stride == 0 || q->head_stride == 0 || k_scales != nullptr)
+    if (rows <= 16 || q->token_stride == 0 || q->head_stride == 0)
         return launch_attn_split(a, static_cast<cudaStream_t>(stream));
     return launch_attn_tile(a, static_cast<cudaStream_t>(stream));
 }

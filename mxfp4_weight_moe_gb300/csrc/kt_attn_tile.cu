@@ -51,7 +51,6 @@
 namespace kt {
 
 constexpr int kTileKeys = 128;
-constexpr int kTileThreads = 384;
 constexpr int kItemUnits = 2;         // what an item costs besides its key tiles, in key tiles
 constexpr int kTileMinUnits = kItemUnits + 2;   // least units of a CTA's run
 constexpr int kPlanSeqs = 512;        // sequences planned at a time
@@ -60,14 +59,20 @@ constexpr float kLazyLog2 = 8.0f;     // growth of the maximum (log2) that is le
 // Tensor memory: the CTA takes all 512 columns, so it starts at 0.  S of the groups, P in its first half, then O.
 constexpr uint32_t kTmemS = 0, kTmemO = 256;
 
-template <int DP>
+template <int DP, bool KV8>
 struct TileCfg {
+    static constexpr int kThreads = KV8 ? 512 : 384;
     static constexpr int kQBytes = 128 * DP * 2;         // one row group
     static constexpr int kStageBytes = kTileKeys * DP * 2;   // one tile of K or V
-    static constexpr int kStages = DP == 128 ? 5 : 9;        // odd: K and V alternate in a stage
+    static constexpr int kStages = KV8 ? (DP == 128 ? 4 : 8) : (DP == 128 ? 5 : 9);   // K and V alternate
+    static constexpr int kRaw = KV8 ? (DP == 128 ? 2 : 4) : 0;                        // tiles as codes, likewise
+    static constexpr int kRawBytes = kTileKeys * DP;
     static constexpr int kQBufs = DP == 128 ? 1 : 2;
     static constexpr int kQAll = kQBufs * 2 * kQBytes;
-    static constexpr int kSmem = kQAll + kStages * kStageBytes + 1024;
+    static constexpr int kSmem = kQAll + kStages * kStageBytes + kRaw * kRawBytes + 1024;
+    // registers a thread: of the softmax, of loads and MMAs, of the widening; their sum over 128 threads each (twice the
+    // softmax) is the launch's 65536 (KV8) or 64512
+    static constexpr int kSoftmaxRegs = KV8 ? 192 : 208, kIssueRegs = KV8 ? 72 : 88, kWidenRegs = 56;
 };
 
 struct TileGeometry {
@@ -185,9 +190,10 @@ struct TileWalk {
 };
 
 // Deals all sequences' units in equal runs.  A warp sums a sequence: a long chunk has many items.
+template <int THREADS>
 __device__ __forceinline__ RunPlan plan_tiles(const AttnShape& s, const TileGeometry& g, unsigned long long* costs,
                                               RunPlan* shared) {
-    constexpr int kWarps = kTileThreads / 32;
+    constexpr int kWarps = THREADS / 32;
     __shared__ long long s_sum[kWarps];
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     auto fill = [&](int b0) {   // costs of sequences [b0, b0 + kPlanSeqs): units / kv_heads
@@ -207,7 +213,7 @@ __device__ __forceinline__ RunPlan plan_tiles(const AttnShape& s, const TileGeom
     for (int b0 = 0; b0 < s.seqs; b0 += kPlanSeqs) {
         if (b0 > 0) __syncthreads();
         fill(b0);
-        for (int i = tid; i < min(s.seqs - b0, kPlanSeqs); i += kTileThreads) mine += static_cast<long long>(costs[i]);
+        for (int i = tid; i < min(s.seqs - b0, kPlanSeqs); i += THREADS) mine += static_cast<long long>(costs[i]);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
@@ -401,15 +407,67 @@ __device__ __forceinline__ int ragged_tile(const TileWalk& w, int box_slots) {
     return j >= w.t0 && j < w.t1 && (w.sq.keys & (box_slots - 1)) != 0 ? j : -1;
 }
 
-template <typename T, int DP>
-__global__ void __launch_bounds__(kTileThreads, 1)
+// 16 e4m3 codes in order as 16 elements of T, each times the pair's factor (`more`: times that as well, for powers that
+// bf16's 2^120 leaves no room for).
+template <typename T>
+__device__ __forceinline__ void widen16(const uint4& v, uint32_t factor, uint32_t more, uint4& a, uint4& b);
+template <>
+__device__ __forceinline__ void widen16<__nv_bfloat16>(const uint4& v, uint32_t factor, uint32_t more, uint4& a,
+                                                       uint4& b) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {   // as widen_e4m3
+        const uint32_t u = __byte_perm(w[i / 2], 0, i & 1 ? 0x3424 : 0x1404);
+        const uint32_t x = ((u >> 4) & 0x07f007f0u) | (u & 0x80008000u);
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(x), "r"(factor));
+    }
+    if (more != 0) {   // the same for the block's lanes; hardly ever
+#pragma unroll
+        for (int i = 0; i < 8; ++i) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(r[i]), "r"(more));
+    }
+    a = make_uint4(r[0], r[1], r[2], r[3]);
+    b = make_uint4(r[4], r[5], r[6], r[7]);
+}
+template <>
+__device__ __forceinline__ void widen16<__half>(const uint4& v, uint32_t factor, uint32_t, uint4& a, uint4& b) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t x;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(x) : "h"(static_cast<unsigned short>(w[i / 2] >> (i & 1 ? 16 : 0))));
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(x), "r"(factor));
+    }
+    a = make_uint4(r[0], r[1], r[2], r[3]);
+    b = make_uint4(r[4], r[5], r[6], r[7]);
+}
+// 2^(byte - 127) as a pair of T for widen16, NaN for 255; `more` as there.
+template <typename T>
+__device__ __forceinline__ uint32_t widen_factor(int byte, uint32_t& more) {
+    more = 0;
+    if (std::is_same<T, __half>::value) return pack2<T>(e8m0_power(byte), e8m0_power(byte));
+    if (byte == 255) return 0x7fc07fc0u;
+    const int e = byte + 120;   // with the 2^120 of the codes' place
+    if (e > 254) more = static_cast<uint32_t>(e - 254 + 127) * 0x00800080u;
+    return static_cast<uint32_t>(min(e, 254)) * 0x00800080u;
+}
+
+// KV8: the cache's tiles come as e4m3 codes into a ring of their own; a fourth warpgroup widens them (exactly, the
+// powers of two included) into the ring that the tensor cores read, so that everything behind it is the 16-bit
+// kernel's.
+template <typename T, int DP, bool KV8>
+__global__ void __launch_bounds__(TileCfg<DP, KV8>::kThreads, 1)
     attn_tile_kernel(const TileParams p, const __grid_constant__ CUtensorMap qmap,
                      const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-    using Cfg = TileCfg<DP>;
+    using Cfg = TileCfg<DP, KV8>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_kv_full[Cfg::kStages], s_kv_empty[Cfg::kStages];
     __shared__ __align__(8) uint64_t s_q_full[Cfg::kQBufs][2], s_q_empty[Cfg::kQBufs][2];
     __shared__ __align__(8) uint64_t s_s_full[2], s_p_full[2][2], s_o_full[2], s_sync[2], s_done;
+    constexpr int kRaw = KV8 ? Cfg::kRaw : 1;
+    __shared__ __align__(8) uint64_t s_raw_full[kRaw], s_raw_empty[kRaw];
+    __shared__ int s_raw_scale[kRaw][kTileKeys / KT_KV8_BLOCK];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_last[2];
     __shared__ long long s_counted[2];   // first tile of the last item that a group has counted
@@ -421,14 +479,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t q_smem = smem_u32(smem);
     uint8_t* kv_ptr = smem + Cfg::kQAll;
     const uint32_t kv_smem = smem_u32(kv_ptr);
+    uint8_t* raw_ptr = kv_ptr + Cfg::kStages * Cfg::kStageBytes;
 
     if (tid == 0) {
         s_abort = 0;
         s_counted[0] = s_counted[1] = -1;
         for (int i = 0; i < Cfg::kStages; ++i) {
-            mbar_init(smem_u32(&s_kv_full[i]), 1);
+            mbar_init(smem_u32(&s_kv_full[i]), KV8 ? 4 : 1);   // (the widening warps)
             mbar_init(smem_u32(&s_kv_empty[i]), 1);
         }
+        if (KV8)
+            for (int i = 0; i < kRaw; ++i) {
+                mbar_init(smem_u32(&s_raw_full[i]), 1);
+                mbar_init(smem_u32(&s_raw_empty[i]), 4);
+            }
         for (int i = 0; i < 2; ++i) {
             for (int b = 0; b < Cfg::kQBufs; ++b) {
                 mbar_init(smem_u32(&s_q_full[b][i]), 1);
@@ -451,12 +515,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc_relinquish();
     }
     if (tpg * sh.group < 128) {   // rows of no token: zeros for good (the loads do not touch them)
-        for (int i = tid; i < Cfg::kQAll / 16; i += kTileThreads)
+        for (int i = tid; i < Cfg::kQAll / 16; i += Cfg::kThreads)
             reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     }
     griddep_wait();
     griddep_launch_dependents();
-    const RunPlan plan = plan_tiles(sh, p.geo, reinterpret_cast<unsigned long long*>(kv_ptr), &s_plan);
+    const RunPlan plan = plan_tiles<Cfg::kThreads>(sh, p.geo, reinterpret_cast<unsigned long long*>(kv_ptr), &s_plan);
     tc_fence_before();
     fence_proxy_async_smem();   // the plan's and the zeros' generic writes before the first loads
     __syncthreads();
@@ -464,8 +528,63 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const int* abort_flag = &s_abort;
     const unsigned long long limit = sh.wait_limit_ns;
 
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (KV8 && warp >= 12) {
+        // ---------------------------------------------------- codes to T, 32 rows of a tile a warp
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kWidenRegs));
+        constexpr int kPieces = DP / 16, kRows = 32 / kPieces;   // 16-byte pieces of a row; rows a pass
+        const int piece = lane % kPieces, row0 = (warp - 12) * 32 + lane / kPieces;
+        const uint32_t out_x = static_cast<uint32_t>(piece >> 2) * (kTileKeys * 128);
+        // 16 codes are two 16-byte chunks of the wide row; upper pieces store the second one first, which spreads the
+        // eight lanes of a row over all banks
+        const int chunk = (piece & 3) * 2, turned = piece >> 2;
+        TileWalk w;
+        bool ok = true;
+        uint32_t load = 0;
+        for (bool more_items = w.start(sh, p.geo, plan); more_items && ok; more_items = w.next(sh, p.geo)) {
+            for (int n = 2 * w.t0; n < 2 * w.t1 && ok; ++n, ++load) {   // K0 V0 K1 V1 ...
+                const uint32_t rs = load % kRaw, st = load % Cfg::kStages;
+                ok = warp_wait(smem_u32(&s_raw_full[rs]), (load / kRaw) & 1u, abort_flag, limit) &&
+                     (load < Cfg::kStages ||
+                      warp_wait(smem_u32(&s_kv_empty[st]), (load / Cfg::kStages - 1) & 1u, abort_flag, limit));
+                if (!ok) break;
+                const uint8_t* raw = raw_ptr + rs * Cfg::kRawBytes + row0 * DP + piece * 16;
+                uint8_t* wide = kv_ptr + st * Cfg::kStageBytes + out_x;
+                const int key0 = w.it.base + (n >> 1) * kTileKeys;
+                const bool ragged = key0 < w.it.lo || key0 + kTileKeys > w.it.hi;
+                auto pass = [&](int r, bool seen, uint32_t factor, uint32_t more) {   // row row0 + r
+                    uint4 v = *reinterpret_cast<const uint4*>(raw + r * DP), a, b;
+                    if (!seen) v = make_uint4(0, 0, 0, 0), factor = more = 0;   // whatever codes and scale are there
+                    widen16<T>(v, factor, more, a, b);
+                    uint8_t* dst = wide + (row0 + r) * 128;
+                    const int at = (chunk + turned) ^ ((row0 + r) & 7);
+                    *reinterpret_cast<uint4*>(dst + at * 16) = turned ? b : a;
+                    *reinterpret_cast<uint4*>(dst + (at ^ 1) * 16) = turned ? a : b;
+                };
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {   // 16 rows under one scale
+                    uint32_t more;
+                    const uint32_t factor =
+                        widen_factor<T>(s_raw_scale[rs][(warp - 12) * 2 + half], more);
+#pragma unroll
+                    for (int r = half * 16; r < half * 16 + 16; r += kRows) {
+                        const int key = key0 + row0 + r;
+                        pass(r, !ragged || (key >= w.it.lo && key < w.it.hi), factor, more);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&s_kv_full[st]));
+                    mbar_arrive(smem_u32(&s_raw_empty[rs]));
+                }
+            }
+        }
+        if (!ok && lane == 0 && !*reinterpret_cast<volatile int*>(&s_abort)) {
+            s_abort = 1;
+            set_error(sh.err, KT_DEVERR_TIMEOUT_LOAD);
+        }
+    } else if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kIssueRegs));
         TileWalk w;
         bool more_items = w.start(sh, p.geo, plan);
         if (warp == 9 || warp == 10) {
@@ -476,18 +595,54 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             const int box = lane % boxes;   // of 1, 2, 4 or 8 per 64 elements (page_size is a multiple of 16)
             const CUtensorMap* map = warp == 10 ? &vmap : &kmap;
             bool ok = true;
+            constexpr uint32_t kRing = KV8 ? kRaw : Cfg::kStages;
+            uint64_t* const ring_full = KV8 ? s_raw_full : s_kv_full;
+            uint64_t* const ring_empty = KV8 ? s_raw_empty : s_kv_empty;
+            const uint8_t* const scales = warp == 10 ? sh.v_scales : sh.k_scales;
             for (; more_items && ok; more_items = w.next(sh, p.geo)) {
                 const int32_t* pages = sh.block_table + w.b * sh.table_stride;
                 for (int j = w.t0; j < w.t1; ++j) {
-                    const uint32_t stage = load % Cfg::kStages, round = load / Cfg::kStages;
-                    const uint32_t full = smem_u32(&s_kv_full[stage]);
+                    const uint32_t stage = load % kRing, round = load / kRing;
+                    const uint32_t full = smem_u32(&ring_full[stage]);
+                    if constexpr (KV8) {
+                        // lane i: page and scale of keys 16 i to 16 i + 15, by the box they lie in
+                        const int my_box = lane * KT_KV8_BLOCK / p.geo.box_slots;
+                        const int box_key = w.it.base + j * kTileKeys + my_box * p.geo.box_slots;
+                        const int key = w.it.base + j * kTileKeys + lane * KT_KV8_BLOCK;
+                        int page = -1, scale = 127;
+                        if (lane < kTileKeys / KT_KV8_BLOCK && box_key < w.it.hi &&
+                            box_key + p.geo.box_slots > w.it.lo) {
+                            page = checked_page(sh, pages, box_key);
+                            if (page >= 0)
+                                scale = scales[(static_cast<long long>(page) * (sh.page_size / KT_KV8_BLOCK) +
+                                                key % sh.page_size / KT_KV8_BLOCK) * sh.kv_heads + w.h];
+                        }
+                        page = __shfl_sync(0xffffffffu, page, box * p.geo.box_slots / KT_KV8_BLOCK);
+                        if (round > 0) ok = warp_wait(smem_u32(&ring_empty[stage]), (round - 1) & 1u, abort_flag, limit);
+                        if (!ok) break;
+                        if (sh.withhold != 0 && blockIdx.x == 0 && load == 0) {   // test hook: the first keys
+                            load += 2;
+                            continue;
+                        }
+                        if (lane < kTileKeys / KT_KV8_BLOCK) s_raw_scale[stage][lane] = scale;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_expect_tx(full, Cfg::kRawBytes);
+                        __syncwarp();
+                        if (lane < boxes)
+                            tma_load_4d(smem_u32(raw_ptr) + stage * Cfg::kRawBytes + box * p.geo.box_slots * DP, map,
+                                        full, 0, (w.it.base + j * kTileKeys + box * p.geo.box_slots) % sh.page_size,
+                                        w.h, page);
+                        __syncwarp();
+                        load += 2;
+                        continue;
+                    }
                     // boxes that no row sees come from outside the cache, as zeros
                     const int key = w.it.base + j * kTileKeys + box * p.geo.box_slots;
                     int page = -1;
                     if (lane < boxes && key < w.it.hi && key + p.geo.box_slots > w.it.lo)
                         page = checked_page(sh, pages, key);
                     page = __shfl_sync(0xffffffffu, page, box);
-                    if (round > 0) ok = warp_wait(smem_u32(&s_kv_empty[stage]), (round - 1) & 1u, abort_flag, limit);
+                    if (round > 0) ok = warp_wait(smem_u32(&ring_empty[stage]), (round - 1) & 1u, abort_flag, limit);
                     if (!ok) break;
                     if (sh.withhold != 0 && blockIdx.x == 0 && load == 0) {   // test hook: the first keys
                         load += 2;
@@ -512,10 +667,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 // loads still in flight land before the CTA ends (each wait bounded)
                 int never = 0;
-                for (int i = 0; i < Cfg::kStages && load >= 2; ++i) {
+                for (uint32_t i = 0; i < (KV8 ? kRing / 2 : kRing) && load >= 2; ++i) {   // K and V share the ring
                     load -= 2;
-                    mbar_wait(smem_u32(&s_kv_full[load % Cfg::kStages]), (load / Cfg::kStages) & 1u, &never,
-                              kDrainLimitNs);
+                    mbar_wait(smem_u32(&ring_full[load % kRing]), (load / kRing) & 1u, &never, kDrainLimitNs);
                 }
             }
         } else if (warp == 11) {
@@ -663,7 +817,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
     } else {
         // ---------------------------------------------------- softmax of one row per thread
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Cfg::kSoftmaxRegs));
         const int grp = warp >> 2;
         const int row = tid & 127;
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -740,7 +894,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&s_p_full[grp][part]));
                 };
-                if (grp == 0 && j == rag) {
+                if (!KV8 && grp == 0 && j == rag) {
                     // Values past the sequence's end are whatever the page holds, and 0 x NaN is NaN: zeros, before
                     // this group lets the tile be multiplied (group 1's product is issued after it).
                     const uint32_t load = loads + 2 * static_cast<uint32_t>(j - w.t0) + 1;   // K0 V0 K1 V1 ...
@@ -986,9 +1140,9 @@ size_t attn_tile_workspace_bytes() {
     return c * 2 * 256 * (128 * sizeof(float) + sizeof(float2));
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool KV8>
 static kt_status launch_tile_typed(const AttnArgs& a, cudaStream_t s) {
-    using Cfg = TileCfg<DP>;
+    using Cfg = TileCfg<DP, KV8>;
     TileParams p{};
     p.sh = attn_shape(a);
     p.out = a.out.ptr;
@@ -998,18 +1152,22 @@ static kt_status launch_tile_typed(const AttnArgs& a, cudaStream_t s) {
     p.geo.box_slots = a.kv.page_size & -a.kv.page_size;
     if (p.geo.box_slots > kTileKeys) p.geo.box_slots = kTileKeys;
     CUtensorMap qmap, kmap, vmap;
+    auto encode = [&](CUtensorMap* m, bool values) {
+        return KV8 ? encode_kv8_map(m, a.kv, values, DP, p.geo.box_slots, CU_TENSOR_MAP_SWIZZLE_NONE)
+                   : encode_kv_map(m, a.kv, values, p.geo.box_slots);
+    };
     const uint64_t qd[3] = {static_cast<uint64_t>(a.kv.head_dim), static_cast<uint64_t>(a.q.heads),
                             static_cast<uint64_t>(a.batch.tokens)};
     const uint64_t qs[2] = {2 * static_cast<uint64_t>(a.q.head_stride), 2 * static_cast<uint64_t>(a.q.token_stride)};
     const uint32_t qb[3] = {64, static_cast<uint32_t>(p.sh.group), static_cast<uint32_t>(p.geo.tokens)};
     if (!encode_tiled_map(&qmap, a.kv.dtype, a.q.ptr, 3, qd, qs, qb, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
-        !encode_kv_map(&kmap, a.kv, false, p.geo.box_slots) || !encode_kv_map(&vmap, a.kv, true, p.geo.box_slots))
+        !encode(&kmap, false) || !encode(&vmap, true))
         return report(KT_ERR_CUDA, "tensor map encoding failed");
     static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(attn_tile_kernel<T, DP>,
+        const cudaError_t e = cudaFuncSetAttribute(attn_tile_kernel<T, DP, KV8>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
         if (e != cudaSuccess) return cuda_status(e);
         attr_set[dev] = true;
@@ -1019,17 +1177,21 @@ static kt_status launch_tile_typed(const AttnArgs& a, cudaStream_t s) {
     p.part_o = reinterpret_cast<float4*>(a.ws);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + c * 2 * 256 * 32);
     count_launches(1);
-    return cuda_status(launch_chained(attn_tile_kernel<T, DP>, dim3(static_cast<unsigned>(c)), dim3(kTileThreads),
+    return cuda_status(launch_chained(attn_tile_kernel<T, DP, KV8>, dim3(static_cast<unsigned>(c)), dim3(Cfg::kThreads),
                                       Cfg::kSmem, s, static_cast<const TileParams&>(p),
                                       static_cast<const CUtensorMap&>(qmap), static_cast<const CUtensorMap&>(kmap),
                                       static_cast<const CUtensorMap&>(vmap)));
 }
 
+template <typename T>
+static kt_status launch_tile_of(const AttnArgs& a, cudaStream_t s) {
+    if (a.k_scales != nullptr)
+        return a.kv.head_dim > 64 ? launch_tile_typed<T, 128, true>(a, s) : launch_tile_typed<T, 64, true>(a, s);
+    return a.kv.head_dim > 64 ? launch_tile_typed<T, 128, false>(a, s) : launch_tile_typed<T, 64, false>(a, s);
+}
+
 kt_status launch_attn_tile(const AttnArgs& a, cudaStream_t s) {
-    const bool wide = a.kv.head_dim > 64;
-    if (a.kv.dtype == KT_DTYPE_BF16)
-        return wide ? launch_tile_typed<__nv_bfloat16, 128>(a, s) : launch_tile_typed<__nv_bfloat16, 64>(a, s);
-    return wide ? launch_tile_typed<__half, 128>(a, s) : launch_tile_typed<__half, 64>(a, s);
+    return a.kv.dtype == KT_DTYPE_BF16 ? launch_tile_of<__nv_bfloat16>(a, s) : launch_tile_of<__half>(a, s);
 }
 
 }  // namespace kt

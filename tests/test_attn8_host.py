@@ -106,11 +106,11 @@ def test_the_statement_of_the_exponent():
 
 
 def test_rounding_statement():
-    """What off_by_a_rounding allows: the nearest number, and nothing a step further on."""
+    """What off_by_a_rounding allows: the nearest number, and nothing two steps further on (1.3 is more than 1.5 steps)."""
     v = torch.linspace(-500, 500, 4001, dtype=torch.float64)
     one = torch.ones(1, dtype=torch.float64)
     got = M.e4m3(v)
     assert float(M.off_by_a_rounding(got, one, v, 0 * v).max()) <= 0
-    inside = (v.abs() > 1) & (v.abs() < 400)
-    wrong = M.e4m3(got[inside] * 1.13)
+    inside = (v.abs() > 1) & (v.abs() < 300)
+    wrong = M.e4m3(got[inside] * 1.3)
     assert bool((M.off_by_a_rounding(wrong, one, v[inside], 0 * v[inside]) > 0).all())
