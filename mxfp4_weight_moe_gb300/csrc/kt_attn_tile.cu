@@ -61,7 +61,8 @@ constexpr uint32_t kTmemS = 0, kTmemO = 256;
 
 template <int DP, bool KV8>
 struct TileCfg {
-    static constexpr int kThreads = KV8 ? 512 : 384;
+    static constexpr int kWideners = 4;                  // warps
+    static constexpr int kThreads = KV8 ? 384 + 32 * kWideners : 384;
     static constexpr int kQBytes = 128 * DP * 2;         // one row group
     static constexpr int kStageBytes = kTileKeys * DP * 2;   // one tile of K or V
     static constexpr int kStages = KV8 ? (DP == 128 ? 4 : 8) : (DP == 128 ? 5 : 9);   // K and V alternate
@@ -72,7 +73,7 @@ struct TileCfg {
     static constexpr int kSmem = kQAll + kStages * kStageBytes + kRaw * kRawBytes + 1024;
     // registers a thread: of the softmax, of loads and MMAs, of the widening; their sum over 128 threads each (twice the
     // softmax) is the launch's 65536 (KV8) or 64512
-    static constexpr int kSoftmaxRegs = KV8 ? 192 : 208, kIssueRegs = KV8 ? 72 : 88, kWidenRegs = 56;
+    static constexpr int kSoftmaxRegs = KV8 ? 192 : 208, kIssueRegs = KV8 ? 56 : 88, kWidenRegs = 72;
 };
 
 struct TileGeometry {
@@ -417,10 +418,11 @@ __device__ __forceinline__ void widen16<__nv_bfloat16>(const uint4& v, uint32_t 
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t r[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {   // as widen_e4m3
-        const uint32_t u = __byte_perm(w[i / 2], 0, i & 1 ? 0x3424 : 0x1404);
-        const uint32_t x = ((u >> 4) & 0x07f007f0u) | (u & 0x80008000u);
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[i]) : "r"(x), "r"(factor));
+    for (int i = 0; i < 4; ++i) {   // as widen_e4m3, the high bytes of four numbers and the low ones at a time
+        const uint32_t high = ((w[i] & 0x70707070u) >> 4) | (w[i] & 0x80808080u);
+        const uint32_t low = (w[i] * 16u) & 0xf0f0f0f0u;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[2 * i]) : "r"(__byte_perm(low, high, 0x5140)), "r"(factor));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[2 * i + 1]) : "r"(__byte_perm(low, high, 0x7362)), "r"(factor));
     }
     if (more != 0) {   // the same for the block's lanes; hardly ever
 #pragma unroll
@@ -468,6 +470,7 @@ __global__ void __launch_bounds__(TileCfg<DP, KV8>::kThreads, 1)
     constexpr int kRaw = KV8 ? Cfg::kRaw : 1;
     __shared__ __align__(8) uint64_t s_raw_full[kRaw], s_raw_empty[kRaw];
     __shared__ int s_raw_scale[kRaw][kTileKeys / KT_KV8_BLOCK];
+    __shared__ int2 s_raw_rows[kRaw];   // rows [x, y) of a tile that some token sees; y < 0: no tile, the run's end
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_last[2];
     __shared__ long long s_counted[2];   // first tile of the last item that a group has counted
@@ -485,13 +488,13 @@ __global__ void __launch_bounds__(TileCfg<DP, KV8>::kThreads, 1)
         s_abort = 0;
         s_counted[0] = s_counted[1] = -1;
         for (int i = 0; i < Cfg::kStages; ++i) {
-            mbar_init(smem_u32(&s_kv_full[i]), KV8 ? 4 : 1);   // (the widening warps)
+            mbar_init(smem_u32(&s_kv_full[i]), KV8 ? Cfg::kWideners : 1);
             mbar_init(smem_u32(&s_kv_empty[i]), 1);
         }
         if (KV8)
             for (int i = 0; i < kRaw; ++i) {
                 mbar_init(smem_u32(&s_raw_full[i]), 1);
-                mbar_init(smem_u32(&s_raw_empty[i]), 4);
+                mbar_init(smem_u32(&s_raw_empty[i]), Cfg::kWideners);
             }
         for (int i = 0; i < 2; ++i) {
             for (int b = 0; b < Cfg::kQBufs; ++b) {
@@ -529,55 +532,71 @@ __global__ void __launch_bounds__(TileCfg<DP, KV8>::kThreads, 1)
     const unsigned long long limit = sh.wait_limit_ns;
 
     if (KV8 && warp >= 12) {
-        // ---------------------------------------------------- codes to T, 32 rows of a tile a warp
+        // ---------------------------------------------------- codes to T, 128 / kWideners rows of a tile a warp
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kWidenRegs));
-        constexpr int kPieces = DP / 16, kRows = 32 / kPieces;   // 16-byte pieces of a row; rows a pass
-        const int piece = lane % kPieces, row0 = (warp - 12) * 32 + lane / kPieces;
-        const uint32_t out_x = static_cast<uint32_t>(piece >> 2) * (kTileKeys * 128);
-        // 16 codes are two 16-byte chunks of the wide row; upper pieces store the second one first, which spreads the
-        // eight lanes of a row over all banks
-        const int chunk = (piece & 3) * 2, turned = piece >> 2;
-        TileWalk w;
+        constexpr int kBlocks = kTileKeys / KT_KV8_BLOCK / Cfg::kWideners;   // of rows under one scale
+        // Eight rows of four 16-byte pieces a pass.  A row's 16 codes are two 16-byte chunks of the wide row (piece p:
+        // 2p and 2p + 1, where its swizzle puts them): lanes 4 to 7 of eight take the row whose number differs in bits 0
+        // and 2, so that the eight meet all banks in loads and stores.
+        const int piece = lane & 3, row8 = (lane >> 3) ^ (lane & 4 ? 5 : 0);
+        const int row0 = (warp - 12) * (kTileKeys / Cfg::kWideners) + row8;
+        const uint32_t in0 = row0 * DP + (DP == 128 ? piece ^ row8 : piece) * 16;   // (128-byte rows are swizzled)
+        const uint32_t out0 = row0 * 128 + ((2 * piece) ^ row8) * 16;
         bool ok = true;
-        uint32_t load = 0;
-        for (bool more_items = w.start(sh, p.geo, plan); more_items && ok; more_items = w.next(sh, p.geo)) {
-            for (int n = 2 * w.t0; n < 2 * w.t1 && ok; ++n, ++load) {   // K0 V0 K1 V1 ...
-                const uint32_t rs = load % kRaw, st = load % Cfg::kStages;
-                ok = warp_wait(smem_u32(&s_raw_full[rs]), (load / kRaw) & 1u, abort_flag, limit) &&
-                     (load < Cfg::kStages ||
-                      warp_wait(smem_u32(&s_kv_empty[st]), (load / Cfg::kStages - 1) & 1u, abort_flag, limit));
-                if (!ok) break;
-                const uint8_t* raw = raw_ptr + rs * Cfg::kRawBytes + row0 * DP + piece * 16;
-                uint8_t* wide = kv_ptr + st * Cfg::kStageBytes + out_x;
-                const int key0 = w.it.base + (n >> 1) * kTileKeys;
-                const bool ragged = key0 < w.it.lo || key0 + kTileKeys > w.it.hi;
-                auto pass = [&](int r, bool seen, uint32_t factor, uint32_t more) {   // row row0 + r
-                    uint4 v = *reinterpret_cast<const uint4*>(raw + r * DP), a, b;
-                    if (!seen) v = make_uint4(0, 0, 0, 0), factor = more = 0;   // whatever codes and scale are there
-                    widen16<T>(v, factor, more, a, b);
-                    uint8_t* dst = wide + (row0 + r) * 128;
-                    const int at = (chunk + turned) ^ ((row0 + r) & 7);
-                    *reinterpret_cast<uint4*>(dst + at * 16) = turned ? b : a;
-                    *reinterpret_cast<uint4*>(dst + (at ^ 1) * 16) = turned ? a : b;
-                };
+        uint32_t rs = 0, raw_parity = 0, st = 0, parity = 1;   // (a first wait for an empty stage: it is)
+        while (true) {   // K0 V0 K1 V1 ...
+            ok = warp_wait(smem_u32(&s_raw_full[rs]), raw_parity, abort_flag, limit);
+            if (!ok) break;
+            const int2 seen = s_raw_rows[rs];
+            if (seen.y < 0) break;
+            const int* scales = &s_raw_scale[rs][(warp - 12) * kBlocks];
+            int top = scales[0];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {   // 16 rows under one scale
-                    uint32_t more;
-                    const uint32_t factor =
-                        widen_factor<T>(s_raw_scale[rs][(warp - 12) * 2 + half], more);
+            for (int i = 1; i < kBlocks; ++i) top = max(top, scales[i]);
+            ok = warp_wait(smem_u32(&s_kv_empty[st]), parity, abort_flag, limit);
+            if (!ok) break;
+            const uint8_t* raw = raw_ptr + rs * Cfg::kRawBytes;
+            uint8_t* wide = kv_ptr + st * Cfg::kStageBytes;
+            const bool ragged = seen.x > 0 || seen.y < kTileKeys;
+            // One copy of the code for a tile's blocks: straight code would not stay in the instruction cache beside the
+            // softmax's (one prompt of 8192, 64 / 8 heads of 128: 1641 us, 1054 so).  Powers that bf16's 2^120 leaves no
+            // room for, and tiles with rows that no token sees, have another copy.
+            auto tile = [&](auto plain) {
+                constexpr bool kPlain = decltype(plain)::value;
+                constexpr int kHalves = DP / 64, kPasses = 2 * kHalves;   // 8 rows of 64 elements each
+#pragma unroll 1
+                for (int i = 0; i < kBlocks; ++i) {
+                    uint32_t more, factor = widen_factor<T>(scales[i], more);
+                    const uint8_t* src = raw + i * KT_KV8_BLOCK * DP;
+                    uint8_t* dst = wide + i * KT_KV8_BLOCK * 128;
+                    uint4 v[kPasses];
 #pragma unroll
-                    for (int r = half * 16; r < half * 16 + 16; r += kRows) {
-                        const int key = key0 + row0 + r;
-                        pass(r, !ragged || (key >= w.it.lo && key < w.it.hi), factor, more);
+                    for (int k = 0; k < kPasses; ++k)
+                        v[k] = *reinterpret_cast<const uint4*>(src + (in0 ^ (k % kHalves * 64)) + k / kHalves * 8 * DP);
+#pragma unroll
+                    for (int k = 0; k < kPasses; ++k) {
+                        uint32_t f = factor, m = kPlain ? 0 : more;
+                        const int row = row0 + i * KT_KV8_BLOCK + k / kHalves * 8;
+                        if (!kPlain && (row < seen.x || row >= seen.y))
+                            v[k] = make_uint4(0, 0, 0, 0), f = m = 0;   // whatever codes and scale are there
+                        uint4 a, b;
+                        widen16<T>(v[k], f, m, a, b);
+                        uint8_t* out = dst + k % kHalves * (kTileKeys * 128) + k / kHalves * 8 * 128;
+                        *reinterpret_cast<uint4*>(out + out0) = a;
+                        *reinterpret_cast<uint4*>(out + (out0 ^ 16)) = b;
                     }
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&s_kv_full[st]));
-                    mbar_arrive(smem_u32(&s_raw_empty[rs]));
-                }
+            };
+            if (!ragged && top <= 134) tile(std::true_type());
+            else tile(std::false_type());
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&s_kv_full[st]));
+                mbar_arrive(smem_u32(&s_raw_empty[rs]));
             }
+            if (++rs == kRaw) rs = 0, raw_parity ^= 1u;
+            if (++st == Cfg::kStages) st = 0, parity ^= 1u;
         }
         if (!ok && lane == 0 && !*reinterpret_cast<volatile int*>(&s_abort)) {
             s_abort = 1;
@@ -625,6 +644,10 @@ __global__ void __launch_bounds__(TileCfg<DP, KV8>::kThreads, 1)
                             continue;
                         }
                         if (lane < kTileKeys / KT_KV8_BLOCK) s_raw_scale[stage][lane] = scale;
+                        if (lane == 0) {
+                            const int key0 = w.it.base + j * kTileKeys;
+                            s_raw_rows[stage] = make_int2(max(w.it.lo - key0, 0), min(max(w.it.hi - key0, 0), kTileKeys));
+                        }
                         __syncwarp();
                         if (lane == 0) mbar_arrive_expect_tx(full, Cfg::kRawBytes);
                         __syncwarp();
@@ -658,6 +681,14 @@ __global__ void __launch_bounds__(TileCfg<DP, KV8>::kThreads, 1)
                     }
                     __syncwarp();
                     load += 2;
+                }
+            }
+            if (KV8 && ok && warp == 9) {   // after the last keys: the widening warps' end
+                const uint32_t stage = load % kRing, round = load / kRing;
+                if (round > 0) ok = warp_wait(smem_u32(&ring_empty[stage]), (round - 1) & 1u, abort_flag, limit);
+                if (ok && lane == 0) {
+                    s_raw_rows[stage] = make_int2(0, -1);
+                    mbar_arrive(smem_u32(&ring_full[stage]));
                 }
             }
             if (!ok) {
@@ -1153,7 +1184,8 @@ static kt_status launch_tile_typed(const AttnArgs& a, cudaStream_t s) {
     if (p.geo.box_slots > kTileKeys) p.geo.box_slots = kTileKeys;
     CUtensorMap qmap, kmap, vmap;
     auto encode = [&](CUtensorMap* m, bool values) {
-        return KV8 ? encode_kv8_map(m, a.kv, values, DP, p.geo.box_slots, CU_TENSOR_MAP_SWIZZLE_NONE)
+        return KV8 ? encode_kv8_map(m, a.kv, values, DP, p.geo.box_slots,
+                                    DP == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE)
                    : encode_kv_map(m, a.kv, values, p.geo.box_slots);
     };
     const uint64_t qd[3] = {static_cast<uint64_t>(a.kv.head_dim), static_cast<uint64_t>(a.q.heads),
