@@ -1,5 +1,6 @@
 // kt_attn_api.cu -- the C ABI declared in include/kt_attn.h: argument checks
 // and the choice of kernel.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdarg>
@@ -414,7 +415,7 @@ static kt_status attention_impl(const kt_paged_kv* cache, const uint8_t* k_scale
     // kernel loads its queries by TMA, which needs strides.
     const long long rows = static_cast<long long>(max_q_len) * (q->heads / cache->heads);
     if (rows <= 16 || q->token_stride == 0 || q->head_stride == 0)
-        return launch_attn_split(a, static_cast<cudaStream_t>(stream));
+        return launch_attn_split(a, static_cast<int>(std::min(rows, 1024ll)), static_cast<cudaStream_t>(stream));
     return launch_attn_tile(a, static_cast<cudaStream_t>(stream));
 }
 

@@ -82,7 +82,8 @@ struct AttnArgs {
 };
 constexpr size_t kAttnMaxCounters = KT_PAGED_ATTENTION_ZEROED / sizeof(unsigned);
 size_t attn_split_workspace_bytes();
-kt_status launch_attn_split(const AttnArgs& a, cudaStream_t s);
+// rows: at most so many query rows a sequence and cache head are likely (picks the form, not the result)
+kt_status launch_attn_split(const AttnArgs& a, int rows, cudaStream_t s);
 size_t attn_tile_workspace_bytes();
 kt_status launch_attn_tile(const AttnArgs& a, cudaStream_t s);
 

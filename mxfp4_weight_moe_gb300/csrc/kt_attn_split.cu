@@ -39,25 +39,26 @@ namespace kt {
 constexpr int kSplitWarps = 4;
 constexpr int kSplitThreads = kSplitWarps * 32;
 constexpr int kSplitKeys = 16;                          // keys of one load (pages hold a multiple of it)
-constexpr int kSplitRows = 16;
-constexpr int kSplitCtasPerSm = 2;
 constexpr int kSplitMinUnits = 2;                       // least units of a piece
 constexpr int kSplitItemUnits = 3;                      // what an item costs besides its units, in units
 constexpr int kSplitJoinUnits = 4;                      // what cutting an item costs its last CTA, in units
 
-template <int DP, bool KV8>
+template <int DP, bool KV8, int ROWS>
 struct SplitCfg {
+    static constexpr int kRows = ROWS;                               // query rows of an item: 16, or 8 (KV8)
     static constexpr int kSub = DP == 128 && !KV8 ? 1 : 2;           // loads of K and of V that make a warp's block
     static constexpr int kBlockKeys = kSub * kSplitKeys;
     static constexpr int kUnit = kSplitWarps * kBlockKeys;           // keys of one unit
     static constexpr int kRowBytes = DP * (KV8 ? 1 : 2);             // of a key in a block
     static constexpr int kBlockBytes = kBlockKeys * kRowBytes;       // one of K, V
-    static constexpr int kStages = KV8 && DP == 64 ? 6 : 3;          // 24 KB a warp
+    static constexpr int kCtasPerSm = ROWS == 8 ? 3 : 2;
+    static constexpr int kStages = !KV8 ? 3 : (DP == 64 ? 2 : 1) * (ROWS == 8 ? 2 : 3);   // 24 KB a warp, 16 for 8 rows
     static constexpr int kRing = kStages * 2 * kBlockBytes;          // per warp
+    static constexpr int kMaxCtas = kSplitWarps * kRing / (kRows * 8);   // what a join of all of them has room for
     static constexpr int kSmem = kSplitWarps * kRing + 1024;
     static constexpr int kMergeRow = DP + 8;                         // floats of a row: rows start 8 banks apart
-    static constexpr int kMergeBytes = kSplitWarps * kSplitRows * kMergeRow * 4;
-    static constexpr int kParts = kSplitRows * DP / 4 / kSplitThreads;   // float4 per thread of 16 rows
+    static constexpr int kMergeBytes = kSplitWarps * kRows * kMergeRow * 4;
+    static constexpr int kParts = kRows * DP / 4 / kSplitThreads;   // float4 per thread of an item's rows
 };
 
 struct SplitParams {
@@ -70,14 +71,16 @@ struct SplitParams {
     unsigned* counters;  // [CTAs]
 };
 
-// Keys that the 16 rows of row tile rt see: [lo, hi); units of the item (at least one, so that its rows are written).
+// Keys that the rows of row tile rt see: [lo, hi); units of the item (at least one, so that its rows are written).
 struct SplitItem {
     int lo, hi, unit0, units;
 };
-__device__ __forceinline__ SplitItem split_item(const AttnShape& s, const SeqInfo& q, int rt, int unit) {
+template <typename Cfg>
+__device__ __forceinline__ SplitItem split_item(const AttnShape& s, const SeqInfo& q, int rt) {
+    constexpr int unit = Cfg::kUnit;
     SplitItem it;
-    const int t0 = rt * kSplitRows / s.group;
-    const int t1 = min((rt * kSplitRows + kSplitRows - 1) / s.group, q.q_len - 1);
+    const int t0 = rt * Cfg::kRows / s.group;
+    const int t1 = min((rt * Cfg::kRows + Cfg::kRows - 1) / s.group, q.q_len - 1);
     it.hi = max(0, min(q.first_pos + t1 + 1, q.keys));
     it.lo = window_start(q.first_pos + t0, s.window);
     if (it.lo >= it.hi) it.lo = it.hi = 0;
@@ -85,8 +88,9 @@ __device__ __forceinline__ SplitItem split_item(const AttnShape& s, const SeqInf
     it.units = max(1, (it.hi + unit - 1) / unit - it.unit0);
     return it;
 }
+template <typename Cfg>
 __device__ __forceinline__ int split_row_tiles(const AttnShape& s, const SeqInfo& q) {
-    return (q.q_len * s.group + kSplitRows - 1) / kSplitRows;
+    return (q.q_len * s.group + Cfg::kRows - 1) / Cfg::kRows;
 }
 
 // How the items are dealt to the CTAs.  Few items: each is cut into pieces of at most `piece` units, a CTA takes one
@@ -101,16 +105,18 @@ __device__ __forceinline__ int pieces_of(int units, int piece) { return (units +
 __device__ __forceinline__ int item_measure(const SplitItem& it, int piece) {
     return piece > 0 ? pieces_of(it.units, piece) : it.units + kSplitItemUnits;
 }
-__device__ __forceinline__ long long seq_measure(const AttnShape& s, int b, int piece, int unit) {
+template <typename Cfg>
+__device__ __forceinline__ long long seq_measure(const AttnShape& s, int b, int piece) {
     const SeqInfo q = seq_info(s, b);
-    const int tiles = split_row_tiles(s, q);
+    const int tiles = split_row_tiles<Cfg>(s, q);
     long long n = 0;
-    for (int rt = 0; rt < tiles; ++rt) n += item_measure(split_item(s, q, rt, unit), piece);
+    for (int rt = 0; rt < tiles; ++rt) n += item_measure(split_item<Cfg>(s, q, rt), piece);
     return n * s.kv_heads;
 }
 
 // All threads of the CTA; `shared` is theirs.
-__device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, int unit, SplitPlan* shared) {
+template <typename Cfg>
+__device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, SplitPlan* shared) {
     __shared__ long long s_units[kSplitWarps], s_items[kSplitWarps];
     __shared__ int s_most[kSplitWarps];
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
@@ -118,9 +124,9 @@ __device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, int unit, Sp
     int most = 0;
     for (int b = tid; b < s.seqs; b += kSplitThreads) {
         const SeqInfo q = seq_info(s, b);
-        const int tiles = split_row_tiles(s, q);
+        const int tiles = split_row_tiles<Cfg>(s, q);
         for (int rt = 0; rt < tiles; ++rt) {
-            const int n = split_item(s, q, rt, unit).units;
+            const int n = split_item<Cfg>(s, q, rt).units;
             units += n;
             most = max(most, n);
         }
@@ -165,7 +171,7 @@ __device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, int unit, Sp
     if (tid == 0) shared->seq = s.seqs;
     long long before = 0;
     for (int b0 = 0; b0 < s.seqs; b0 += kSplitThreads) {
-        const long long n = b0 + tid < s.seqs ? seq_measure(s, b0 + tid, piece, unit) : 0;
+        const long long n = b0 + tid < s.seqs ? seq_measure<Cfg>(s, b0 + tid, piece) : 0;
         long long incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -205,15 +211,15 @@ __device__ __forceinline__ uint32_t piece8(uint32_t base, int row, int piece) {
 // and 1 and 3: for S that is another order of the head's elements, which the queries follow; for O the lane's columns
 // are four neighbours.  The keys' power multiplies the scores, the values' the softmax weights (bf16) or the codes
 // (fp16, where a weight would leave the type's range).
-template <typename T, int DP, bool KV8>
-__global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
+template <typename T, int DP, bool KV8, int ROWS>
+__global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasPerSm)
     attn_split_kernel(const SplitParams p, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap) {
-    using Cfg = SplitCfg<DP, KV8>;
+    using Cfg = SplitCfg<DP, KV8, ROWS>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[kSplitWarps][Cfg::kStages];
     __shared__ int s_abort, s_last;
-    __shared__ float2 s_ml[kSplitWarps][kSplitRows];
+    __shared__ float2 s_ml[kSplitWarps][Cfg::kRows];
     __shared__ SplitPlan s_plan;
     __shared__ uint32_t s_scales[KV8 ? kSplitWarps : 1][Cfg::kStages][Cfg::kSub];   // of keys, of values << 8
     const AttnShape& sh = p.sh;
@@ -232,18 +238,18 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     }
     griddep_wait();
     griddep_launch_dependents();
-    const SplitPlan plan = split_plan(sh, Cfg::kUnit, &s_plan);
+    const SplitPlan plan = split_plan<Cfg>(sh, &s_plan);
     if (plan.seq >= sh.seqs) return;
 
     // ---- the item of this CTA's first piece or unit
     int b = plan.seq, rt = 0;
     SeqInfo sq = seq_info(sh, b);
-    int row_tiles = split_row_tiles(sh, sq);
-    SplitItem it = split_item(sh, sq, 0, Cfg::kUnit);
+    int row_tiles = split_row_tiles<Cfg>(sh, sq);
+    SplitItem it = split_item<Cfg>(sh, sq, 0);
     long long at = plan.in_seq;
     while (at >= static_cast<long long>(item_measure(it, plan.piece)) * sh.kv_heads) {
         at -= static_cast<long long>(item_measure(it, plan.piece)) * sh.kv_heads;
-        it = split_item(sh, sq, ++rt, Cfg::kUnit);
+        it = split_item<Cfg>(sh, sq, ++rt);
     }
     int h, u0, u1;                 // cache head; the item's units in this run
     long long first = 0;           // line: the item's first unit
@@ -331,15 +337,36 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
         for (int i = 0; i < min(n_blocks, Cfg::kStages); ++i) issue(i0 + i);
         if (KV8) __syncwarp();   // the scales of those blocks
 
-        // ---- queries: rows g and g + 8 of the tile in the MMA's A layout
+        auto block_ready = [&](int i) -> bool {   // whole warp
+            const uint32_t seq_no = loads + static_cast<uint32_t>(i - i0);
+            const uint32_t st = seq_no % Cfg::kStages;
+            if (warp_wait(smem_u32(&s_full[warp][st]), (seq_no / Cfg::kStages) & 1u, &s_abort, sh.wait_limit_ns))
+                return true;
+            if (lane == 0 && !*reinterpret_cast<volatile int*>(&s_abort)) {
+                s_abort = 1;
+                set_error(sh.err, KT_DEVERR_TIMEOUT_LOAD);
+            }
+            // loads still in flight land before their memory has another use (each wait bounded)
+            int never = 0;
+            for (int k = i; k < min(i + Cfg::kStages, i1); ++k) {
+                const uint32_t no = loads + static_cast<uint32_t>(k - i0);
+                mbar_wait(smem_u32(&s_full[warp][no % Cfg::kStages]), (no / Cfg::kStages) & 1u, &never, kDrainLimitNs);
+            }
+            gave_up = true;
+            return false;
+        };
         const int g = lane >> 2, t4 = lane & 3;
+        const int rows = min(Cfg::kRows, sq.q_len * sh.group - rt * Cfg::kRows);   // of the tile that hold tokens
+        float* const mo = merge + warp * Cfg::kRows * Cfg::kMergeRow;
+        if constexpr (ROWS == 16) {
+        // ---- queries: rows g and g + 8 of the tile in the MMA's A layout
         uint32_t qa[DP / 16][4];
         int last_key[2], first_key[2];   // what the row sees; rows of no token need no mask
         {
             const T* qp[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int row = rt * kSplitRows + g + 8 * e;
+                const int row = rt * Cfg::kRows + g + 8 * e;
                 const int tok = row / sh.group;
                 const bool ok = tok < sq.q_len;
                 last_key[e] = ok ? min(sq.first_pos + tok, sq.keys - 1) : 0x7fffffff;
@@ -376,23 +403,8 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
         for (int i = i0; i < i1; ++i) {
-            const uint32_t seq_no = loads + static_cast<uint32_t>(i - i0);
-            const uint32_t st = seq_no % Cfg::kStages;
-            if (!warp_wait(smem_u32(&s_full[warp][st]), (seq_no / Cfg::kStages) & 1u, &s_abort, sh.wait_limit_ns)) {
-                if (lane == 0 && !*reinterpret_cast<volatile int*>(&s_abort)) {
-                    s_abort = 1;
-                    set_error(sh.err, KT_DEVERR_TIMEOUT_LOAD);
-                }
-                // loads still in flight land before their memory has another use (each wait bounded)
-                int never = 0;
-                for (int k = i; k < min(i + Cfg::kStages, i1); ++k) {
-                    const uint32_t no = loads + static_cast<uint32_t>(k - i0);
-                    mbar_wait(smem_u32(&s_full[warp][no % Cfg::kStages]), (no / Cfg::kStages) & 1u, &never,
-                              kDrainLimitNs);
-                }
-                gave_up = true;
-                break;
-            }
+            if (!block_ready(i)) break;
+            const uint32_t st = (loads + static_cast<uint32_t>(i - i0)) % Cfg::kStages;
             const uint32_t kb = smem_u32(ring + st * 2 * Cfg::kBlockBytes);
             const uint32_t vb = kb + Cfg::kBlockBytes;
             const int key0 = base + i * Cfg::kUnit;
@@ -552,11 +564,9 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
         }
 
-        // ---- join the warps: a thread takes the float4 tid, tid + 128, .. of the tile's rows that hold tokens
-        const int rows = min(kSplitRows, sq.q_len * sh.group - rt * kSplitRows);
+        // ---- join the warps: a thread takes the float4 tid, tid + 128, .. of the rows
         __syncthreads();
         {
-            float* mo = merge + warp * kSplitRows * Cfg::kMergeRow;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 if (8 * e >= rows) break;
@@ -573,6 +583,163 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                 }
                 if (t4 == 0) s_ml[warp][g + 8 * e] = make_float2(m[e], l[e]);
             }
+        }
+        } else {
+        // ---- eight rows: S^T = K Q^T and O^T += V^T P^T, so that keys and head elements are the products' 16 rows and
+        // the query rows their 8 columns: half the products and half the registers of the other form.  Query row r of
+        // the tile is a lane's column: queries in the MMA's B layout are row g's, scores and sums rows 2t and 2t + 1's.
+        uint32_t qb[DP / 16][2];
+        int last_key[2], first_key[2];
+        {
+            const int row = rt * 8 + g, tok = row / sh.group;
+            const T* qp = static_cast<const T*>(p.q) + static_cast<long long>(sq.first_token + tok) * p.q_token +
+                          static_cast<long long>(h * sh.group + row - tok * sh.group) * p.q_head;
+            const bool ok = g < rows;
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks) {
+                const int d = ks * 16 + t4 * 4;
+                const uint32_t lo = ok && d < sh.head_dim ? *reinterpret_cast<const uint32_t*>(qp + d) : 0u;
+                const uint32_t hi = ok && d < sh.head_dim ? *reinterpret_cast<const uint32_t*>(qp + d + 2) : 0u;
+                qb[ks][0] = __byte_perm(lo, hi, 0x5410);   // elements 4t and 4t + 2, 4t + 1 and 4t + 3 of the 16
+                qb[ks][1] = __byte_perm(lo, hi, 0x7632);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = t4 * 2 + e, t = (rt * 8 + r) / sh.group;
+                last_key[e] = r < rows ? min(sq.first_pos + t, sq.keys - 1) : 0x7fffffff;
+                first_key[e] = r < rows ? window_start(sq.first_pos + t, sh.window) : 0;
+            }
+        }
+        float o[DP / 16][4];   // elements 2g and 2g + 1 of each 16, rows 2t and 2t + 1
+#pragma unroll
+        for (int n = 0; n < DP / 16; ++n)
+#pragma unroll
+            for (int f = 0; f < 4; ++f) o[n][f] = 0.0f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        for (int i = i0; i < i1; ++i) {
+            if (!block_ready(i)) break;
+            const uint32_t st = (loads + static_cast<uint32_t>(i - i0)) % Cfg::kStages;
+            const uint32_t kb = smem_u32(ring + st * 2 * Cfg::kBlockBytes);
+            const uint32_t vb = kb + Cfg::kBlockBytes;
+            const int key0 = base + i * Cfg::kUnit;
+            float sc[Cfg::kSub][4];   // keys g and g + 8 of each 16, rows 2t and 2t + 1
+#pragma unroll
+            for (int c = 0; c < Cfg::kSub * 4; ++c) sc[c / 4][c % 4] = 0.0f;
+            float v_scale[Cfg::kSub];
+            const int krow = (lane & 7) + ((lane >> 4) << 3);
+            const uint32_t one = std::is_same<T, __half>::value ? 0x3c003c00u : kBf16Widen;
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ks += 2)
+#pragma unroll
+                for (int sub = 0; sub < Cfg::kSub; ++sub) {
+                    uint32_t kf[4];   // keys 0-7 and 8-15 of two steps of 16 elements
+                    ldmatrix_x4(kf, piece8<DP>(kb + sub * kSplitKeys * DP, krow, ks + ((lane >> 3) & 1)));
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        uint32_t a[4];
+                        widen_e4m3<T>(kf[f], one, a[0], a[2]);
+                        widen_e4m3<T>(kf[f + 2], one, a[1], a[3]);
+                        mma_16816<T>(sc[sub], a, qb[ks + f][0], qb[ks + f][1]);
+                    }
+                }
+            const bool masked = __any_sync(0xffffffffu, min(last_key[0], last_key[1]) < key0 + Cfg::kBlockKeys - 1 ||
+                                                            max(first_key[0], first_key[1]) > key0);
+#pragma unroll
+            for (int sub = 0; sub < Cfg::kSub; ++sub) {
+                const uint32_t scales = s_scales[warp][st][sub];
+                const float k_scale = sh.scale_log2 * e8m0_power(scales & 255u);
+                v_scale[sub] = e8m0_power(scales >> 8);
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    sc[sub][f] *= k_scale;
+                    const int key = key0 + sub * kSplitKeys + g + (f >> 1) * 8;
+                    if (masked && (key > last_key[f & 1] || key < first_key[f & 1])) sc[sub][f] = -INFINITY;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float top = fmaxf(sc[0][e], sc[0][e + 2]);
+#pragma unroll
+                for (int sub = 1; sub < Cfg::kSub; ++sub) top = fmaxf(top, fmaxf(sc[sub][e], sc[sub][e + 2]));
+#pragma unroll
+                for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                const float mn = fmaxf(m[e], top);
+                const float base_m = mn == -INFINITY ? 0.0f : mn;
+                const float scale = ex2(m[e] - base_m);
+                m[e] = mn;
+                float sum = 0.0f;
+#pragma unroll
+                for (int sub = 0; sub < Cfg::kSub; ++sub)
+#pragma unroll
+                    for (int f = e; f < 4; f += 2) {
+                        sc[sub][f] = ex2(sc[sub][f] - base_m);
+                        sum += sc[sub][f];
+                    }
+                l[e] = l[e] * scale + sum;
+                if (__any_sync(0xffffffffu, scale != 1.0f)) {
+#pragma unroll
+                    for (int n = 0; n < DP / 16; ++n) {
+                        o[n][e] *= scale;
+                        o[n][e + 2] *= scale;
+                    }
+                }
+            }
+            // ---- the weights turned to the B layout, in two parts
+            const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3);
+            const bool ragged = key0 + Cfg::kBlockKeys > it.hi || key0 < it.lo;
+            constexpr bool kScaledWeights = std::is_same<T, __nv_bfloat16>::value;
+#pragma unroll
+            for (int sub = 0; sub < Cfg::kSub; ++sub) {
+                uint32_t pa[2], pb[2];
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {   // keys 0-7, 8-15
+                    float lo = sc[sub][2 * f], hi = sc[sub][2 * f + 1];
+                    if (kScaledWeights) lo *= v_scale[sub], hi *= v_scale[sub];
+                    pa[f] = pack2<T>(lo, hi);
+                    pb[f] = transpose_8x8(pack2<T>(lo - low_of<T>(pa[f]), hi - high_of<T>(pa[f])));
+                    pa[f] = transpose_8x8(pa[f]);
+                }
+                const uint32_t factor = kScaledWeights ? kBf16Widen : pack2<T>(v_scale[sub], v_scale[sub]);
+#pragma unroll
+                for (int n = 0; n < DP / 16; n += 2) {
+                    uint32_t vf[4];   // keys 0-7 and 8-15 of two times 16 elements
+                    ldmatrix_x4_trans(vf, piece8<DP>(vb + sub * kSplitKeys * DP, vrow, n + (lane >> 4)));
+                    if (ragged) {   // value rows that no token sees
+                        const int key = key0 + sub * kSplitKeys + t4 * 2;
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const int k = key + (f & 1) * 8;
+                            if (k >= it.hi || k < it.lo) vf[f] &= 0xffff0000u;
+                            if (k + 1 >= it.hi || k + 1 < it.lo) vf[f] &= 0x0000ffffu;
+                        }
+                    }
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        uint32_t a[4];
+                        widen_e4m3<T>(vf[2 * f], factor, a[0], a[1]);
+                        widen_e4m3<T>(vf[2 * f + 1], factor, a[2], a[3]);
+                        mma_16816<T>(o[n + f], a, pa[0], pa[1]);
+                        mma_16816<T>(o[n + f], a, pb[0], pb[1]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (i + Cfg::kStages < i1) issue(i + Cfg::kStages);
+        }
+        loads += static_cast<uint32_t>(n_blocks);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int x = 4; x < 32; x *= 2) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int n = 0; n < DP / 16; ++n)
+                *reinterpret_cast<float2*>(mo + (t4 * 2 + e) * Cfg::kMergeRow + n * 16 + g * 2) =
+                    make_float2(o[n][e], o[n][e + 2]);
+            if (g == 0) s_ml[warp][t4 * 2 + e] = make_float2(m[e], l[e]);
+        }
         }
         __syncthreads();
         float4 acc[Cfg::kParts];
@@ -594,7 +761,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                 const float2 e = s_ml[w][row];
                 const float f = ex2(e.x - ref);
                 const float4 v =
-                    *reinterpret_cast<const float4*>(merge + (w * kSplitRows + row) * Cfg::kMergeRow + d);
+                    *reinterpret_cast<const float4*>(merge + (w * Cfg::kRows + row) * Cfg::kMergeRow + d);
                 sum += f * e.y;
                 a.x += f * v.x;
                 a.y += f * v.y;
@@ -605,7 +772,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
             ml[k] = make_float2(top, sum);
         }
         auto store = [&](int row, float4 a, float2 e) {
-            const int r = rt * kSplitRows + row;
+            const int r = rt * Cfg::kRows + row;
             const int tok = r / sh.group;
             const int head = h * sh.group + r - tok * sh.group;
             if (d >= sh.head_dim) return;
@@ -643,8 +810,8 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
             for (int k = 0; k < Cfg::kParts; ++k) {
                 const int row = part_row(k);
                 if (row >= rows) break;
-                p.part_o[(slot * kSplitRows + row) * (DP / 4) + d / 4] = acc[k];
-                if (d == 0) p.part_ml[slot * kSplitRows + row] = ml[k];
+                p.part_o[(slot * Cfg::kRows + row) * (DP / 4) + d / 4] = acc[k];
+                if (d == 0) p.part_ml[slot * Cfg::kRows + row] = ml[k];
             }
             __syncthreads();
             if (tid == 0) {
@@ -657,10 +824,10 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
             __syncthreads();
             if (s_last) {
                 // maxima and sums of all pieces into shared memory, then their outputs, several loads under way
-                float2* all = reinterpret_cast<float2*>(ring_base + Cfg::kMergeBytes);   // [pieces][16]
+                float2* all = reinterpret_cast<float2*>(ring_base);   // [pieces][16]; the merge is over
                 auto slot_of = [&](int c) { return 2 * (c0 + c) + (c == 0 ? 1 : 0); };
-                for (int i = tid; i < n * kSplitRows; i += kSplitThreads)
-                    all[i] = __ldcg(&p.part_ml[slot_of(i / kSplitRows) * kSplitRows + i % kSplitRows]);
+                for (int i = tid; i < n * Cfg::kRows; i += kSplitThreads)
+                    all[i] = __ldcg(&p.part_ml[slot_of(i / Cfg::kRows) * Cfg::kRows + i % Cfg::kRows]);
                 __syncthreads();
                 auto join = [&](auto live) {   // live: parts per thread that hold rows, so that 16 loads are under way
                     constexpr int kLive = decltype(live)::value;
@@ -669,7 +836,7 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                     for (int k = 0; k < kLive; ++k) {
                         const int row = part_row(k);
                         float top = -INFINITY;
-                        for (int c = 0; c < n; ++c) top = fmaxf(top, all[c * kSplitRows + row].x);
+                        for (int c = 0; c < n; ++c) top = fmaxf(top, all[c * Cfg::kRows + row].x);
                         ref[k] = top == -INFINITY ? 0.0f : top;
                         ml[k] = make_float2(top, 0.0f);
                         acc[k] = make_float4(0, 0, 0, 0);
@@ -679,9 +846,9 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
 #pragma unroll
                         for (int k = 0; k < kLive; ++k) {
                             const int row = part_row(k);
-                            const float2 e = all[c * kSplitRows + row];
+                            const float2 e = all[c * Cfg::kRows + row];
                             const float4 v = row < rows
-                                                 ? __ldcg(&p.part_o[(slot_of(c) * kSplitRows + row) * (DP / 4) + d / 4])
+                                                 ? __ldcg(&p.part_o[(slot_of(c) * Cfg::kRows + row) * (DP / 4) + d / 4])
                                                  : make_float4(0, 0, 0, 0);
                             const float f = ex2(e.x - ref[k]);
                             ml[k].y += f * e.y;
@@ -714,10 +881,10 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
                 do {
                     if (++b >= sh.seqs) return;
                     sq = seq_info(sh, b);
-                    row_tiles = split_row_tiles(sh, sq);
+                    row_tiles = split_row_tiles<Cfg>(sh, sq);
                 } while (row_tiles == 0);
             }
-            it = split_item(sh, sq, rt, Cfg::kUnit);
+            it = split_item<Cfg>(sh, sq, rt);
         }
         u0 = 0;
         u1 = static_cast<int>(min(end - first, static_cast<long long>(it.units)));
@@ -727,18 +894,19 @@ __global__ void __launch_bounds__(kSplitThreads, kSplitCtasPerSm)
     }
 }
 
+template <typename Cfg>
 static int split_ctas() {
-    return std::min(sm_count() * kSplitCtasPerSm, static_cast<int>(kAttnMaxCounters));
+    return std::min(sm_count() * Cfg::kCtasPerSm, std::min(static_cast<int>(kAttnMaxCounters), Cfg::kMaxCtas));
 }
 
 size_t attn_split_workspace_bytes() {
-    const size_t c = static_cast<size_t>(split_ctas());
-    return c * 2 * kSplitRows * (128 + 2) * sizeof(float);
+    const size_t c = static_cast<size_t>(std::max(split_ctas<SplitCfg<128, false, 16>>(), split_ctas<SplitCfg<128, true, 16>>()));
+    return c * 2 * 16 * (128 + 2) * sizeof(float);
 }
 
-template <typename T, int DP, bool KV8>
+template <typename T, int DP, bool KV8, int ROWS>
 static kt_status launch_split_typed(const AttnArgs& a, cudaStream_t s) {
-    using Cfg = SplitCfg<DP, KV8>;
+    using Cfg = SplitCfg<DP, KV8, ROWS>;
     CUtensorMap kmap, vmap;
     auto encode = [&](CUtensorMap* m, bool values) {
         const CUtensorMapSwizzle swizzle = DP == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
@@ -750,7 +918,7 @@ static kt_status launch_split_typed(const AttnArgs& a, cudaStream_t s) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<T, DP, KV8>,
+        const cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<T, DP, KV8, ROWS>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
         if (e != cudaSuccess) return cuda_status(e);
         attr_set[dev] = true;
@@ -763,25 +931,26 @@ static kt_status launch_split_typed(const AttnArgs& a, cudaStream_t s) {
     p.q_head = a.q.head_stride;
     p.o_token = a.out.token_stride;
     p.o_head = a.out.head_stride;
-    const size_t c = static_cast<size_t>(split_ctas());
+    const size_t c = static_cast<size_t>(split_ctas<Cfg>());
     p.counters = a.counters;
     p.part_o = reinterpret_cast<float4*>(a.ws);
-    p.part_ml = reinterpret_cast<float2*>(p.part_o + c * 2 * kSplitRows * 32);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + c * 2 * Cfg::kRows * 32);
     count_launches(1);
-    return cuda_status(launch_chained(attn_split_kernel<T, DP, KV8>, dim3(static_cast<unsigned>(c)), dim3(kSplitThreads),
+    return cuda_status(launch_chained(attn_split_kernel<T, DP, KV8, ROWS>, dim3(static_cast<unsigned>(c)), dim3(kSplitThreads),
                                       Cfg::kSmem, s, static_cast<const SplitParams&>(p),
                                       static_cast<const CUtensorMap&>(kmap), static_cast<const CUtensorMap&>(vmap)));
 }
 
 template <typename T>
-static kt_status launch_split_of(const AttnArgs& a, cudaStream_t s) {
-    if (a.k_scales != nullptr)
-        return a.kv.head_dim > 64 ? launch_split_typed<T, 128, true>(a, s) : launch_split_typed<T, 64, true>(a, s);
-    return a.kv.head_dim > 64 ? launch_split_typed<T, 128, false>(a, s) : launch_split_typed<T, 64, false>(a, s);
+static kt_status launch_split_of(const AttnArgs& a, int rows, cudaStream_t s) {
+    const bool wide = a.kv.head_dim > 64;
+    if (a.k_scales == nullptr) return wide ? launch_split_typed<T, 128, false, 16>(a, s) : launch_split_typed<T, 64, false, 16>(a, s);
+    if (rows <= 8) return wide ? launch_split_typed<T, 128, true, 8>(a, s) : launch_split_typed<T, 64, true, 8>(a, s);
+    return wide ? launch_split_typed<T, 128, true, 16>(a, s) : launch_split_typed<T, 64, true, 16>(a, s);
 }
 
-kt_status launch_attn_split(const AttnArgs& a, cudaStream_t s) {
-    return a.kv.dtype == KT_DTYPE_BF16 ? launch_split_of<__nv_bfloat16>(a, s) : launch_split_of<__half>(a, s);
+kt_status launch_attn_split(const AttnArgs& a, int rows, cudaStream_t s) {
+    return a.kv.dtype == KT_DTYPE_BF16 ? launch_split_of<__nv_bfloat16>(a, rows, s) : launch_split_of<__half>(a, rows, s);
 }
 
 }  // namespace kt
