@@ -176,6 +176,20 @@ __device__ __forceinline__ void mma_16816<__half>(float (&d)[4], const uint32_t 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The first product of a sum, fp16.
+__device__ __forceinline__ void mma_16816_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+        " {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // Pairs of fp32 in one instruction.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
     uint64_t r;
@@ -234,30 +248,6 @@ __device__ __forceinline__ float high_of(uint32_t v) {
     if (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(v & 0xffff0000u);
     return __half2float(__ushort_as_half(static_cast<unsigned short>(v >> 16)));
 }
-// Four e4m3 codes as two pairs of T: bytes 0 and 2, bytes 1 and 3, times `factor` (a pair of T).  For bf16, which has
-// no conversion from e4m3, the code's bits are put where bf16 has them (an e4m3 exponent of 7 means 0, a bf16 exponent
-// of 127 does, and subnormal codes become subnormal numbers): what stands there is 2^-120 of the value, so that the
-// factor holds 2^120 besides.  NaN codes do not come out as NaN.
-template <typename T>
-__device__ __forceinline__ void widen_e4m3(uint32_t w, uint32_t factor, uint32_t& even, uint32_t& odd);
-template <>
-__device__ __forceinline__ void widen_e4m3<__nv_bfloat16>(uint32_t w, uint32_t factor, uint32_t& even, uint32_t& odd) {
-    const uint32_t e = ((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u);
-    const uint32_t o = ((w >> 4) & 0x07f007f0u) | (w & 0x80008000u);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(even) : "r"(e), "r"(factor));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(odd) : "r"(o), "r"(factor));
-}
-template <>
-__device__ __forceinline__ void widen_e4m3<__half>(uint32_t w, uint32_t factor, uint32_t& even, uint32_t& odd) {
-    const uint32_t s = __byte_perm(w, 0, 0x3120);
-    uint32_t e, o;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(e) : "h"(static_cast<unsigned short>(s)));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o) : "h"(static_cast<unsigned short>(s >> 16)));
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(even) : "r"(e), "r"(factor));
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(odd) : "r"(o), "r"(factor));
-}
-constexpr uint32_t kBf16Widen = 0x7b807b80u;   // 2^120 twice
-
 // 2^(byte - 127) of a scale byte, NaN for 255 (byte 0 as 2^-126: no subnormals, which a product might flush).
 __device__ __forceinline__ float e8m0_power(int byte) {
     return __uint_as_float(byte == 255 ? 0x7fc00000u : static_cast<uint32_t>(max(byte, 1)) << 23);

@@ -93,7 +93,24 @@ __device__ __forceinline__ int split_row_tiles(const AttnShape& s, const SeqInfo
     return (q.q_len * s.group + Cfg::kRows - 1) / Cfg::kRows;
 }
 
-// How the items are dealt to the CTAs.  Few items: each is cut into pieces of at most `piece` units, a CTA takes one
+// The order of the CTAs.  A slot's heads lie side by side in memory, and a head's row of an 8-bit cache is 128 bytes at
+// most: read at different times, such rows come at 5.5 TB/s (64 single tokens after up to 16383, 8 heads of 128: 264 us),
+// where each head's slots follow one another at 6.7.  So there the runs are those of one head, and neighbouring CTAs
+// take the same run of neighbouring heads (XXX us), unless there are so many heads that CTAs would be left over.
+struct SplitOrder {
+    int runs;         // CTAs that share a line
+    int heads;        // cache heads on a line
+    int run, head;    // this CTA's
+    int step, first;  // CTA of run r of the line: r * step + first
+};
+template <bool KV8>
+__device__ __forceinline__ SplitOrder split_order(const AttnShape& s) {
+    const int ctas = static_cast<int>(gridDim.x), cta = static_cast<int>(blockIdx.x);
+    if (!KV8 || s.kv_heads * 8 > ctas) return SplitOrder{ctas, s.kv_heads, cta, 0, 1, 0};
+    return SplitOrder{ctas / s.kv_heads, 1, cta / s.kv_heads, cta % s.kv_heads, s.kv_heads, cta % s.kv_heads};
+}
+
+// How the items are dealt to the CTAs of a line.  Few items: each is cut into pieces of at most `piece` units, a CTA takes one
 // piece (piece > 0).  Many: they lie on a line, kSplitItemUnits before each one's units, that is cut into equal runs
 // (piece == 0).  In both, [begin, begin + per) of `total` are this CTA's, in pieces or in units of the line.
 struct SplitPlan {
@@ -106,17 +123,17 @@ __device__ __forceinline__ int item_measure(const SplitItem& it, int piece) {
     return piece > 0 ? pieces_of(it.units, piece) : it.units + kSplitItemUnits;
 }
 template <typename Cfg>
-__device__ __forceinline__ long long seq_measure(const AttnShape& s, int b, int piece) {
+__device__ __forceinline__ long long seq_measure(const AttnShape& s, int b, int piece, int heads) {
     const SeqInfo q = seq_info(s, b);
     const int tiles = split_row_tiles<Cfg>(s, q);
     long long n = 0;
     for (int rt = 0; rt < tiles; ++rt) n += item_measure(split_item<Cfg>(s, q, rt), piece);
-    return n * s.kv_heads;
+    return n * heads;
 }
 
 // All threads of the CTA; `shared` is theirs.
 template <typename Cfg>
-__device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, SplitPlan* shared) {
+__device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, const SplitOrder& order, SplitPlan* shared) {
     __shared__ long long s_units[kSplitWarps], s_items[kSplitWarps];
     __shared__ int s_most[kSplitWarps];
     const int tid = static_cast<int>(threadIdx.x), lane = tid & 31, warp = tid >> 5;
@@ -151,9 +168,9 @@ __device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, SplitPlan* s
         items += s_items[w];
         most = max(most, s_most[w]);
     }
-    units *= s.kv_heads;
-    items *= s.kv_heads;
-    const long long ctas = gridDim.x;
+    units *= order.heads;
+    items *= order.heads;
+    const long long ctas = order.runs;
     const long long line = units + items * kSplitItemUnits;
     const long long run = (line + ctas - 1) / ctas;
     int piece = 0;
@@ -166,12 +183,12 @@ __device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, SplitPlan* s
     SplitPlan plan;
     plan.piece = piece;
     plan.per = piece > 0 ? 1 : (run > kSplitItemUnits + kSplitMinUnits ? run : kSplitItemUnits + kSplitMinUnits);
-    plan.begin = plan.per * blockIdx.x;
+    plan.begin = plan.per * order.run;
     // the sequence of this CTA's first piece or unit
     if (tid == 0) shared->seq = s.seqs;
     long long before = 0;
     for (int b0 = 0; b0 < s.seqs; b0 += kSplitThreads) {
-        const long long n = b0 + tid < s.seqs ? seq_measure<Cfg>(s, b0 + tid, piece) : 0;
+        const long long n = b0 + tid < s.seqs ? seq_measure<Cfg>(s, b0 + tid, piece, order.heads) : 0;
         long long incl = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -206,11 +223,21 @@ __device__ __forceinline__ uint32_t piece8(uint32_t base, int row, int piece) {
     return DP == 128 ? base + row * 128 + ((piece ^ (row & 7)) << 4) : base + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
 }
 
-// KV8: the cache's elements are e4m3 codes with a power of two for 16 keys of a head.  Codes go through ldmatrix as
-// pairs and are widened to T (exactly) in registers.  Of four codes that a lane gets, the products take bytes 0 and 2,
-// and 1 and 3: for S that is another order of the head's elements, which the queries follow; for O the lane's columns
-// are four neighbours.  The keys' power multiplies the scores, the values' the softmax weights (bf16) or the codes
-// (fp16, where a weight would leave the type's range).
+// KV8: the cache's elements are e4m3 codes with a power of two for 16 keys of a head.  The products are fp16 ones,
+// which e4m3 has a conversion to (bf16 has none: bits moved by hand take 2.2 instructions an element, and 265 us for 64
+// single tokens after up to 16383): codes go in without their powers, exact; bf16 queries times a power of two per row,
+// exact down to 2^-31 of the row's largest element and off by at most 2^-40 of that below; softmax weights, their
+// value's power included, relative to the largest of the row in the block's 32 keys, times 2^10: rounded to 11 bits
+// down to 2^-24 of that largest and off by at most 2^-35 of it below.  For fp16 results, which have as many bits, the
+// weights go in in two parts.
+constexpr float kWeightLog2 = 10.0f;   // the largest weight of a block, log2; O stays multiplied by that to the end
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// Codes 0 and 1 (in `lo`), 2 and 3 as pairs of fp16.
+__device__ __forceinline__ void widen_e4m3(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<unsigned short>(w)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<unsigned short>(w >> 16)));
+}
+
 template <typename T, int DP, bool KV8, int ROWS>
 __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasPerSm)
     attn_split_kernel(const SplitParams p, const __grid_constant__ CUtensorMap kmap,
@@ -238,7 +265,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
     }
     griddep_wait();
     griddep_launch_dependents();
-    const SplitPlan plan = split_plan<Cfg>(sh, &s_plan);
+    const SplitOrder order = split_order<KV8>(sh);
+    const SplitPlan plan = split_plan<Cfg>(sh, order, &s_plan);
     if (plan.seq >= sh.seqs) return;
 
     // ---- the item of this CTA's first piece or unit
@@ -247,17 +275,17 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
     int row_tiles = split_row_tiles<Cfg>(sh, sq);
     SplitItem it = split_item<Cfg>(sh, sq, 0);
     long long at = plan.in_seq;
-    while (at >= static_cast<long long>(item_measure(it, plan.piece)) * sh.kv_heads) {
-        at -= static_cast<long long>(item_measure(it, plan.piece)) * sh.kv_heads;
+    while (at >= static_cast<long long>(item_measure(it, plan.piece)) * order.heads) {
+        at -= static_cast<long long>(item_measure(it, plan.piece)) * order.heads;
         it = split_item<Cfg>(sh, sq, ++rt);
     }
-    int h, u0, u1;                 // cache head; the item's units in this run
+    int hl, u0, u1;                // cache head of the line; the item's units in this run
     long long first = 0;           // line: the item's first unit
     const long long end = plan.begin + plan.per;
     {
         const int n = item_measure(it, plan.piece);
-        h = at >> 31 == 0 ? static_cast<int>(at) / n : static_cast<int>(at / n);
-        const int in = static_cast<int>(at - static_cast<long long>(h) * n);
+        hl = at >> 31 == 0 ? static_cast<int>(at) / n : static_cast<int>(at / n);
+        const int in = static_cast<int>(at - static_cast<long long>(hl) * n);
         if (plan.piece > 0) {
             const int chunk = (it.units + n - 1) / n;   // the pieces of an item alike
             u0 = in * chunk;
@@ -275,6 +303,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
     while (true) {
         if (u1 > u0) {
         const int32_t* pages = sh.block_table + b * sh.table_stride;
+        const int h = order.head + hl;
 
         // ---- this warp's blocks: keys base + kUnit i, i in [i0, i1)
         const int base = (it.unit0 + u0) * Cfg::kUnit + warp * Cfg::kBlockKeys;
@@ -283,7 +312,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
         while (i1 > i0 && base + (i1 - 1) * Cfg::kUnit >= it.hi) --i1;
         if (gave_up) i1 = i0;
         int page_batch = -1, my_page = -1, my_slot = 0;
-        uint32_t my_scales = 127u << 8 | 127u;
+        uint32_t my_scales = 127u;   // nothing there: the values' power is the least
         auto issue = [&](int i) {   // whole warp; block i into its stage
             if (withhold && loads == 0 && i == i0) return;   // test hook
             // lanes look up the pages of the next 32 loads at a time
@@ -294,7 +323,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
                 const int key = base + mine * Cfg::kUnit + lane % Cfg::kSub * kSplitKeys;
                 my_page = -1;
                 my_slot = 0;
-                my_scales = 127u << 8 | 127u;
+                my_scales = 127u;
                 // (16 keys that no row sees, past them all or before the window: zeros from outside the cache)
                 if (mine < i1 && key < it.hi && key + kSplitKeys > it.lo) {
                     my_page = checked_page(sh, pages, key);
@@ -358,7 +387,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
         const int g = lane >> 2, t4 = lane & 3;
         const int rows = min(Cfg::kRows, sq.q_len * sh.group - rt * Cfg::kRows);   // of the tile that hold tokens
         float* const mo = merge + warp * Cfg::kRows * Cfg::kMergeRow;
-        if constexpr (ROWS == 16) {
+        if constexpr (!KV8) {
         // ---- queries: rows g and g + 8 of the tile in the MMA's A layout
         uint32_t qa[DP / 16][4];
         int last_key[2], first_key[2];   // what the row sees; rows of no token need no mask
@@ -379,20 +408,10 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
             for (int ks = 0; ks < DP / 16; ++ks)
 #pragma unroll
                 for (int f = 0; f < 4; ++f) {
-                    const int d = KV8 ? ks * 16 + t4 * 4 + (f >> 1) * 2 : ks * 16 + t4 * 2 + (f >> 1) * 8;
+                    const int d = ks * 16 + t4 * 2 + (f >> 1) * 8;
                     const T* src = qp[f & 1];
                     qa[ks][f] = src != nullptr && d < sh.head_dim ? *reinterpret_cast<const uint32_t*>(src + d) : 0u;
                 }
-            if (KV8) {   // elements 4t and 4t + 2, 4t + 1 and 4t + 3 of the 16
-#pragma unroll
-                for (int ks = 0; ks < DP / 16; ++ks)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t lo = qa[ks][e], hi = qa[ks][e + 2];
-                        qa[ks][e] = __byte_perm(lo, hi, 0x5410);
-                        qa[ks][e + 2] = __byte_perm(lo, hi, 0x7632);
-                    }
-            }
         }
 
         float o[DP / 8][4];
@@ -415,42 +434,17 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
 #pragma unroll
             for (int c = 0; c < kChains * kCols * 4; ++c) sc[c / (kCols * 4)][c / 4 % kCols][c % 4] = 0.0f;
             const int krow = (lane & 7) + ((lane >> 4) << 3);
-            float k_scale[Cfg::kSub], v_scale[Cfg::kSub];   // of the scores, of the weights or the codes
-            if constexpr (KV8) {
+#pragma unroll
+            for (int ks = 0; ks < DP / 16; ++ks)
 #pragma unroll
                 for (int sub = 0; sub < Cfg::kSub; ++sub) {
-                    const uint32_t scales = s_scales[warp][st][sub];
-                    k_scale[sub] = sh.scale_log2 * e8m0_power(scales & 255u);
-                    v_scale[sub] = e8m0_power(scales >> 8);
+                    uint32_t kf[4];
+                    const int chunk = (ks & 3) * 2 + ((lane >> 3) & 1);
+                    ldmatrix_x4(kf, kb + (ks >> 2) * (Cfg::kBlockKeys * 128) + sub * 2048 + krow * 128 +
+                                        ((chunk ^ (krow & 7)) << 4));
+                    mma_16816<T>(sc[ks % kChains][2 * sub], qa[ks], kf[0], kf[1]);
+                    mma_16816<T>(sc[ks % kChains][2 * sub + 1], qa[ks], kf[2], kf[3]);
                 }
-                const uint32_t one = std::is_same<T, __half>::value ? 0x3c003c00u : kBf16Widen;
-#pragma unroll
-                for (int ks = 0; ks < DP / 16; ks += 2)
-#pragma unroll
-                    for (int sub = 0; sub < Cfg::kSub; ++sub) {
-                        uint32_t kf[4], b0, b1;   // keys 0-7 and 8-15 of two steps of 16 elements
-                        ldmatrix_x4(kf, piece8<DP>(kb + sub * kSplitKeys * DP, krow, ks + ((lane >> 3) & 1)));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            widen_e4m3<T>(kf[i], one, b0, b1);
-                            mma_16816<T>(sc[0][2 * sub + (i >> 1)], qa[ks + (i & 1)], b0, b1);
-                        }
-                    }
-            } else {
-#pragma unroll
-                for (int sub = 0; sub < Cfg::kSub; ++sub) k_scale[sub] = sh.scale_log2, v_scale[sub] = 1.0f;
-#pragma unroll
-                for (int ks = 0; ks < DP / 16; ++ks)
-#pragma unroll
-                    for (int sub = 0; sub < Cfg::kSub; ++sub) {
-                        uint32_t kf[4];
-                        const int chunk = (ks & 3) * 2 + ((lane >> 3) & 1);
-                        ldmatrix_x4(kf, kb + (ks >> 2) * (Cfg::kBlockKeys * 128) + sub * 2048 + krow * 128 +
-                                            ((chunk ^ (krow & 7)) << 4));
-                        mma_16816<T>(sc[ks % kChains][2 * sub], qa[ks], kf[0], kf[1]);
-                        mma_16816<T>(sc[ks % kChains][2 * sub + 1], qa[ks], kf[2], kf[3]);
-                    }
-            }
             // ---- scale, mask, running maximum (base-2 exponents); x[e]: row g + 8 e, keys k0 + 8 c and the next
             float x[2][2 * kCols];
             const int k0 = key0 + t4 * 2;
@@ -464,7 +458,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
                     for (int f = 0; f < 2; ++f) {
                         float v = sc[0][c][2 * e + f];
                         if (kChains == 2) v += sc[kChains - 1][c][2 * e + f];
-                        x[e][2 * c + f] = v * k_scale[c >> 1];
+                        x[e][2 * c + f] = v * sh.scale_log2;
                     }
                 if (masked) {
 #pragma unroll
@@ -503,55 +497,32 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
 #pragma unroll
             for (int sub = 0; sub < Cfg::kSub; ++sub) {
                 uint32_t pa[4], pb[4];   // the two parts of the weights
-                constexpr bool kScaledWeights = KV8 && std::is_same<T, __nv_bfloat16>::value;
 #pragma unroll
                 for (int f = 0; f < 4; ++f) {
-                    float lo = x[f & 1][4 * sub + (f >> 1) * 2], hi = x[f & 1][4 * sub + (f >> 1) * 2 + 1];
-                    if (kScaledWeights) lo *= v_scale[sub], hi *= v_scale[sub];
+                    const float lo = x[f & 1][4 * sub + (f >> 1) * 2], hi = x[f & 1][4 * sub + (f >> 1) * 2 + 1];
                     pa[f] = pack2<T>(lo, hi);
                     pb[f] = pack2<T>(lo - low_of<T>(pa[f]), hi - high_of<T>(pa[f]));
                 }
-                auto hide = [&](uint32_t(&vf)[4]) {   // value rows that no token sees
 #pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                        const int key = k0 + sub * kSplitKeys + (f & 1) * 8;
-                        if (key >= it.hi || key < it.lo) vf[f] &= 0xffff0000u;
-                        if (key + 1 >= it.hi || key + 1 < it.lo) vf[f] &= 0x0000ffffu;
-                    }
-                };
-                if constexpr (KV8) {
-                    const uint32_t factor = kScaledWeights ? kBf16Widen : pack2<T>(v_scale[sub], v_scale[sub]);
+                for (int n = 0; n < DP / 8; n += 2) {
+                    uint32_t vf[4];
+                    const int chunk = (n & 7) + (lane >> 4);
+                    ldmatrix_x4_trans(vf, vb + (n >> 3) * (Cfg::kBlockKeys * 128) + sub * 2048 + vrow * 128 +
+                                              ((chunk ^ (vrow & 7)) << 4));
+                    if (ragged) {
 #pragma unroll
-                    for (int n = 0; n < DP / 8; n += 4) {
-                        uint32_t vf[4];   // keys 0-7 and 8-15 of two times 16 elements
-                        ldmatrix_x4_trans(vf, piece8<DP>(vb + sub * kSplitKeys * DP, vrow, (n >> 1) + (lane >> 4)));
-                        if (ragged) hide(vf);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            uint32_t even0, odd0, even1, odd1;
-                            widen_e4m3<T>(vf[2 * i], factor, even0, odd0);
-                            widen_e4m3<T>(vf[2 * i + 1], factor, even1, odd1);
-                            mma_16816<T>(o[n + 2 * i], pa, even0, even1);
-                            mma_16816<T>(o[n + 2 * i + 1], pa, odd0, odd1);
-                            mma_16816<T>(o[n + 2 * i], pb, even0, even1);
-                            mma_16816<T>(o[n + 2 * i + 1], pb, odd0, odd1);
+                        for (int f = 0; f < 4; ++f) {
+                            const int key = k0 + sub * kSplitKeys + (f & 1) * 8;
+                            if (key >= it.hi || key < it.lo) vf[f] &= 0xffff0000u;
+                            if (key + 1 >= it.hi || key + 1 < it.lo) vf[f] &= 0x0000ffffu;
                         }
                     }
-                } else {
+                    mma_16816<T>(o[n], pa, vf[0], vf[1]);
+                    mma_16816<T>(o[n + 1], pa, vf[2], vf[3]);
 #pragma unroll
-                    for (int n = 0; n < DP / 8; n += 2) {
-                        uint32_t vf[4];
-                        const int chunk = (n & 7) + (lane >> 4);
-                        ldmatrix_x4_trans(vf, vb + (n >> 3) * (Cfg::kBlockKeys * 128) + sub * 2048 + vrow * 128 +
-                                                  ((chunk ^ (vrow & 7)) << 4));
-                        if (ragged) hide(vf);
-                        mma_16816<T>(o[n], pa, vf[0], vf[1]);
-                        mma_16816<T>(o[n + 1], pa, vf[2], vf[3]);
-#pragma unroll
-                        for (int f = 0; f < 4; ++f) vf[f] = finite_pair<T>(vf[f]);   // (a second part of 0 x infinity)
-                        mma_16816<T>(o[n], pb, vf[0], vf[1]);
-                        mma_16816<T>(o[n + 1], pb, vf[2], vf[3]);
-                    }
+                    for (int f = 0; f < 4; ++f) vf[f] = finite_pair<T>(vf[f]);   // (a second part of 0 x infinity)
+                    mma_16816<T>(o[n], pb, vf[0], vf[1]);
+                    mma_16816<T>(o[n + 1], pb, vf[2], vf[3]);
                 }
             }
             __syncwarp();
@@ -564,163 +535,223 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
             l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
         }
 
-        // ---- join the warps: a thread takes the float4 tid, tid + 128, .. of the rows
         __syncthreads();
         {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 if (8 * e >= rows) break;
-                if constexpr (KV8) {   // elements 4t to 4t + 3 of each 16
 #pragma unroll
-                    for (int n = 0; n < DP / 8; n += 2)
-                        *reinterpret_cast<float4*>(mo + (g + 8 * e) * Cfg::kMergeRow + n * 8 + t4 * 4) =
-                            make_float4(o[n][2 * e], o[n + 1][2 * e], o[n][2 * e + 1], o[n + 1][2 * e + 1]);
-                } else {
-#pragma unroll
-                    for (int n = 0; n < DP / 8; ++n)
-                        *reinterpret_cast<float2*>(mo + (g + 8 * e) * Cfg::kMergeRow + n * 8 + t4 * 2) =
-                            make_float2(o[n][2 * e], o[n][2 * e + 1]);
-                }
+                for (int n = 0; n < DP / 8; ++n)
+                    *reinterpret_cast<float2*>(mo + (g + 8 * e) * Cfg::kMergeRow + n * 8 + t4 * 2) =
+                        make_float2(o[n][2 * e], o[n][2 * e + 1]);
                 if (t4 == 0) s_ml[warp][g + 8 * e] = make_float2(m[e], l[e]);
             }
         }
         } else {
-        // ---- eight rows: S^T = K Q^T and O^T += V^T P^T, so that keys and head elements are the products' 16 rows and
-        // the query rows their 8 columns: half the products and half the registers of the other form.  Query row r of
-        // the tile is a lane's column: queries in the MMA's B layout are row g's, scores and sums rows 2t and 2t + 1's.
-        uint32_t qb[DP / 16][2];
-        int last_key[2], first_key[2];
-        {
-            const int row = rt * 8 + g, tok = row / sh.group;
+        // ---- S^T = K Q^T and O^T += V^T P^T: keys and head elements are the products' 16 rows, query rows their columns,
+        // eight to a tile (a single token's rows under 8 heads: half the products and registers of rows as rows).  Lane (g, t) holds keys g and g + 8 and elements 2g and 2g + 1 of each 16 under the
+        // query rows 2t and 2t + 1.
+        constexpr int kTiles = ROWS / 8;
+        constexpr bool kHalf = std::is_same<T, __half>::value;
+        constexpr int kParts = kHalf ? 2 : 1;       // of the weights
+        uint32_t qb[kTiles][DP / 16][2];            // rows g of the tiles in the MMA's B layout, pairs of fp16
+        float q_scale[kTiles][2];                   // of rows 2t and 2t + 1: what their scores are to be multiplied by
+        int last_key[kTiles][2], first_key[kTiles][2];
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+            const int row = rt * ROWS + n * 8 + g, tok = row / sh.group;
             const T* qp = static_cast<const T*>(p.q) + static_cast<long long>(sq.first_token + tok) * p.q_token +
                           static_cast<long long>(h * sh.group + row - tok * sh.group) * p.q_head;
-            const bool ok = g < rows;
+            uint2 raw[DP / 16];
+            uint32_t top = 0;
 #pragma unroll
-            for (int ks = 0; ks < DP / 16; ++ks) {
-                const int d = ks * 16 + t4 * 4;
-                const uint32_t lo = ok && d < sh.head_dim ? *reinterpret_cast<const uint32_t*>(qp + d) : 0u;
-                const uint32_t hi = ok && d < sh.head_dim ? *reinterpret_cast<const uint32_t*>(qp + d + 2) : 0u;
-                qb[ks][0] = __byte_perm(lo, hi, 0x5410);   // elements 4t and 4t + 2, 4t + 1 and 4t + 3 of the 16
-                qb[ks][1] = __byte_perm(lo, hi, 0x7632);
+            for (int c = 0; c < DP / 16; ++c) {
+                const int d = c * 16 + t4 * 4;
+                raw[c] = n * 8 + g < rows && d < sh.head_dim ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0, 0);
+                top = max(top, max(max(magnitude(low_of<T>(raw[c].x)), magnitude(high_of<T>(raw[c].x))),
+                                   max(magnitude(low_of<T>(raw[c].y)), magnitude(high_of<T>(raw[c].y)))));
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // times 2^a the largest is 2^14 to 2^15 (a up to 126, for rows of next to nothing); the scores' factor back is
+            // NaN for a row that is not finite
+            const int a = kHalf ? 0 : max(min(141 - static_cast<int>(top >> 23), 126), -113);
+            const float up = __uint_as_float(static_cast<uint32_t>(a + 127) << 23);
+            const float back = !kHalf && top >= 0x7f800000u
+                                   ? __uint_as_float(0x7fc00000u)
+                                   : sh.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
+#pragma unroll
+            for (int c = 0; c < DP / 16; ++c) {   // elements 4t to 4t + 3 of the 16
+                qb[n][c][0] = raw[c].x;
+                qb[n][c][1] = raw[c].y;
+                if (!kHalf) {
+                    qb[n][c][0] = pack2<__half>(low_of<T>(raw[c].x) * up, high_of<T>(raw[c].x) * up);
+                    qb[n][c][1] = pack2<__half>(low_of<T>(raw[c].y) * up, high_of<T>(raw[c].y) * up);
+                }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = t4 * 2 + e, t = (rt * 8 + r) / sh.group;
-                last_key[e] = r < rows ? min(sq.first_pos + t, sq.keys - 1) : 0x7fffffff;
-                first_key[e] = r < rows ? window_start(sq.first_pos + t, sh.window) : 0;
+                q_scale[n][e] = __shfl_sync(0xffffffffu, back, (t4 * 2 + e) * 4);
+                const int r = n * 8 + t4 * 2 + e, t = (rt * ROWS + r) / sh.group;
+                last_key[n][e] = r < rows ? min(sq.first_pos + t, sq.keys - 1) : 0x7fffffff;
+                first_key[n][e] = r < rows ? window_start(sq.first_pos + t, sh.window) : 0;
             }
         }
-        float o[DP / 16][4];   // elements 2g and 2g + 1 of each 16, rows 2t and 2t + 1
+        float o[kTiles][DP / 16][4], m[kTiles][2], l[kTiles][2];
 #pragma unroll
-        for (int n = 0; n < DP / 16; ++n)
+        for (int n = 0; n < kTiles; ++n) {
 #pragma unroll
-            for (int f = 0; f < 4; ++f) o[n][f] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+            for (int c = 0; c < DP / 4; ++c) o[n][c / 4][c % 4] = 0.0f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.0f;
+        }
         for (int i = i0; i < i1; ++i) {
             if (!block_ready(i)) break;
             const uint32_t st = (loads + static_cast<uint32_t>(i - i0)) % Cfg::kStages;
             const uint32_t kb = smem_u32(ring + st * 2 * Cfg::kBlockBytes);
             const uint32_t vb = kb + Cfg::kBlockBytes;
             const int key0 = base + i * Cfg::kUnit;
-            float sc[Cfg::kSub][4];   // keys g and g + 8 of each 16, rows 2t and 2t + 1
+            float sc[kTiles][2][4];   // of two times 16 keys
 #pragma unroll
-            for (int c = 0; c < Cfg::kSub * 4; ++c) sc[c / 4][c % 4] = 0.0f;
-            float v_scale[Cfg::kSub];
+            for (int c = 0; c < kTiles * 8; ++c) sc[c / 8][c / 4 % 2][c % 4] = 0.0f;
             const int krow = (lane & 7) + ((lane >> 4) << 3);
-            const uint32_t one = std::is_same<T, __half>::value ? 0x3c003c00u : kBf16Widen;
 #pragma unroll
             for (int ks = 0; ks < DP / 16; ks += 2)
 #pragma unroll
-                for (int sub = 0; sub < Cfg::kSub; ++sub) {
-                    uint32_t kf[4];   // keys 0-7 and 8-15 of two steps of 16 elements
+                for (int sub = 0; sub < 2; ++sub) {
+                    uint32_t kf[4];   // keys 0-7 of two times 16 elements, keys 8-15
                     ldmatrix_x4(kf, piece8<DP>(kb + sub * kSplitKeys * DP, krow, ks + ((lane >> 3) & 1)));
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) {
+                    for (int k = 0; k < 2; ++k) {
                         uint32_t a[4];
-                        widen_e4m3<T>(kf[f], one, a[0], a[2]);
-                        widen_e4m3<T>(kf[f + 2], one, a[1], a[3]);
-                        mma_16816<T>(sc[sub], a, qb[ks + f][0], qb[ks + f][1]);
+                        widen_e4m3(kf[k], a[0], a[2]);
+                        widen_e4m3(kf[k + 2], a[1], a[3]);
+#pragma unroll
+                        for (int n = 0; n < kTiles; ++n)
+                            mma_16816<__half>(sc[n][sub], a, qb[n][ks + k][0], qb[n][ks + k][1]);
                     }
                 }
-            const bool masked = __any_sync(0xffffffffu, min(last_key[0], last_key[1]) < key0 + Cfg::kBlockKeys - 1 ||
-                                                            max(first_key[0], first_key[1]) > key0);
+            // ---- scores (base-2 exponents), masks, maxima; weights in parts, turned to the B layout
+            int first_all = first_key[0][0], last_all = last_key[0][0];
 #pragma unroll
-            for (int sub = 0; sub < Cfg::kSub; ++sub) {
-                const uint32_t scales = s_scales[warp][st][sub];
-                const float k_scale = sh.scale_log2 * e8m0_power(scales & 255u);
-                v_scale[sub] = e8m0_power(scales >> 8);
-#pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    sc[sub][f] *= k_scale;
-                    const int key = key0 + sub * kSplitKeys + g + (f >> 1) * 8;
-                    if (masked && (key > last_key[f & 1] || key < first_key[f & 1])) sc[sub][f] = -INFINITY;
-                }
+            for (int c = 1; c < 2 * kTiles; ++c) {
+                first_all = max(first_all, first_key[c / 2][c % 2]);
+                last_all = min(last_all, last_key[c / 2][c % 2]);
             }
+            const bool masked = __any_sync(0xffffffffu, last_all < key0 + Cfg::kBlockKeys - 1 || first_all > key0);
+            const uint32_t scales[2] = {s_scales[warp][st][0], s_scales[warp][st][1]};
+            float v_exp[2];   // the values' exponents
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float top = fmaxf(sc[0][e], sc[0][e + 2]);
-#pragma unroll
-                for (int sub = 1; sub < Cfg::kSub; ++sub) top = fmaxf(top, fmaxf(sc[sub][e], sc[sub][e + 2]));
-#pragma unroll
-                for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                const float mn = fmaxf(m[e], top);
-                const float base_m = mn == -INFINITY ? 0.0f : mn;
-                const float scale = ex2(m[e] - base_m);
-                m[e] = mn;
-                float sum = 0.0f;
-#pragma unroll
-                for (int sub = 0; sub < Cfg::kSub; ++sub)
-#pragma unroll
-                    for (int f = e; f < 4; f += 2) {
-                        sc[sub][f] = ex2(sc[sub][f] - base_m);
-                        sum += sc[sub][f];
-                    }
-                l[e] = l[e] * scale + sum;
-                if (__any_sync(0xffffffffu, scale != 1.0f)) {
-#pragma unroll
-                    for (int n = 0; n < DP / 16; ++n) {
-                        o[n][e] *= scale;
-                        o[n][e + 2] *= scale;
-                    }
-                }
+            for (int sub = 0; sub < 2; ++sub) {
+                const int byte = static_cast<int>(scales[sub] >> 8);
+                v_exp[sub] = byte == 255 ? __uint_as_float(0x7fc00000u) : static_cast<float>(byte - 127);
             }
-            // ---- the weights turned to the B layout, in two parts
-            const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3);
-            const bool ragged = key0 + Cfg::kBlockKeys > it.hi || key0 < it.lo;
-            constexpr bool kScaledWeights = std::is_same<T, __nv_bfloat16>::value;
+            uint32_t pw[kTiles][2][kParts][2];   // [16 keys][part][keys 0-7, 8-15]
+            float share[kTiles][2];   // what a row's sums over this block are to be multiplied by
 #pragma unroll
-            for (int sub = 0; sub < Cfg::kSub; ++sub) {
-                uint32_t pa[2], pb[2];
+            for (int n = 0; n < kTiles; ++n) {
+                float x[2][4];
 #pragma unroll
-                for (int f = 0; f < 2; ++f) {   // keys 0-7, 8-15
-                    float lo = sc[sub][2 * f], hi = sc[sub][2 * f + 1];
-                    if (kScaledWeights) lo *= v_scale[sub], hi *= v_scale[sub];
-                    pa[f] = pack2<T>(lo, hi);
-                    pb[f] = transpose_8x8(pack2<T>(lo - low_of<T>(pa[f]), hi - high_of<T>(pa[f])));
-                    pa[f] = transpose_8x8(pa[f]);
+                for (int sub = 0; sub < 2; ++sub) {
+                    const float k_scale = e8m0_power(scales[sub] & 255u);
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        x[sub][f] = sc[n][sub][f] * (q_scale[n][f & 1] * k_scale);
+                        const int key = key0 + sub * kSplitKeys + g + (f >> 1) * 8;
+                        if (masked && (key > last_key[n][f & 1] || key < first_key[n][f & 1])) x[sub][f] = -INFINITY;
+                    }
                 }
-                const uint32_t factor = kScaledWeights ? kBf16Widen : pack2<T>(v_scale[sub], v_scale[sub]);
 #pragma unroll
-                for (int n = 0; n < DP / 16; n += 2) {
-                    uint32_t vf[4];   // keys 0-7 and 8-15 of two times 16 elements
-                    ldmatrix_x4_trans(vf, piece8<DP>(vb + sub * kSplitKeys * DP, vrow, n + (lane >> 4)));
-                    if (ragged) {   // value rows that no token sees
-                        const int key = key0 + sub * kSplitKeys + t4 * 2;
+                for (int e = 0; e < 2; ++e) {
+                    float top[2] = {fmaxf(x[0][e], x[0][e + 2]), fmaxf(x[1][e], x[1][e + 2])};
 #pragma unroll
-                        for (int f = 0; f < 4; ++f) {
-                            const int k = key + (f & 1) * 8;
-                            if (k >= it.hi || k < it.lo) vf[f] &= 0xffff0000u;
-                            if (k + 1 >= it.hi || k + 1 < it.lo) vf[f] &= 0x0000ffffu;
+                    for (int d = 4; d < 32; d *= 2)
+#pragma unroll
+                        for (int sub = 0; sub < 2; ++sub)
+                            top[sub] = fmaxf(top[sub], __shfl_xor_sync(0xffffffffu, top[sub], d));
+                    const float mn = max3(m[n][e], top[0], top[1]);
+                    const float base_m = mn == -INFINITY ? 0.0f : mn;
+                    const float scale = ex2(m[n][e] - base_m);
+                    m[n][e] = mn;
+                    // The largest weight times its value's power: the block's weights, powers included, are taken as
+                    // multiples of it, so that they use fp16's range whatever the blocks' powers are.  (A sum, not
+                    // fmaxf: NaN stays.)
+                    const float r0 = top[0] + v_exp[0], r1 = top[1] + v_exp[1];
+                    const float ref = r0 >= r1 || r0 != r0 ? r0 : r1;
+                    const float base_r = ref == -INFINITY ? 0.0f : ref;
+                    share[n][e] = ex2(ref - base_m);
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                        for (int f = e; f < 4; f += 2) {
+                            sum += ex2(x[sub][f] - base_m);
+                            x[sub][f] = ex2(x[sub][f] + (v_exp[sub] - base_r + kWeightLog2));
+                        }
+                    l[n][e] = l[n][e] * scale + sum;
+                    if (__any_sync(0xffffffffu, scale != 1.0f)) {
+#pragma unroll
+                        for (int c = 0; c < DP / 16; ++c) {
+                            o[n][c][e] *= scale;
+                            o[n][c][e + 2] *= scale;
                         }
                     }
+                }
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
                     for (int f = 0; f < 2; ++f) {
-                        uint32_t a[4];
-                        widen_e4m3<T>(vf[2 * f], factor, a[0], a[1]);
-                        widen_e4m3<T>(vf[2 * f + 1], factor, a[2], a[3]);
-                        mma_16816<T>(o[n + f], a, pa[0], pa[1]);
-                        mma_16816<T>(o[n + f], a, pb[0], pb[1]);
+                        const float lo = x[sub][2 * f], hi = x[sub][2 * f + 1];
+                        const uint32_t w = pack2<__half>(lo, hi);
+                        pw[n][sub][0][f] = transpose_8x8(w);
+                        if (kParts == 2)
+                            pw[n][sub][kParts - 1][f] =
+                                transpose_8x8(pack2<__half>(lo - low_of<__half>(w), hi - high_of<__half>(w)));
                     }
+            }
+            // ---- O^T += V^T P^T; value rows that no token sees are not multiplied (0 x NaN)
+            const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3);
+            const bool ragged = key0 + Cfg::kBlockKeys > it.hi || key0 < it.lo;
+#pragma unroll
+            for (int c = 0; c < DP / 16; c += 2) {
+                uint32_t a[2][2][4];   // [16 keys][16 elements]
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub) {
+                    uint32_t vf[4];    // keys 0-7 and 8-15 of two times 16 elements
+                    ldmatrix_x4_trans(vf, piece8<DP>(vb + sub * kSplitKeys * DP, vrow, c + (lane >> 4)));
+                    if (ragged) {
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) {
+                            const int key = key0 + sub * kSplitKeys + t4 * 2 + (f & 1) * 8;
+                            if (key >= it.hi || key < it.lo) vf[f] &= 0xffff0000u;
+                            if (key + 1 >= it.hi || key + 1 < it.lo) vf[f] &= 0x0000ffffu;
+                        }
+                    }
+                    // keys 2t and 2t + 1 of element 2g, of element 2g + 1
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        widen_e4m3(__byte_perm(vf[2 * k], 0, 0x3120), a[sub][k][0], a[sub][k][1]);
+                        widen_e4m3(__byte_perm(vf[2 * k + 1], 0, 0x3120), a[sub][k][2], a[sub][k][3]);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < kTiles; ++n) {
+                    float y[2][4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) mma_16816_first(y[k], a[0][k], pw[n][0][0][0], pw[n][0][0][1]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) mma_16816<__half>(y[k], a[1][k], pw[n][1][0][0], pw[n][1][0][1]);
+                    if (kParts == 2) {
+#pragma unroll
+                        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+                                mma_16816<__half>(y[k], a[sub][k], pw[n][sub][kParts - 1][0], pw[n][sub][kParts - 1][1]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int f = 0; f < 4; ++f) o[n][c + k][f] = fmaf(y[k][f], share[n][f & 1], o[n][c + k][f]);
                 }
             }
             __syncwarp();
@@ -728,20 +759,27 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
         }
         loads += static_cast<uint32_t>(n_blocks);
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-            for (int x = 4; x < 32; x *= 2) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+        constexpr float kUnweight = 1.0f / 1024.0f;   // 2^-kWeightLog2
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-            for (int n = 0; n < DP / 16; ++n)
-                *reinterpret_cast<float2*>(mo + (t4 * 2 + e) * Cfg::kMergeRow + n * 16 + g * 2) =
-                    make_float2(o[n][e], o[n][e + 2]);
-            if (g == 0) s_ml[warp][t4 * 2 + e] = make_float2(m[e], l[e]);
-        }
+            for (int e = 0; e < 2; ++e) {
+                const int row = n * 8 + t4 * 2 + e;
+#pragma unroll
+                for (int c = 0; c < DP / 16; ++c)
+                    *reinterpret_cast<float2*>(mo + row * Cfg::kMergeRow + c * 16 + g * 2) =
+                        make_float2(o[n][c][e] * kUnweight, o[n][c][e + 2] * kUnweight);
+                if (g == 0) s_ml[warp][row] = make_float2(m[n][e], l[n][e]);
+            }
         }
         __syncthreads();
+        // ---- join the warps: a thread takes the float4 tid, tid + 128, .. of the rows
         float4 acc[Cfg::kParts];
         float2 ml[Cfg::kParts];
         auto part_row = [&](int k) { return (tid + k * kSplitThreads) / (DP / 4); };
@@ -795,12 +833,12 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
             for (int k = 0; k < Cfg::kParts; ++k)
                 if (part_row(k) < rows) store(part_row(k), acc[k], ml[k]);
         } else {
-            // The item's pieces lie with CTAs c0 .. c0 + n - 1.  On the line, the first is its CTA's last piece (slot
+            // The item's pieces lie with the CTAs of runs c0 .. c0 + n - 1.  On the line, the first is its CTA's last piece (slot
             // 1), the others their CTAs' first (slot 0).
             int c0, n;
             if (plan.piece > 0) {
                 n = pieces_of(it.units, plan.piece);
-                c0 = static_cast<int>(blockIdx.x) - u0 / ((it.units + n - 1) / n);
+                c0 = order.run - u0 / ((it.units + n - 1) / n);
             } else {
                 c0 = static_cast<int>(first / plan.per);
                 n = static_cast<int>((first + it.units - 1) / plan.per) - c0 + 1;
@@ -816,16 +854,16 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
             __syncthreads();
             if (tid == 0) {
                 __threadfence();
-                const unsigned seen = atomicAdd(&p.counters[c0], 1u);
+                const unsigned seen = atomicAdd(&p.counters[c0 * order.step + order.first], 1u);
                 s_last = seen == static_cast<unsigned>(n - 1);
-                if (s_last) p.counters[c0] = 0;
+                if (s_last) p.counters[c0 * order.step + order.first] = 0;
                 __threadfence();
             }
             __syncthreads();
             if (s_last) {
                 // maxima and sums of all pieces into shared memory, then their outputs, several loads under way
                 float2* all = reinterpret_cast<float2*>(ring_base);   // [pieces][16]; the merge is over
-                auto slot_of = [&](int c) { return 2 * (c0 + c) + (c == 0 ? 1 : 0); };
+                auto slot_of = [&](int c) { return 2 * ((c0 + c) * order.step + order.first) + (c == 0 ? 1 : 0); };
                 for (int i = tid; i < n * Cfg::kRows; i += kSplitThreads)
                     all[i] = __ldcg(&p.part_ml[slot_of(i / Cfg::kRows) * Cfg::kRows + i % Cfg::kRows]);
                 __syncthreads();
@@ -874,8 +912,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
         if (plan.piece > 0) break;
         first += it.units + kSplitItemUnits;
         if (first >= end) break;
-        if (++h == sh.kv_heads) {
-            h = 0;
+        if (++hl == order.heads) {
+            hl = 0;
             if (++rt == row_tiles) {
                 rt = 0;
                 do {

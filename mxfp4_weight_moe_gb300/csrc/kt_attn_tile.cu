@@ -367,11 +367,6 @@ __device__ __forceinline__ void mask32(float (&x)[32], int lo, int hi) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) x[i] = (seen >> i) & 1u ? x[i] : -INFINITY;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
 __device__ __forceinline__ float max32(const float (&x)[32]) {
     float a = max3(x[0], x[1], x[2]), b = max3(x[3], x[4], x[5]);
 #pragma unroll
@@ -409,7 +404,9 @@ __device__ __forceinline__ int ragged_tile(const TileWalk& w, int box_slots) {
 }
 
 // 16 e4m3 codes in order as 16 elements of T, each times the pair's factor (`more`: times that as well, for powers that
-// bf16's 2^120 leaves no room for).
+// bf16's 2^120 leaves no room for).  For bf16, which has no conversion from e4m3, the code's bits are put where bf16 has
+// them (an e4m3 exponent of 7 means 0, a bf16 exponent of 127 does, and subnormal codes become subnormal numbers): what
+// stands there is 2^-120 of the value, so that the factor holds 2^120 besides.  NaN codes do not come out as NaN.
 template <typename T>
 __device__ __forceinline__ void widen16(const uint4& v, uint32_t factor, uint32_t more, uint4& a, uint4& b);
 template <>
@@ -418,7 +415,7 @@ __device__ __forceinline__ void widen16<__nv_bfloat16>(const uint4& v, uint32_t 
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t r[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {   // as widen_e4m3, the high bytes of four numbers and the low ones at a time
+    for (int i = 0; i < 4; ++i) {   // the high bytes of four numbers and the low ones at a time
         const uint32_t high = ((w[i] & 0x70707070u) >> 4) | (w[i] & 0x80808080u);
         const uint32_t low = (w[i] * 16u) & 0xf0f0f0f0u;
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r[2 * i]) : "r"(__byte_perm(low, high, 0x5140)), "r"(factor));
