@@ -46,13 +46,15 @@ constexpr int kSplitJoinUnits = 4;                      // what cutting an item 
 template <int DP, bool KV8, int ROWS>
 struct SplitCfg {
     static constexpr int kRows = ROWS;                               // query rows of an item: 16, or 8 (KV8)
-    static constexpr int kSub = DP == 128 && !KV8 ? 1 : 2;           // loads of K and of V that make a warp's block
+    static constexpr int kSub = (DP == 128 ? 1 : 2) * (KV8 ? 2 : 1);   // loads of K and of V that make a warp's block
     static constexpr int kBlockKeys = kSub * kSplitKeys;
     static constexpr int kUnit = kSplitWarps * kBlockKeys;           // keys of one unit
     static constexpr int kRowBytes = DP * (KV8 ? 1 : 2);             // of a key in a block
     static constexpr int kBlockBytes = kBlockKeys * kRowBytes;       // one of K, V
-    static constexpr int kCtasPerSm = ROWS == 8 ? 3 : 2;
-    static constexpr int kStages = !KV8 ? 3 : (DP == 64 ? 2 : 1) * (ROWS == 8 ? 2 : 3);   // 24 KB a warp, 16 for 8 rows
+    // KV8 heads of 64 wait for the arithmetic (4 x 131k keys: 67 us with three CTAs an SM, 71 with two), of 128 for the
+    // loads (64 single tokens: 222 us with two CTAs, 234 with three, whose rings are smaller)
+    static constexpr int kCtasPerSm = ROWS == 8 && DP == 64 ? 3 : 2;
+    static constexpr int kStages = kCtasPerSm == 3 ? 2 : 3;          // 24 KB a warp, or 16
     static constexpr int kRing = kStages * 2 * kBlockBytes;          // per warp
     static constexpr int kMaxCtas = kSplitWarps * kRing / (kRows * 8);   // what a join of all of them has room for
     static constexpr int kSmem = kSplitWarps * kRing + 1024;
@@ -96,7 +98,7 @@ __device__ __forceinline__ int split_row_tiles(const AttnShape& s, const SeqInfo
 // The order of the CTAs.  A slot's heads lie side by side in memory, and a head's row of an 8-bit cache is 128 bytes at
 // most: read at different times, such rows come at 5.5 TB/s (64 single tokens after up to 16383, 8 heads of 128: 264 us),
 // where each head's slots follow one another at 6.7.  So there the runs are those of one head, and neighbouring CTAs
-// take the same run of neighbouring heads (XXX us), unless there are so many heads that CTAs would be left over.
+// take the same run of neighbouring heads (234), unless there are so many heads that CTAs would be left over.
 struct SplitOrder {
     int runs;         // CTAs that share a line
     int heads;        // cache heads on a line
@@ -227,7 +229,7 @@ __device__ __forceinline__ uint32_t piece8(uint32_t base, int row, int piece) {
 // which e4m3 has a conversion to (bf16 has none: bits moved by hand take 2.2 instructions an element, and 265 us for 64
 // single tokens after up to 16383): codes go in without their powers, exact; bf16 queries times a power of two per row,
 // exact down to 2^-31 of the row's largest element and off by at most 2^-40 of that below; softmax weights, their
-// value's power included, relative to the largest of the row in the block's 32 keys, times 2^10: rounded to 11 bits
+// value's power included, relative to the largest of the row in the block's 32 or 64 keys, times 2^10: rounded to 11 bits
 // down to 2^-24 of that largest and off by at most 2^-35 of it below.  For fp16 results, which have as many bits, the
 // weights go in in two parts.
 constexpr float kWeightLog2 = 10.0f;   // the largest weight of a block, log2; O stays multiplied by that to the end
@@ -551,7 +553,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
         // ---- S^T = K Q^T and O^T += V^T P^T: keys and head elements are the products' 16 rows, query rows their columns,
         // eight to a tile (a single token's rows under 8 heads: half the products and registers of rows as rows).  Lane (g, t) holds keys g and g + 8 and elements 2g and 2g + 1 of each 16 under the
         // query rows 2t and 2t + 1.
-        constexpr int kTiles = ROWS / 8;
+        constexpr int kTiles = ROWS / 8, kSub = Cfg::kSub;
         constexpr bool kHalf = std::is_same<T, __half>::value;
         constexpr int kParts = kHalf ? 2 : 1;       // of the weights
         uint32_t qb[kTiles][DP / 16][2];            // rows g of the tiles in the MMA's B layout, pairs of fp16
@@ -611,14 +613,14 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
             const uint32_t kb = smem_u32(ring + st * 2 * Cfg::kBlockBytes);
             const uint32_t vb = kb + Cfg::kBlockBytes;
             const int key0 = base + i * Cfg::kUnit;
-            float sc[kTiles][2][4];   // of two times 16 keys
+            float sc[kTiles][kSub][4];   // of each 16 keys
 #pragma unroll
-            for (int c = 0; c < kTiles * 8; ++c) sc[c / 8][c / 4 % 2][c % 4] = 0.0f;
+            for (int c = 0; c < kTiles * kSub * 4; ++c) sc[c / (4 * kSub)][c / 4 % kSub][c % 4] = 0.0f;
             const int krow = (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
             for (int ks = 0; ks < DP / 16; ks += 2)
 #pragma unroll
-                for (int sub = 0; sub < 2; ++sub) {
+                for (int sub = 0; sub < kSub; ++sub) {
                     uint32_t kf[4];   // keys 0-7 of two times 16 elements, keys 8-15
                     ldmatrix_x4(kf, piece8<DP>(kb + sub * kSplitKeys * DP, krow, ks + ((lane >> 3) & 1)));
 #pragma unroll
@@ -639,20 +641,21 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
                 last_all = min(last_all, last_key[c / 2][c % 2]);
             }
             const bool masked = __any_sync(0xffffffffu, last_all < key0 + Cfg::kBlockKeys - 1 || first_all > key0);
-            const uint32_t scales[2] = {s_scales[warp][st][0], s_scales[warp][st][1]};
-            float v_exp[2];   // the values' exponents
+            uint32_t scales[kSub];
+            float v_exp[kSub];   // the values' exponents
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
+            for (int sub = 0; sub < kSub; ++sub) {
+                scales[sub] = s_scales[warp][st][sub];
                 const int byte = static_cast<int>(scales[sub] >> 8);
                 v_exp[sub] = byte == 255 ? __uint_as_float(0x7fc00000u) : static_cast<float>(byte - 127);
             }
-            uint32_t pw[kTiles][2][kParts][2];   // [16 keys][part][keys 0-7, 8-15]
+            uint32_t pw[kTiles][kSub][kParts][2];   // [16 keys][part][keys 0-7, 8-15]
             float share[kTiles][2];   // what a row's sums over this block are to be multiplied by
 #pragma unroll
             for (int n = 0; n < kTiles; ++n) {
-                float x[2][4];
+                float x[kSub][4];
 #pragma unroll
-                for (int sub = 0; sub < 2; ++sub) {
+                for (int sub = 0; sub < kSub; ++sub) {
                     const float k_scale = e8m0_power(scales[sub] & 255u);
 #pragma unroll
                     for (int f = 0; f < 4; ++f) {
@@ -663,26 +666,33 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float top[2] = {fmaxf(x[0][e], x[0][e + 2]), fmaxf(x[1][e], x[1][e + 2])};
+                    float top[kSub], mn = m[n][e];
+#pragma unroll
+                    for (int sub = 0; sub < kSub; ++sub) top[sub] = fmaxf(x[sub][e], x[sub][e + 2]);
 #pragma unroll
                     for (int d = 4; d < 32; d *= 2)
 #pragma unroll
-                        for (int sub = 0; sub < 2; ++sub)
+                        for (int sub = 0; sub < kSub; ++sub)
                             top[sub] = fmaxf(top[sub], __shfl_xor_sync(0xffffffffu, top[sub], d));
-                    const float mn = max3(m[n][e], top[0], top[1]);
+#pragma unroll
+                    for (int sub = 0; sub < kSub; sub += 2) mn = max3(mn, top[sub], top[sub + 1]);
                     const float base_m = mn == -INFINITY ? 0.0f : mn;
                     const float scale = ex2(m[n][e] - base_m);
                     m[n][e] = mn;
                     // The largest weight times its value's power: the block's weights, powers included, are taken as
                     // multiples of it, so that they use fp16's range whatever the blocks' powers are.  (A sum, not
                     // fmaxf: NaN stays.)
-                    const float r0 = top[0] + v_exp[0], r1 = top[1] + v_exp[1];
-                    const float ref = r0 >= r1 || r0 != r0 ? r0 : r1;
+                    float ref = top[0] + v_exp[0];
+#pragma unroll
+                    for (int sub = 1; sub < kSub; ++sub) {
+                        const float r = top[sub] + v_exp[sub];
+                        ref = ref >= r || ref != ref ? ref : r;
+                    }
                     const float base_r = ref == -INFINITY ? 0.0f : ref;
                     share[n][e] = ex2(ref - base_m);
                     float sum = 0.0f;
 #pragma unroll
-                    for (int sub = 0; sub < 2; ++sub)
+                    for (int sub = 0; sub < kSub; ++sub)
 #pragma unroll
                         for (int f = e; f < 4; f += 2) {
                             sum += ex2(x[sub][f] - base_m);
@@ -698,7 +708,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
                     }
                 }
 #pragma unroll
-                for (int sub = 0; sub < 2; ++sub)
+                for (int sub = 0; sub < kSub; ++sub)
 #pragma unroll
                     for (int f = 0; f < 2; ++f) {
                         const float lo = x[sub][2 * f], hi = x[sub][2 * f + 1];
@@ -714,9 +724,9 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
             const bool ragged = key0 + Cfg::kBlockKeys > it.hi || key0 < it.lo;
 #pragma unroll
             for (int c = 0; c < DP / 16; c += 2) {
-                uint32_t a[2][2][4];   // [16 keys][16 elements]
+                uint32_t a[kSub][2][4];   // [16 keys][16 elements]
 #pragma unroll
-                for (int sub = 0; sub < 2; ++sub) {
+                for (int sub = 0; sub < kSub; ++sub) {
                     uint32_t vf[4];    // keys 0-7 and 8-15 of two times 16 elements
                     ldmatrix_x4_trans(vf, piece8<DP>(vb + sub * kSplitKeys * DP, vrow, c + (lane >> 4)));
                     if (ragged) {
@@ -740,10 +750,13 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
 #pragma unroll
                     for (int k = 0; k < 2; ++k) mma_16816_first(y[k], a[0][k], pw[n][0][0][0], pw[n][0][0][1]);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) mma_16816<__half>(y[k], a[1][k], pw[n][1][0][0], pw[n][1][0][1]);
+                    for (int sub = 1; sub < kSub; ++sub)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            mma_16816<__half>(y[k], a[sub][k], pw[n][sub][0][0], pw[n][sub][0][1]);
                     if (kParts == 2) {
 #pragma unroll
-                        for (int sub = 0; sub < 2; ++sub)
+                        for (int sub = 0; sub < kSub; ++sub)
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
                                 mma_16816<__half>(y[k], a[sub][k], pw[n][sub][kParts - 1][0], pw[n][sub][kParts - 1][1]);
@@ -938,7 +951,7 @@ static int split_ctas() {
 }
 
 size_t attn_split_workspace_bytes() {
-    const size_t c = static_cast<size_t>(std::max(split_ctas<SplitCfg<128, false, 16>>(), split_ctas<SplitCfg<128, true, 16>>()));
+    const size_t c = static_cast<size_t>(std::max(split_ctas<SplitCfg<128, false, 16>>(), split_ctas<SplitCfg<64, true, 8>>()));
     return c * 2 * 16 * (128 + 2) * sizeof(float);
 }
 
