@@ -324,6 +324,8 @@ kt_status kt_kv8_append(const kt_paged_kv8* cache, const kt_paged_batch* batch, 
     if (k->heads != cache->heads || v->heads != cache->heads || (q && q_out->heads != q->heads))
         return refuse(KT_ERR_INVALID_ARG, "k and v must have the cache's heads, q_out q's");
     if (!aligned(err, 4)) return refuse(KT_ERR_ALIGNMENT, "err must be 4-byte aligned");
+    if ((batch->tokens / KT_KV8_BLOCK + 2ll * batch->seqs) * (cache->heads / 2 + 1) > INT_MAX / 2)
+        return refuse(KT_ERR_UNSUPPORTED_SHAPE, "too many blocks");
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     Kv8AppendParams p{};
     p.side[0] = Kv8Side{k->ptr, k->token_stride, k->head_stride, cache->k, cache->k_scales, cache->k_page_stride,
@@ -373,8 +375,7 @@ kt_status kt_kv8_append(const kt_paged_kv8* cache, const kt_paged_batch* batch, 
         h.err = err;
         if (too_many_rows(h)) return refuse(KT_ERR_UNSUPPORTED_SHAPE, "too many head rows");
     }
-    if ((st = cuda_status(launch_kv8_append(p, cache->dtype, s))) != KT_OK || !q) return st;
-    return cuda_status(launch_head_rows(h, cache->dtype, wide_rows(h), s));
+    return cuda_status(launch_kv8_append(p, q ? &h : nullptr, q && wide_rows(h), cache->dtype, s));
 }
 
 size_t kt_paged_attention_workspace_bytes(void) {

@@ -64,7 +64,8 @@ struct Kv8AppendParams {
     int least, most;      // scale exponents
     int* err;
 };
-cudaError_t launch_kv8_append(const Kv8AppendParams& p, int dtype, cudaStream_t s);
+// q: the step's queries (NULL for none), `wide` as launch_head_rows's of them.
+cudaError_t launch_kv8_append(const Kv8AppendParams& p, HeadRowsParams* q, bool wide, int dtype, cudaStream_t s);
 
 // ------------------------------------------------------------- attention
 struct AttnArgs {

@@ -8,9 +8,12 @@
 // most 16 of at most 128 elements, 64 elements a lane) stay in registers as fp32
 // from the loads to the codes.  Bound by memory (large steps) or by the chain of
 // look-ups, cu_q -> block table -> old scale (decode steps).
+//
+// The step's queries go through the head-row kernel's code: in the same launch where
+// there are few of them, whose time is that of launches.
 #include <algorithm>
 
-#include "kt_head_dev.cuh"
+#include "kt_head_rows_dev.cuh"
 #include "kt_internal.h"
 
 namespace kt {
@@ -56,19 +59,19 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float factor) {
     return r;
 }
 
-template <typename T, int NORM>   // NORM: 0 none, 1 weights of T, 2 fp32 weights
-__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Kv8AppendParams p) {
-    griddep_wait();
-    griddep_launch_dependents();
+template <typename T, int NORM>
+__device__ __forceinline__ void kv8_append_block(const Kv8AppendParams& p, unsigned launch_block) {
     const int lane = static_cast<int>(threadIdx.x) & 31;
-    const int unit = static_cast<int>(blockIdx.y) * (kAppendThreads / 32) + static_cast<int>(threadIdx.x >> 5);
+    const unsigned blocks = static_cast<unsigned>(first_block(p.tokens, p.seqs));
+    const int unit =
+        static_cast<int>(launch_block / blocks) * (kAppendThreads / 32) + static_cast<int>(threadIdx.x >> 5);
     if (unit >= 2 * p.heads) return;
     const bool keys = unit < p.heads;
     const int h = keys ? unit : unit - p.heads;
     const Kv8Side& sd = p.side[keys ? 0 : 1];
 
     // ---- the block: positions [lo, hi) of it are new, tok0 + position its tokens
-    const long long u = blockIdx.x;
+    const long long u = launch_block % blocks;
     const int b = sequence_of_block(p, u);
     const int t0 = min(max(p.cu_q[b], 0), p.tokens), t1 = min(max(p.cu_q[b + 1], t0), p.tokens);
     const int start = max(p.seq_lens[b], 0) - (t1 - t0);   // position of the first new token
@@ -123,8 +126,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Kv8App
     }
     uint64_t y[kPasses][2][kVec / 2];
     uint64_t w0[kVec / 2], w1[kVec / 2];
-    if (NORM != 0 && keys && used) {
-        if (NORM == 1) {
+    const bool normed = NORM != kNoNorm && keys && p.weight != nullptr;   // the same for the whole warp
+    if (normed && used) {
+        if (NORM == kWeightsTyped) {
             const uint4 a = load_weights<T, kVec>(p.weight, e0, p.weight_vector);
             const uint4 d = load_weights<T, kVec>(p.weight, e1, p.weight_vector);
             widen<T, kVec>(a, w0);
@@ -146,7 +150,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Kv8App
         const bool fresh = used && pos >= lo && pos < hi;
         widen<T, kVec>(x[i][0], y[i][0]);
         widen<T, kVec>(x[i][1], y[i][1]);
-        if (NORM != 0 && keys) {   // the same for the whole warp
+        if (normed) {
             uint64_t s2 = 0;       // two zeros
 #pragma unroll
             for (int k = 0; k < kVec / 2; ++k) s2 = fma2(y[i][1][k], y[i][1][k], fma2(y[i][0][k], y[i][0][k], s2));
@@ -226,19 +230,51 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(const Kv8App
     }
 }
 
-template <typename T>
-static cudaError_t launch_kv8_typed(const Kv8AppendParams& p, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(first_block(p.tokens, p.seqs)),
-                    static_cast<unsigned>((2 * p.heads + kAppendThreads / 32 - 1) / (kAppendThreads / 32)));
-    count_launches(1);
-    return launch_chained(p.weight == nullptr ? kv8_append_kernel<T, 0>
-                          : p.weight_f32      ? kv8_append_kernel<T, 2>
-                                              : kv8_append_kernel<T, 1>,
-                          grid, dim3(kAppendThreads), 0, s, p);
+template <typename T, int NORM>
+__global__ void __launch_bounds__(kAppendThreads, 5) kv8_append_kernel(const Kv8AppendParams p) {
+    griddep_wait();
+    griddep_launch_dependents();
+    kv8_append_block<T, NORM>(p, blockIdx.x);
+}
+// The same and the queries: blocks from `blocks` on are the head rows'.
+template <typename T, int NORM>
+__global__ void __launch_bounds__(kAppendThreads)
+    kv8_append_queries_kernel(const Kv8AppendParams p, const HeadRowsParams q, unsigned blocks) {
+    static_assert(kAppendThreads == kRowThreads, "one launch");
+    griddep_wait();
+    griddep_launch_dependents();
+    if (blockIdx.x < blocks) kv8_append_block<T, NORM>(p, blockIdx.x);
+    else head_rows_block<T, 8, 1, NORM, false>(q, blockIdx.x - blocks);
 }
 
-cudaError_t launch_kv8_append(const Kv8AppendParams& p, int dtype, cudaStream_t s) {
-    return dtype == KT_DTYPE_BF16 ? launch_kv8_typed<__nv_bfloat16>(p, s) : launch_kv8_typed<__half>(p, s);
+template <typename T>
+static cudaError_t launch_kv8_typed(const Kv8AppendParams& p, HeadRowsParams* q, bool wide, int dtype, cudaStream_t s) {
+    const unsigned blocks = static_cast<unsigned>(first_block(p.tokens, p.seqs)) *
+                            static_cast<unsigned>((2 * p.heads + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
+    const bool normed = p.weight != nullptr || (q != nullptr && q->seg[0].weight != nullptr);
+    // Few query rows: one launch (48 single tokens of 64 + 8 heads of 128: 4.9 us in two, 3.3 in one).  Many: two, for
+    // one row at a time and this kernel's registers leave too few loads under way (three prompts of up to 3500 tokens:
+    // 45 us in two, 83 in one).
+    if (q != nullptr && wide && static_cast<long long>(q->tokens) * q->seg[0].heads < 16384) {
+        const unsigned rows = plan_head_rows<8, 1>(*q);
+        count_launches(1);
+        return launch_chained(!normed          ? kv8_append_queries_kernel<T, kNoNorm>
+                              : p.weight_f32   ? kv8_append_queries_kernel<T, kWeightsF32>
+                                               : kv8_append_queries_kernel<T, kWeightsTyped>,
+                              dim3(blocks + rows), dim3(kAppendThreads), 0, s, p, static_cast<const HeadRowsParams&>(*q),
+                              blocks);
+    }
+    count_launches(1);
+    const cudaError_t e = launch_chained(p.weight == nullptr ? kv8_append_kernel<T, kNoNorm>
+                                         : p.weight_f32      ? kv8_append_kernel<T, kWeightsF32>
+                                                             : kv8_append_kernel<T, kWeightsTyped>,
+                                         dim3(blocks), dim3(kAppendThreads), 0, s, p);
+    return e != cudaSuccess || q == nullptr ? e : launch_head_rows(*q, dtype, wide, s);
+}
+
+cudaError_t launch_kv8_append(const Kv8AppendParams& p, HeadRowsParams* q, bool wide, int dtype, cudaStream_t s) {
+    return dtype == KT_DTYPE_BF16 ? launch_kv8_typed<__nv_bfloat16>(p, q, wide, dtype, s)
+                                  : launch_kv8_typed<__half>(p, q, wide, dtype, s);
 }
 
 }  // namespace kt

@@ -23,6 +23,7 @@ MAX_HIDDEN = 32768   # KT_NORM_MAX_HIDDEN
 TOKEN_ROWS = "Pq"    # kt_token_rows: ptr, token_stride
 _ROWS_BYTES = struct.calcsize(TOKEN_ROWS)
 _CALL = struct.Struct(4 * TOKEN_ROWS)
+_NO_ROWS = (0, 0)
 
 
 def _rows(t, name: str, dtype, device: int, shape):
@@ -50,6 +51,14 @@ def _bytes(t, name: str, device: int, shape):
     if t.get_device() != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {list(shape)} on cuda:{device}")
     return t.data_ptr()
+
+
+def _empty_mx(x, n: int, h: int, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _empty_mx(x, n, h, None)
+    return (torch.empty((n, h), dtype=torch.uint8, device=x.device),
+            torch.empty((n, h // 32), dtype=torch.uint8, device=x.device))
 
 
 def _apart(outs, ins, n: int, h: int):
@@ -100,18 +109,17 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
     n, h = shape
     rx = _rows(x, "x", dt, dev, shape)
     w = _a._weight(weight, "weight", dt, h, dev)
-    given, ins = [], [("x", rx[0], 2 * rx[1], 2 * h), ("weight", w, 0, weight.element_size() * h)]
-    rr = ro = ry = (0, 0)
+    rr = ro = ry = _NO_ROWS
     codes = scales = None
+    given = []                                             # outputs that the caller brings
     if residual is not None:
         rr = _rows(residual, "residual", dt, dev, shape)
-        ins.append(("residual", rr[0], 2 * rr[1], 2 * h))
         if residual_out is None:
             residual_out = _a._output(x, stream)
+            ro = (residual_out.data_ptr(), h)
         else:
             ro = _rows(residual_out, "residual_out", dt, dev, shape)
             given.append(("residual_out", ro[0], 2 * ro[1], 2 * h))
-        ro = ro if ro[0] else (residual_out.data_ptr(), h)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if plain:
@@ -127,10 +135,8 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
         if h % 32:
             raise ValueError(f"hidden={h} must be a multiple of 32 for MXFP8")
         if mx_out is None:
-            with torch.cuda.stream(stream):
-                mx_out = (torch.empty(n, h, dtype=torch.uint8, device=x.device),
-                          torch.empty(n, h // 32, dtype=torch.uint8, device=x.device))
-            codes, scales = (t.data_ptr() for t in mx_out)
+            mx_out = _empty_mx(x, n, h, stream)
+            codes, scales = mx_out[0].data_ptr(), mx_out[1].data_ptr()
         else:
             codes = _bytes(mx_out[0], "mx_out[0]", dev, (n, h))
             scales = _bytes(mx_out[1], "mx_out[1]", dev, (n, h // 32))
@@ -138,10 +144,13 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
     elif mx_out is not None:
         raise ValueError("mx_out needs mx=True")
     if given:
+        ins = [("x", rx[0], 2 * rx[1], 2 * h), ("weight", w, 0, weight.element_size() * h)]
+        if residual is not None:
+            ins.append(("residual", rr[0], 2 * rr[1], 2 * h))
         _apart(given, ins, n, h)
     b = _a._buffer
     _CALL.pack_into(b.buf, 0, *rx, *rr, *ro, *ry)
-    _a._call(dev, stream, "kt_add_rms_norm", b.at, b.at + _ROWS_BYTES, w,
-             _a.DTYPE_CODES.get(weight.dtype, _a.KT_DTYPE_F32), eps, n, h, _a.DTYPE_CODES[dt], b.at + 2 * _ROWS_BYTES,
-             b.at + 3 * _ROWS_BYTES, codes, scales)
+    at = b.at
+    _a._call(dev, stream, "kt_add_rms_norm", at, at + _ROWS_BYTES, w, _a.DTYPE_CODES.get(weight.dtype, _a.KT_DTYPE_F32),
+             eps, n, h, _a.DTYPE_CODES[dt], at + 2 * _ROWS_BYTES, at + 3 * _ROWS_BYTES, codes, scales)
     return (out if plain else None), (residual_out if residual is not None else None), (tuple(mx_out) if mx else None)
