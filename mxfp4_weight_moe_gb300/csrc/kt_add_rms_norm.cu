@@ -5,7 +5,8 @@
 // registers as fp32 between its sum of squares and its outputs, so that x and the
 // residual are read once.  A chunk of 8 elements (16 bytes) belongs to one thread;
 // the 32 elements of an MXFP8 scale to four neighbouring lanes.  Bound by memory
-// for many rows, by latency for few.
+// for many rows (8192 tokens of 7168
+// in 77.8 us, the measured copy rate), by latency for few.
 #include <climits>
 #include <cmath>
 #include <cstdarg>
@@ -45,15 +46,18 @@ __device__ __forceinline__ uint4 narrow8(const float (&v)[8]) {
     return make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
 }
 
-// ROWS rows a block of ROWS * WARPS warps, CHUNKS chunks of 8 elements a thread.
-template <typename T, int WARPS, int ROWS, int CHUNKS>
-__global__ void __launch_bounds__(WARPS * ROWS * 32) add_rms_norm_kernel(const NormParams p) {
-    __shared__ float s_sum[ROWS][WARPS];
+constexpr int kSmallRows = 4;   // rows a block where a row is one warp's
+
+// CHUNKS chunks of 8 elements a thread; a row is a block's (as many warps as it takes), or a warp's (SMALL).
+template <typename T, int CHUNKS, bool SMALL>
+__global__ void __launch_bounds__(SMALL ? kSmallRows * 32 : 1024) add_rms_norm_kernel(const NormParams p) {
+    __shared__ float s_sum[32];
     griddep_wait();
     griddep_launch_dependents();
-    constexpr int kThreads = WARPS * 32;   // of a row
-    const int tid = static_cast<int>(threadIdx.x) % kThreads, sub = static_cast<int>(threadIdx.x) / kThreads;
-    const long long token = static_cast<long long>(blockIdx.x) * ROWS + sub;
+    const int kThreads = SMALL ? 32 : static_cast<int>(blockDim.x);   // of a row
+    const int tid = SMALL ? static_cast<int>(threadIdx.x) % 32 : static_cast<int>(threadIdx.x);
+    const long long token =
+        SMALL ? static_cast<long long>(blockIdx.x) * kSmallRows + threadIdx.x / 32 : static_cast<long long>(blockIdx.x);
     const bool row = token < p.tokens;
     const int chunks = p.hidden >> 3;
     const T* x = static_cast<const T*>(p.x) + token * p.x_stride;
@@ -64,8 +68,8 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) add_rms_norm_kernel(const N
         const int at = tid + c * kThreads;
         rx[c] = rr[c] = make_uint4(0, 0, 0, 0);
         if (row && at < chunks) {
-            rx[c] = __ldcs(reinterpret_cast<const uint4*>(x) + at);
-            if (p.residual != nullptr) rr[c] = __ldcs(reinterpret_cast<const uint4*>(r) + at);
+            rx[c] = reinterpret_cast<const uint4*>(x)[at];
+            if (p.residual != nullptr) rr[c] = reinterpret_cast<const uint4*>(r)[at];
         }
     }
     float s[CHUNKS][8];
@@ -83,15 +87,15 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) add_rms_norm_kernel(const N
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (WARPS > 1) {
-        if ((tid & 31) == 0) s_sum[sub][tid >> 5] = sum;
+    if (!SMALL) {
+        if ((tid & 31) == 0) s_sum[tid >> 5] = sum;
         __syncthreads();
-        sum = 0.0f;
+        sum = (tid & 31) < kThreads / 32 ? s_sum[tid & 31] : 0.0f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) sum += s_sum[sub][w];
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
     const float inv = rsqrtf(sum * p.inv_hidden + p.eps);
-    if (!row) return;   // whole warps: WARPS > 1 has one row a block
+    if (!row) return;   // a whole warp
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
         const int at = tid + c * kThreads;
@@ -99,8 +103,7 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) add_rms_norm_kernel(const N
         float y[8];
         if (mine) {
             if (p.residual_out != nullptr)
-                __stcs(reinterpret_cast<uint4*>(static_cast<T*>(p.residual_out) + token * p.ro_stride) + at,
-                       narrow8<T>(s[c]));
+                reinterpret_cast<uint4*>(static_cast<T*>(p.residual_out) + token * p.ro_stride)[at] = narrow8<T>(s[c]);
             float w[8];
             if (p.weight_f32) {
                 const float4 a = reinterpret_cast<const float4*>(p.weight)[2 * at];
@@ -139,23 +142,27 @@ __global__ void __launch_bounds__(WARPS * ROWS * 32) add_rms_norm_kernel(const N
     }
 }
 
-template <typename T, int WARPS, int ROWS, int CHUNKS>
+template <typename T, int CHUNKS, bool SMALL>
 static cudaError_t launch_norm(const NormParams& p, cudaStream_t s) {
     count_launches(1);
-    return launch_chained(add_rms_norm_kernel<T, WARPS, ROWS, CHUNKS>,
-                          dim3(static_cast<unsigned>((p.tokens + ROWS - 1) / ROWS)), dim3(WARPS * ROWS * 32), 0, s, p);
+    const int chunks = p.hidden / 8;
+    const int threads = SMALL ? kSmallRows * 32 : (chunks + 32 * CHUNKS - 1) / (32 * CHUNKS) * 32;
+    const int blocks = SMALL ? (p.tokens + kSmallRows - 1) / kSmallRows : p.tokens;
+    return launch_chained(add_rms_norm_kernel<T, CHUNKS, SMALL>, dim3(static_cast<unsigned>(blocks)),
+                          dim3(static_cast<unsigned>(threads)), 0, s, p);
 }
 
 template <typename T>
 static cudaError_t launch_norm_typed(const NormParams& p, cudaStream_t s) {
     const int chunks = p.hidden / 8;
-    if (chunks <= 32) return launch_norm<T, 1, 4, 1>(p, s);
-    if (chunks <= 128) return launch_norm<T, 1, 4, 4>(p, s);
-    if (chunks <= 256) return launch_norm<T, 4, 1, 2>(p, s);
-    if (chunks <= 512) return launch_norm<T, 8, 1, 2>(p, s);
-    if (chunks <= 1024) return launch_norm<T, 16, 1, 2>(p, s);
-    if (chunks <= 2048) return launch_norm<T, 32, 1, 2>(p, s);
-    return launch_norm<T, 32, 1, 4>(p, s);
+    if (chunks <= 32) return launch_norm<T, 1, true>(p, s);
+    if (chunks <= 128) return launch_norm<T, 4, true>(p, s);
+    // Small steps: a chunk a thread (1 token of 7168: 2.3 us, 2.9 with four; 600 tokens of 2048: 2.4 and 3.3).  Large
+    // ones: four, for the loads under way (8192 tokens of 7168, all outputs, 531 MB: 77.8 us, 6.8 TB/s, and 89.9 with
+    // one).  They meet at 2 to 4 million elements (450 tokens of 7168: 5.0 and 5.2; 600: 5.8 and 5.0; 2000 of 2048: 5.0
+    // and 5.4).
+    if (static_cast<long long>(p.tokens) * chunks <= (1 << 19) && chunks <= 1024) return launch_norm<T, 1, false>(p, s);
+    return launch_norm<T, 4, false>(p, s);
 }
 
 static bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
