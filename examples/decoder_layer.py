@@ -5,14 +5,17 @@
 A step takes the hidden states of some sequences' new tokens (whole prompts, chunks of them, single tokens, or all of
 these together) and runs
 
+    norm                                  add_rms_norm         (one launch)
     qkv projection                        torch matmul
     norm + rotation of q and k, append    PagedKV.append       (one launch)
     attention over the pages              PagedKV.attend       (one launch)
-    output projection, residual           torch matmul
-    routing + experts, residual           MoeLayer             (MXFP4 weights)
+    output projection                     torch matmul
+    residual + norm, in 16 bits for the   add_rms_norm         (one launch)
+      router and in MXFP8 for the experts
+    routing + experts, residual           MoeLayer             (MXFP4 weights, MXFP8 tokens)
 
-The script prefills two prompts of different lengths, decodes a few tokens of each, and compares the decoded tokens'
-hidden states with those of one prefill of everything.
+The cache holds 16 bits an element, or 8 (PagedKV8).  The script prefills two prompts of different lengths, decodes a few
+tokens of each, and compares the decoded tokens' hidden states with those of one prefill of everything.
 """
 from __future__ import annotations
 
@@ -53,7 +56,8 @@ class Pages:
 
 class DecoderLayer:
     def __init__(self, hidden: int, q_heads: int, kv_heads: int, head_dim: int, experts: int, top_k: int, inter: int,
-                 num_pages: int, page_size: int = 16, max_positions: int = 4096, seed: int = 0, device="cuda"):
+                 num_pages: int, page_size: int = 16, max_positions: int = 4096, seed: int = 0, device="cuda",
+                 cache_bits: int = 16):
         g = torch.Generator(device=device)
         g.manual_seed(seed)
 
@@ -67,37 +71,39 @@ class DecoderLayer:
         self.q_norm = torch.ones(head_dim, dtype=torch.bfloat16, device=device)
         self.k_norm = torch.ones(head_dim, dtype=torch.bfloat16, device=device)
         self.rope = kt.rope_table(max_positions, head_dim, device=device)
-        pages = torch.empty(2, num_pages, page_size, kv_heads, head_dim, dtype=torch.bfloat16, device=device)
-        self.cache = kt.PagedKV(pages[0], pages[1])
+        self.in_norm, self.out_norm = (torch.ones(hidden, dtype=torch.bfloat16, device=device) for _ in range(2))
+        pages = torch.empty(2, num_pages, page_size, kv_heads, head_dim, device=device,
+                            dtype=torch.bfloat16 if cache_bits == 16 else torch.float8_e4m3fn)
+        if cache_bits == 16:
+            self.cache = kt.PagedKV(pages[0], pages[1])
+        else:
+            scales = torch.empty(2, num_pages, page_size // kt.PagedKV8.BLOCK, kv_heads, dtype=torch.uint8, device=device)
+            self.cache = kt.PagedKV8(pages[0], pages[1], scales[0], scales[1], torch.bfloat16)
         packed = [syn.make_expert(e, hidden, inter, seed, device) for e in range(experts)]
         self.moe = kt.MoeLayer(*[torch.stack(t).contiguous() for t in zip(*packed)], top_k)
 
     def __call__(self, x: torch.Tensor, block_table, cu_q, seq_lens, max_q_len) -> torch.Tensor:
         """x: bf16 [tokens, hidden] of the step; returns the layer's output of the same shape."""
         n = x.shape[0]
-        qkv = (self._rms(x) @ self.w_qkv.T).view(n, self.hq + 2 * self.hk, self.d)
+        h, _, _ = kt.add_rms_norm(x, self.in_norm)
+        qkv = (h @ self.w_qkv.T).view(n, self.hq + 2 * self.hk, self.d)
         q, k, v = qkv.split((self.hq, self.hk, self.hk), dim=1)
         q = self.cache.append(k, v, block_table, cu_q, seq_lens, self.rope, q=q, q_weight=self.q_norm,
                               k_weight=self.k_norm)
         y = self.cache.attend(q, block_table, cu_q, seq_lens, max_q_len)
-        x = x + y.view(n, -1) @ self.w_o.T
-        h = self._rms(x)
-        out, _, _ = self.moe(h, (h @ self.w_router.T).float())
+        h, x, tokens = kt.add_rms_norm(y.view(n, -1) @ self.w_o.T, self.out_norm, x, mx=True)
+        out, _, _ = self.moe(tokens, (h @ self.w_router.T).float())
         return x + out
-
-    @staticmethod
-    def _rms(x):
-        return torch.nn.functional.rms_norm(x.float(), x.shape[-1:], eps=1e-6).to(x.dtype)
 
 
 def run(prompts=(37, 150), decode=4, hidden=1024, q_heads=16, kv_heads=2, head_dim=128, experts=16, top_k=4, inter=512,
-        seed=0, device="cuda"):
+        seed=0, device="cuda", cache_bits=16):
     """Largest relative difference (per token, by norm) of the decoded tokens between serving and one prefill."""
     g = torch.Generator(device=device)
     g.manual_seed(seed)
     total = [p + decode for p in prompts]
     layer = DecoderLayer(hidden, q_heads, kv_heads, head_dim, experts, top_k, inter,
-                         num_pages=2 * sum(-(-t // 16) for t in total), device=device)
+                         num_pages=2 * sum(-(-t // 16) for t in total), device=device, cache_bits=cache_bits)
     xs = [torch.randn(t, hidden, generator=g, device=device).to(torch.bfloat16) for t in total]
     pages = Pages(layer.cache.num_pages, layer.cache.page_size, device)
     for _ in prompts:
@@ -119,4 +125,6 @@ def run(prompts=(37, 150), decode=4, hidden=1024, q_heads=16, kv_heads=2, head_d
 
 
 if __name__ == "__main__":
-    print(f"decoded tokens against one prefill: largest relative difference {run():.2e}")
+    for bits in (16, 8):
+        print(f"decoded tokens against one prefill, {bits}-bit cache: largest relative difference "
+              f"{run(cache_bits=bits):.2e}")

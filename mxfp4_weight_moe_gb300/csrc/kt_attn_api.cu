@@ -412,10 +412,12 @@ static kt_status attention_impl(const kt_paged_kv* cache, const uint8_t* k_scale
                       kt_paged_attention_workspace_bytes());
     AttnArgs a{*cache, k_scales, v_scales, *batch, *q, *out, scale, window, sinks, err, static_cast<unsigned*>(ws),
                static_cast<uint8_t*>(ws) + KT_PAGED_ATTENTION_ZEROED};
-    // The split kernel's tiles hold 16 query rows: it reads the keys once for chunks of up to so many.  The tile
-    // kernel loads its queries by TMA, which needs strides.
+    // The split kernel's tiles hold 16 query rows: it reads the keys once for chunks of up to so many.  Over an 8-bit
+    // cache, which the tile kernel has to widen, reading them twice is no slower (64 x 4 tokens after up to 8191 under 8
+    // heads a cache head, 32 rows: 433 us and 449; 16 x 4 after 3000: 53 and 57; one sequence after 16000: 28.7 and 30.3;
+    // three times: 640 and 453).  The tile kernel loads its queries by TMA, which needs strides.
     const long long rows = static_cast<long long>(max_q_len) * (q->heads / cache->heads);
-    if (rows <= 16 || q->token_stride == 0 || q->head_stride == 0)
+    if (rows <= (k_scales != nullptr ? 32 : 16) || q->token_stride == 0 || q->head_stride == 0)
         return launch_attn_split(a, static_cast<int>(std::min(rows, 1024ll)), static_cast<cudaStream_t>(stream));
     return launch_attn_tile(a, static_cast<cudaStream_t>(stream));
 }

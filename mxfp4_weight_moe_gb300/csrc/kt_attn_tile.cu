@@ -26,7 +26,8 @@
 // last joins them in order, so the result does not depend on which that was.
 //
 // Warps: 0-3 softmax of group 0, 4-7 of group 1, 8 issues the MMAs, 9 to 11 the
-// TMA loads of keys, values and queries.
+// TMA loads of keys, values and queries; over an 8-bit cache, 12 to 15 widen the
+// tiles' codes.
 //
 // Bound: for heads of 128 the tensor cores (2630 of 3000 cycles of a tile pair),
 // for smaller heads the softmax (128 exponentials a row and tile: 1370 cycles of
@@ -36,13 +37,24 @@
 // of the sustained one), up to 790 us on others; heads of 64, 600 to 652 us, 842 to
 // 916 TFLOP/s; 2048 tokens after 30001 on 16-slot pages (fp16, 32 / 8 heads of 128)
 // 652 to 702 us, 1480 to 1600 TFLOP/s (757 us in seconds of calls, under the power
-// cap at 1537 MHz).
+// cap at 1537 MHz).  Over 8-bit caches: the prompt (bf16) 950 us, 1160 TFLOP/s, in
+// fp16 870; 24 sequences of up to 500 new tokens, 40 / 8 heads of 96, 262 us (16-bit:
+// 184); heads of 64, window 128, 76 us (68).  There the widening is what is waited for:
+// without its arithmetic and stores (a wrong result, timed) the prompt takes 693 us,
+// with the loads and stores alone 857: its stores share the shared memory with the
+// products of Q K^T, whose operands take all of its bandwidth, its instructions the
+// schedulers with the softmax (36 for 16 codes in bf16, 20 in fp16).
 //
 // Tried and left out (8192-token prompt): P beside S so that the next S comes
 // early (heads of 64: 636 against 614 us, both groups then contend for the
 // exponential unit); the maximum of the second half under the first half's
 // weights (738 against 677 us, registers spill); 224 registers for the softmax
 // warps (694 against 674 us); the weights handed over at once (705 against 674).
+// Over 8-bit caches (bf16, 950 us): eight widening warps instead of four (1020 to
+// 1060, the softmax spills), two for keys and two for values (1088 when four took
+// 1054), more tiles of codes and fewer wide ones in the rings (964), the next 16 rows'
+// codes loaded ahead (1024), two copies of the widening loop's body (1230: it and the
+// softmax then do not fit the instruction cache together).
 #include <algorithm>
 #include <type_traits>
 
@@ -556,7 +568,7 @@ __global__ void __launch_bounds__(TileCfg<DP, KV8>::kThreads, 1)
             uint8_t* wide = kv_ptr + st * Cfg::kStageBytes;
             const bool ragged = seen.x > 0 || seen.y < kTileKeys;
             // One copy of the code for a tile's blocks: straight code would not stay in the instruction cache beside the
-            // softmax's (one prompt of 8192, 64 / 8 heads of 128: 1641 us, 1054 so).  Powers that bf16's 2^120 leaves no
+            // softmax's.  Powers that bf16's 2^120 leaves no
             // room for, and tiles with rows that no token sees, have another copy.
             auto tile = [&](auto plain) {
                 constexpr bool kPlain = decltype(plain)::value;
