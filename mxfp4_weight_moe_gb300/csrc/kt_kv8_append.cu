@@ -265,9 +265,9 @@ static cudaError_t launch_kv8_typed(const Kv8AppendParams& p, HeadRowsParams* q,
                               blocks);
     }
     count_launches(1);
-    const cudaError_t e = launch_chained(p.weight == nullptr ? kv8_append_kernel<T, kNoNorm>
-                                         : p.weight_f32      ? kv8_append_kernel<T, kWeightsF32>
-                                                             : kv8_append_kernel<T, kWeightsTyped>,
+    const cudaError_t e = launch_chained(!p.weight        ? kv8_append_kernel<T, kNoNorm>
+                                         : p.weight_f32   ? kv8_append_kernel<T, kWeightsF32>
+                                                          : kv8_append_kernel<T, kWeightsTyped>,
                                          dim3(blocks), dim3(kAppendThreads), 0, s, p);
     return e != cudaSuccess || q == nullptr ? e : launch_head_rows(*q, dtype, wide, s);
 }
