@@ -37,24 +37,27 @@
 // of the sustained one), up to 790 us on others; heads of 64, 600 to 652 us, 842 to
 // 916 TFLOP/s; 2048 tokens after 30001 on 16-slot pages (fp16, 32 / 8 heads of 128)
 // 652 to 702 us, 1480 to 1600 TFLOP/s (757 us in seconds of calls, under the power
-// cap at 1537 MHz).  Over 8-bit caches: the prompt (bf16) 950 us, 1160 TFLOP/s, in
-// fp16 870; 24 sequences of up to 500 new tokens, 40 / 8 heads of 96, 262 us (16-bit:
-// 184); heads of 64, window 128, 76 us (68).  There the widening is what is waited for:
-// without its arithmetic and stores (a wrong result, timed) the prompt takes 693 us,
-// with the loads and stores alone 857: its stores share the shared memory with the
-// products of Q K^T, whose operands take all of its bandwidth, its instructions the
-// schedulers with the softmax (36 for 16 codes in bf16, 20 in fp16).
+// cap at 1537 MHz).
+//
+// Over 8-bit caches: the prompt 863 us (bf16; fp16 900), 1270 TFLOP/s; 24 sequences of
+// up to 500 new tokens, 40 / 8 heads of 96, 248 us (16-bit: 184); heads of 64, window
+// 128, 76 us (68).  With nothing widened (a wrong result, timed) the prompt takes 723
+// us, with the widening's loads and stores but not its arithmetic no less than with
+// it: its traffic shares the shared memory with the products of Q K^T, whose operands
+// take all of its bandwidth.
 //
 // Tried and left out (8192-token prompt): P beside S so that the next S comes
 // early (heads of 64: 636 against 614 us, both groups then contend for the
 // exponential unit); the maximum of the second half under the first half's
 // weights (738 against 677 us, registers spill); 224 registers for the softmax
 // warps (694 against 674 us); the weights handed over at once (705 against 674).
-// Over 8-bit caches (bf16, 950 us): eight widening warps instead of four (1020 to
-// 1060, the softmax spills), two for keys and two for values (1088 when four took
-// 1054), more tiles of codes and fewer wide ones in the rings (964), the next 16 rows'
-// codes loaded ahead (1024), two copies of the widening loop's body (1230: it and the
-// softmax then do not fit the instruction cache together).
+// Over 8-bit caches (bf16): a tile's slot freed after its widening instead of after
+// its loads (952 against 863 us; the next tile's load then waits); when that was so,
+// eight widening warps instead of four (1020 to 1060, the softmax spills), two for
+// keys and two for values (1088 against 1054), the codes of 16 rows loaded ahead
+// (1024), two copies of the loop's body (1230: it and the softmax then do not fit the
+// instruction cache together; 1065 now); more tiles of codes and fewer wide ones in
+// the rings (882 against 863).
 #include <algorithm>
 #include <type_traits>
 
@@ -544,6 +547,7 @@ __global__ void __launch_bounds__(TileCfg<DP, KV8>::kThreads, 1)
         // ---------------------------------------------------- codes to T, 128 / kWideners rows of a tile a warp
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kWidenRegs));
         constexpr int kBlocks = kTileKeys / KT_KV8_BLOCK / Cfg::kWideners;   // of rows under one scale
+        constexpr int kHalves = DP / 64, kPasses = 2 * kHalves;              // 8 rows of 64 elements each, of a block
         // Eight rows of four 16-byte pieces a pass.  A row's 16 codes are two 16-byte chunks of the wide row (piece p:
         // 2p and 2p + 1, where its swizzle puts them): lanes 4 to 7 of eight take the row whose number differs in bits 0
         // and 2, so that the eight meet all banks in loads and stores.
@@ -558,41 +562,53 @@ __global__ void __launch_bounds__(TileCfg<DP, KV8>::kThreads, 1)
             if (!ok) break;
             const int2 seen = s_raw_rows[rs];
             if (seen.y < 0) break;
-            const int* scales = &s_raw_scale[rs][(warp - 12) * kBlocks];
-            int top = scales[0];
+            // The codes into registers and their slot free at once: the next tile's load, longer than the widening, begins.
+            const uint8_t* raw = raw_ptr + rs * Cfg::kRawBytes;
+            int scale[kBlocks];
+            uint4 v[kBlocks][kPasses];
 #pragma unroll
-            for (int i = 1; i < kBlocks; ++i) top = max(top, scales[i]);
+            for (int i = 0; i < kBlocks; ++i) {
+                scale[i] = s_raw_scale[rs][(warp - 12) * kBlocks + i];
+#pragma unroll
+                for (int k = 0; k < kPasses; ++k)
+                    v[i][k] = *reinterpret_cast<const uint4*>(raw + (in0 ^ (k % kHalves * 64)) +
+                                                              (i * KT_KV8_BLOCK + k / kHalves * 8) * DP);
+            }
+            int top = scale[0];
+#pragma unroll
+            for (int i = 1; i < kBlocks; ++i) top = max(top, scale[i]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&s_raw_empty[rs]));
             ok = warp_wait(smem_u32(&s_kv_empty[st]), parity, abort_flag, limit);
             if (!ok) break;
-            const uint8_t* raw = raw_ptr + rs * Cfg::kRawBytes;
             uint8_t* wide = kv_ptr + st * Cfg::kStageBytes;
             const bool ragged = seen.x > 0 || seen.y < kTileKeys;
             // One copy of the code for a tile's blocks: straight code would not stay in the instruction cache beside the
-            // softmax's.  Powers that bf16's 2^120 leaves no
-            // room for, and tiles with rows that no token sees, have another copy.
+            // softmax's.  Powers that bf16's 2^120 leaves no room for, and tiles with rows that no token sees, have
+            // another copy.
             auto tile = [&](auto plain) {
                 constexpr bool kPlain = decltype(plain)::value;
-                constexpr int kHalves = DP / 64, kPasses = 2 * kHalves;   // 8 rows of 64 elements each
 #pragma unroll 1
                 for (int i = 0; i < kBlocks; ++i) {
-                    uint32_t more, factor = widen_factor<T>(scales[i], more);
-                    const uint8_t* src = raw + i * KT_KV8_BLOCK * DP;
+                    uint32_t more, factor = widen_factor<T>(scale[0], more);
                     uint8_t* dst = wide + i * KT_KV8_BLOCK * 128;
-                    uint4 v[kPasses];
-#pragma unroll
-                    for (int k = 0; k < kPasses; ++k)
-                        v[k] = *reinterpret_cast<const uint4*>(src + (in0 ^ (k % kHalves * 64)) + k / kHalves * 8 * DP);
 #pragma unroll
                     for (int k = 0; k < kPasses; ++k) {
                         uint32_t f = factor, m = kPlain ? 0 : more;
                         const int row = row0 + i * KT_KV8_BLOCK + k / kHalves * 8;
                         if (!kPlain && (row < seen.x || row >= seen.y))
-                            v[k] = make_uint4(0, 0, 0, 0), f = m = 0;   // whatever codes and scale are there
+                            v[0][k] = make_uint4(0, 0, 0, 0), f = m = 0;   // whatever codes and scale are there
                         uint4 a, b;
-                        widen16<T>(v[k], f, m, a, b);
+                        widen16<T>(v[0][k], f, m, a, b);
                         uint8_t* out = dst + k % kHalves * (kTileKeys * 128) + k / kHalves * 8 * 128;
                         *reinterpret_cast<uint4*>(out + out0) = a;
                         *reinterpret_cast<uint4*>(out + (out0 ^ 16)) = b;
+                    }
+#pragma unroll
+                    for (int j = 0; j + 1 < kBlocks; ++j) {   // the next block's (registers cannot be indexed by i)
+                        scale[j] = scale[j + 1];
+#pragma unroll
+                        for (int k = 0; k < kPasses; ++k) v[j][k] = v[j + 1][k];
                     }
                 }
             };
@@ -600,10 +616,7 @@ __global__ void __launch_bounds__(TileCfg<DP, KV8>::kThreads, 1)
             else tile(std::false_type());
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_u32(&s_kv_full[st]));
-                mbar_arrive(smem_u32(&s_raw_empty[rs]));
-            }
+            if (lane == 0) mbar_arrive(smem_u32(&s_kv_full[st]));
             if (++rs == kRaw) rs = 0, raw_parity ^= 1u;
             if (++st == Cfg::kStages) st = 0, parity ^= 1u;
         }
