@@ -84,26 +84,10 @@ __device__ __forceinline__ void kv8_append_block(const Kv8AppendParams& p, unsig
     const int base = static_cast<int>(at);
     const int lo = max(first, base);
     int hi = static_cast<int>(min(end, at + kBlk));
-    const int index = base / p.page_size;
-    int page = -1;
-    if (index < p.max_pages) page = p.block_table[b * p.table_stride + index];
-    if (page < 0 || page >= p.num_pages) {
-        if (lane == 0) set_error(p.err, KT_DEVERR_BAD_PAGE);
-        return;
-    }
     if (p.table != nullptr && hi > p.positions_end) {
         if (lane == 0) set_error(p.err, KT_DEVERR_BAD_POSITION);
         hi = p.positions_end;
-        if (lo >= hi) return;
     }
-    const int slot = base - index * p.page_size;
-    uint8_t* const scale_at =
-        sd.scales + (static_cast<long long>(page) * (p.page_size / kBlk) + slot / kBlk) * p.heads + h;
-    uint8_t* const block = sd.codes + page * sd.page + slot * sd.slot + h * sd.head;
-    const int older = lo - base;   // rows of the block that were there before
-    int exponent = p.least;
-    const int old_byte = older > 0 ? *scale_at : p.least + 127;
-
     // ---- new rows: lane c of a row owns the chunks that hold both halves of its rotated pairs
     const int c = lane % kRowLanes, r0 = lane / kRowLanes;
     const bool used = c * 2 * kVec < p.head_dim;
@@ -120,10 +104,27 @@ __device__ __forceinline__ void kv8_append_block(const Kv8AppendParams& p, unsig
         x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
         if (used && pos >= lo && pos < hi) {
             const T* row = src + (static_cast<long long>(t0) + (pos - start)) * sd.src_token;
-            x[i][0] = __ldcs(reinterpret_cast<const uint4*>(row + e0));
-            x[i][1] = __ldcs(reinterpret_cast<const uint4*>(row + e1));
+            x[i][0] = *reinterpret_cast<const uint4*>(row + e0);
+            x[i][1] = *reinterpret_cast<const uint4*>(row + e1);
         }
     }
+    // ---- its place in the cache, looked up while the rows come
+    const int index = base / p.page_size;
+    int page = -1;
+    if (index < p.max_pages) page = p.block_table[b * p.table_stride + index];
+    if (page < 0 || page >= p.num_pages) {
+        if (lane == 0) set_error(p.err, KT_DEVERR_BAD_PAGE);
+        return;
+    }
+    if (lo >= hi) return;
+    const int slot = base - index * p.page_size;
+    uint8_t* const scale_at =
+        sd.scales + (static_cast<long long>(page) * (p.page_size / kBlk) + slot / kBlk) * p.heads + h;
+    uint8_t* const block = sd.codes + page * sd.page + slot * sd.slot + h * sd.head;
+    const int older = lo - base;   // rows of the block that were there before
+    int exponent = p.least;
+    const int old_byte = older > 0 ? *scale_at : p.least + 127;
+
     uint64_t y[kPasses][2][kVec / 2];
     uint64_t w0[kVec / 2], w1[kVec / 2];
     const bool normed = NORM != kNoNorm && keys && p.weight != nullptr;   // the same for the whole warp
@@ -254,7 +255,7 @@ static cudaError_t launch_kv8_typed(const Kv8AppendParams& p, HeadRowsParams* q,
     const bool normed = p.weight != nullptr || (q != nullptr && q->seg[0].weight != nullptr);
     // Few query rows: one launch (48 single tokens of 64 + 8 heads of 128: 4.9 us in two, 3.3 in one).  Many: two, for
     // one row at a time and this kernel's registers leave too few loads under way (three prompts of up to 3500 tokens:
-    // 45 us in two, 83 in one).
+    // 43 us in two, 11 of them this kernel's, and 83 in one).
     if (q != nullptr && wide && static_cast<long long>(q->tokens) * q->seg[0].heads < 16384) {
         const unsigned rows = plan_head_rows<8, 1>(*q);
         count_launches(1);
