@@ -63,11 +63,12 @@ typedef struct kt_paged_kv {
  * k + p*k_page_stride + s*k_slot_stride + h*k_head_stride; an element stands for
  * e4m3(code) * 2^(scale - 127) with scale = k_scales[(p * page_size / KT_KV8_BLOCK +
  * s / KT_KV8_BLOCK) * heads + h] (e8m0; dense); a scale of 255 makes the whole block
- * NaN, the codes 0x7f and 0xff are not used otherwise.  page_size is a multiple of 16, head_dim a multiple of 16 up to 128; rows are 16-byte aligned,
- * strides positive multiples of 16 bytes.  dtype: the type of the keys, values and
- * queries that come in and of the output; kt_kv8_append keeps exponents with which
- * every element is a number of that type and attention's fp32 sums are finite
- * (2^-117 to 2^87 for bf16, 2^-14 to 2^7 for fp16): larger numbers saturate.
+ * NaN, the codes 0x7f and 0xff are not used otherwise.  page_size is a multiple of
+ * 16, head_dim a multiple of 16 up to 128; rows are 16-byte aligned, strides
+ * positive multiples of 16 bytes.  dtype: the type of the keys, values and queries
+ * that come in and of the output; kt_kv8_append keeps exponents with which every
+ * element is a number of that type and attention's fp32 sums are finite (2^-117 to
+ * 2^87 for bf16, 2^-14 to 2^7 for fp16): larger numbers saturate.
  */
 #define KT_KV8_BLOCK 16
 typedef struct kt_paged_kv8 {

@@ -465,7 +465,8 @@ class MoeLayer:
     only the step's own tensors are
     checked and marshalled; workspaces and routing buffers are kept per T.
     Results are those of route_permute + forward (or decode) with the same
-    options.  hidden: as forward's (MXFP8 pairs: not with single_launch).  Returns (out, topk_ids, topk_w); the three are reused by the
+    options.  hidden: as forward's (MXFP8 pairs: not with single_launch).
+    Returns (out, topk_ids, topk_w); the three are reused by the
     next call with the same T unless `out` is given."""
 
     def __init__(self, w13: torch.Tensor, w13_sf: torch.Tensor, w2: torch.Tensor, w2_sf: torch.Tensor, k: int,
@@ -514,9 +515,10 @@ class MoeLayer:
                 raise ValueError("a single launch quantises its tokens itself: hidden must be bf16")
             hidden, scales = _mx_tokens(hidden, self.H, -1, self.device)
         T = hidden.shape[0]
-        if ((scales is None and hidden.dtype != torch.bfloat16) or (logits.dtype != torch.float32 or hidden.shape != (T, self.H)
-                or logits.shape != (T, self.E) or hidden.get_device() != self._dev_idx
-                or logits.get_device() != self._dev_idx or not hidden.is_contiguous() or not logits.is_contiguous())):
+        if ((scales is None and hidden.dtype != torch.bfloat16) or logits.dtype != torch.float32
+                or hidden.shape != (T, self.H) or logits.shape != (T, self.E)
+                or hidden.get_device() != self._dev_idx or logits.get_device() != self._dev_idx
+                or not hidden.is_contiguous() or not logits.is_contiguous()):
             raise ValueError(f"hidden must be contiguous bf16 [T, {self.H}] and logits contiguous f32 [T, {self.E}] "
                              f"on {self.device}")
         decode, ws, route, rws, own_out = self._buffers(T)

@@ -455,10 +455,10 @@ class PagedKV8(PagedKV):
 
     dtype: of the keys, values and queries that come in and of the attention's output (bf16 or fp16).  `append` and
     `attend` are PagedKV's: `append` picks the powers (the least that hold the 16 positions' values, from 2^-117 to
-    2^87 for bf16 and from 2^-14 to 2^7 for fp16, past which values saturate at 448 times that; a block that has older tokens keeps its power or rescales their codes to a larger
-    one), and `attend` computes with the numbers that the cache stands for.  A rotation table's width is a multiple of
-    16, k and v are 16-byte aligned with strides that are multiples of 8.  A key or value element that is not finite
-    makes its 16 positions of that head NaN."""
+    2^87 for bf16 and from 2^-14 to 2^7 for fp16, past which values saturate at 448 times that; a block that has older
+    tokens keeps its power or rescales their codes to a larger one), and `attend` computes with the numbers that the
+    cache stands for.  A rotation table's width is a multiple of 16, k and v are 16-byte aligned with strides that are
+    multiples of 8.  A key or value element that is not finite makes its 16 positions of that head NaN."""
 
     BLOCK = 16   # KT_KV8_BLOCK
     _append, _attend = "kt_kv8_append", "kt_paged_attention8"

@@ -337,8 +337,8 @@ kt_status kt_mxfp4_moe_forward_ex(const uint16_t* hidden, int T, int H, const in
                                   const float* topk_w, int k, const uint8_t* w13, const uint8_t* w13_sf,
                                   const uint8_t* w2, const uint8_t* w2_sf, int E, int I, uint16_t* out, void* ws,
                                   size_t ws_bytes, const kt_moe_options* opts, void* stream) {
-    return forward_impl({hidden, nullptr, nullptr}, T, H, topk_ids, topk_w, k, false, nullptr, nullptr, nullptr, w13, w13_sf, w2, w2_sf,
-                        E, I, out, ws, ws_bytes, opts, stream);
+    return forward_impl({hidden, nullptr, nullptr}, T, H, topk_ids, topk_w, k, false, nullptr, nullptr, nullptr, w13,
+                        w13_sf, w2, w2_sf, E, I, out, ws, ws_bytes, opts, stream);
 }
 
 kt_status kt_mxfp4_moe_forward_routed(const uint16_t* hidden, int T, int H, const int32_t* topk_ids,

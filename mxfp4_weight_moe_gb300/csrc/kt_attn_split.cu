@@ -2,8 +2,9 @@
 // warp streams its own keys and values and keeps its own softmax state.
 //
 // An item is (sequence, cache head, 16 query rows; of an 8-bit cache 8 for calls of
-// up to 8 rows): row r of a sequence is its new token r / group under query head r % group of the cache head's group, so
-// the heads that share a cache head share its loads.  A warp takes blocks of 16
+// up to 8 rows): row r of a sequence is its new token r / group under query head
+// r % group of the cache head's group, so the heads that share a cache head share
+// its loads.  A warp takes blocks of 16
 // keys (32 for heads of up to 64: the same bytes), through a ring of TMA loads
 // of its own: no barrier among warps until the item's end.  S = Q K^T and P V
 // are mma.sync products of 16 rows: the operator is bound by reading the cache
@@ -100,9 +101,10 @@ __device__ __forceinline__ int split_row_tiles(const AttnShape& s, const SeqInfo
 }
 
 // The order of the CTAs.  A slot's heads lie side by side in memory, and a head's row of an 8-bit cache is 128 bytes at
-// most: read at different times, such rows come at 5.5 TB/s (64 single tokens after up to 16383, 8 heads of 128: 264 us),
-// where each head's slots follow one another at 6.7.  So there the runs are those of one head, and neighbouring CTAs
-// take the same run of neighbouring heads (234), unless there are so many heads that CTAs would be left over.
+// most: read at different times, such rows come at 5.5 TB/s (64 single tokens after up to 16383, 8 heads of 128:
+// 264 us), where each head's slots follow one another at 6.7.  So there the runs are those of one head, and
+// neighbouring CTAs take the same run of neighbouring heads (234), unless there are so many heads that CTAs would be
+// left over.
 struct SplitOrder {
     int runs;         // CTAs that share a line
     int heads;        // cache heads on a line
@@ -116,9 +118,9 @@ __device__ __forceinline__ SplitOrder split_order(const AttnShape& s) {
     return SplitOrder{ctas / s.kv_heads, 1, cta / s.kv_heads, cta % s.kv_heads, s.kv_heads, cta % s.kv_heads};
 }
 
-// How the items are dealt to the CTAs of a line.  Few items: each is cut into pieces of at most `piece` units, a CTA takes one
-// piece (piece > 0).  Many: they lie on a line, kSplitItemUnits before each one's units, that is cut into equal runs
-// (piece == 0).  In both, [begin, begin + per) of `total` are this CTA's, in pieces or in units of the line.
+// How the items are dealt to the CTAs of a line.  Few items: each is cut into pieces of at most `piece` units, a CTA
+// takes one piece (piece > 0).  Many: they lie on a line, kSplitItemUnits before each one's units, that is cut into
+// equal runs (piece == 0).  In both, [begin, begin + per) of `total` are this CTA's, in pieces or in units of the line.
 struct SplitPlan {
     long long total, per, begin;
     long long in_seq;   // begin's place in sequence seq
@@ -226,16 +228,17 @@ __device__ __forceinline__ SplitPlan split_plan(const AttnShape& s, const SplitO
 // Address of 16-byte piece `piece` of key `row` in 16 keys of an 8-bit block at `base`, as TMA's swizzle leaves it.
 template <int DP>
 __device__ __forceinline__ uint32_t piece8(uint32_t base, int row, int piece) {
-    return DP == 128 ? base + row * 128 + ((piece ^ (row & 7)) << 4) : base + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+    return DP == 128 ? base + row * 128 + ((piece ^ (row & 7)) << 4)
+                     : base + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
 }
 
 // KV8: the cache's elements are e4m3 codes with a power of two for 16 keys of a head.  The products are fp16 ones,
 // which e4m3 has a conversion to (bf16 has none: bits moved by hand take 2.2 instructions an element, and 265 us for 64
 // single tokens after up to 16383): codes go in without their powers, exact; bf16 queries times a power of two per row,
-// exact down to 2^-31 of the row's largest element and off by at most 2^-40 of that below; softmax weights, their
-// value's power included, relative to the largest of the row in the block's 32 or 64 keys, times 2^10: rounded to 11 bits
-// down to 2^-24 of that largest and off by at most 2^-35 of it below.  For fp16 results, which have as many bits, the
-// weights go in in two parts.
+// exact down to 2^-31 of the row's largest element and off by at most 2^-39 of that below; softmax weights, their
+// value's power included, relative to the largest of the row in the block's 32 or 64 keys, times 2^10: rounded to 11
+// bits down to 2^-24 of that largest and off by at most 2^-35 of it below.  For fp16 results, which have as many bits,
+// the weights go in in two parts.
 constexpr float kWeightLog2 = 10.0f;   // the largest weight of a block, log2; O stays multiplied by that to the end
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 // Codes 0 and 1 (in `lo`), 2 and 3 as pairs of fp16.
@@ -554,9 +557,10 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
             }
         }
         } else {
-        // ---- S^T = K Q^T and O^T += V^T P^T: keys and head elements are the products' 16 rows, query rows their columns,
-        // eight to a tile (a single token's rows under 8 heads: half the products and registers of rows as rows).  Lane (g, t) holds keys g and g + 8 and elements 2g and 2g + 1 of each 16 under the
-        // query rows 2t and 2t + 1.
+        // ---- S^T = K Q^T and O^T += V^T P^T: keys and head elements are the products' 16 rows, query rows their
+        // columns, eight to a tile (a single token's rows under 8 heads: half the products and registers of rows as
+        // rows).  Lane (g, t) holds keys g and g + 8 and elements 2g and 2g + 1 of each 16 under the query rows 2t and
+        // 2t + 1.
         constexpr int kTiles = ROWS / 8, kSub = Cfg::kSub;
         constexpr bool kHalf = std::is_same<T, __half>::value;
         constexpr int kParts = kHalf ? 2 : 1;       // of the weights
@@ -573,14 +577,15 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
 #pragma unroll
             for (int c = 0; c < DP / 16; ++c) {
                 const int d = c * 16 + t4 * 4;
-                raw[c] = n * 8 + g < rows && d < sh.head_dim ? *reinterpret_cast<const uint2*>(qp + d) : make_uint2(0, 0);
+                raw[c] = n * 8 + g < rows && d < sh.head_dim ? *reinterpret_cast<const uint2*>(qp + d)
+                                                             : make_uint2(0, 0);
                 top = max(top, max(max(magnitude(low_of<T>(raw[c].x)), magnitude(high_of<T>(raw[c].x))),
                                    max(magnitude(low_of<T>(raw[c].y)), magnitude(high_of<T>(raw[c].y)))));
             }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // times 2^a the largest is 2^14 to 2^15 (a up to 126, for rows of next to nothing); the scores' factor back is
-            // NaN for a row that is not finite
+            // times 2^a the largest is 2^14 to 2^15 (a up to 126, for rows of next to nothing); the scores' factor back
+            // is NaN for a row that is not finite
             const int a = kHalf ? 0 : max(min(141 - static_cast<int>(top >> 23), 126), -113);
             const float up = __uint_as_float(static_cast<uint32_t>(a + 127) << 23);
             const float back = !kHalf && top >= 0x7f800000u
@@ -763,7 +768,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
                         for (int sub = 0; sub < kSub; ++sub)
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
-                                mma_16816<__half>(y[k], a[sub][k], pw[n][sub][kParts - 1][0], pw[n][sub][kParts - 1][1]);
+                                mma_16816<__half>(y[k], a[sub][k], pw[n][sub][kParts - 1][0],
+                                                  pw[n][sub][kParts - 1][1]);
                     }
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
@@ -850,8 +856,8 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
             for (int k = 0; k < Cfg::kParts; ++k)
                 if (part_row(k) < rows) store(part_row(k), acc[k], ml[k]);
         } else {
-            // The item's pieces lie with the CTAs of runs c0 .. c0 + n - 1.  On the line, the first is its CTA's last piece (slot
-            // 1), the others their CTAs' first (slot 0).
+            // The item's pieces lie with the CTAs of runs c0 .. c0 + n - 1.  On the line, the first is its CTA's last
+            // piece (slot 1), the others their CTAs' first (slot 0).
             int c0, n;
             if (plan.piece > 0) {
                 n = pieces_of(it.units, plan.piece);
@@ -955,7 +961,8 @@ static int split_ctas() {
 }
 
 size_t attn_split_workspace_bytes() {
-    const size_t c = static_cast<size_t>(std::max(split_ctas<SplitCfg<128, false, 16>>(), split_ctas<SplitCfg<64, true, 8>>()));
+    const size_t c =
+        static_cast<size_t>(std::max(split_ctas<SplitCfg<128, false, 16>>(), split_ctas<SplitCfg<64, true, 8>>()));
     return c * 2 * 16 * (128 + 2) * sizeof(float);
 }
 
@@ -965,7 +972,8 @@ static kt_status launch_split_typed(const AttnArgs& a, cudaStream_t s) {
     CUtensorMap kmap, vmap;
     auto encode = [&](CUtensorMap* m, bool values) {
         const CUtensorMapSwizzle swizzle = DP == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
-        return KV8 ? encode_kv8_map(m, a.kv, values, DP, kSplitKeys, swizzle) : encode_kv_map(m, a.kv, values, kSplitKeys);
+        return KV8 ? encode_kv8_map(m, a.kv, values, DP, kSplitKeys, swizzle)
+                   : encode_kv_map(m, a.kv, values, kSplitKeys);
     };
     if (!encode(&kmap, false) || !encode(&vmap, true))
         return report(KT_ERR_CUDA, "tensor map encoding failed");
@@ -991,21 +999,23 @@ static kt_status launch_split_typed(const AttnArgs& a, cudaStream_t s) {
     p.part_o = reinterpret_cast<float4*>(a.ws);
     p.part_ml = reinterpret_cast<float2*>(p.part_o + c * 2 * Cfg::kRows * 32);
     count_launches(1);
-    return cuda_status(launch_chained(attn_split_kernel<T, DP, KV8, ROWS>, dim3(static_cast<unsigned>(c)), dim3(kSplitThreads),
-                                      Cfg::kSmem, s, static_cast<const SplitParams&>(p),
+    return cuda_status(launch_chained(attn_split_kernel<T, DP, KV8, ROWS>, dim3(static_cast<unsigned>(c)),
+                                      dim3(kSplitThreads), Cfg::kSmem, s, static_cast<const SplitParams&>(p),
                                       static_cast<const CUtensorMap&>(kmap), static_cast<const CUtensorMap&>(vmap)));
 }
 
 template <typename T>
 static kt_status launch_split_of(const AttnArgs& a, int rows, cudaStream_t s) {
     const bool wide = a.kv.head_dim > 64;
-    if (a.k_scales == nullptr) return wide ? launch_split_typed<T, 128, false, 16>(a, s) : launch_split_typed<T, 64, false, 16>(a, s);
+    if (a.k_scales == nullptr)
+        return wide ? launch_split_typed<T, 128, false, 16>(a, s) : launch_split_typed<T, 64, false, 16>(a, s);
     if (rows <= 8) return wide ? launch_split_typed<T, 128, true, 8>(a, s) : launch_split_typed<T, 64, true, 8>(a, s);
     return wide ? launch_split_typed<T, 128, true, 16>(a, s) : launch_split_typed<T, 64, true, 16>(a, s);
 }
 
 kt_status launch_attn_split(const AttnArgs& a, int rows, cudaStream_t s) {
-    return a.kv.dtype == KT_DTYPE_BF16 ? launch_split_of<__nv_bfloat16>(a, rows, s) : launch_split_of<__half>(a, rows, s);
+    return a.kv.dtype == KT_DTYPE_BF16 ? launch_split_of<__nv_bfloat16>(a, rows, s)
+                                       : launch_split_of<__half>(a, rows, s);
 }
 
 }  // namespace kt

@@ -94,11 +94,11 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
     """s = x + residual and y = s * weight / sqrt(mean(s^2) + eps) of each token, in one launch; returns
     (y, s, (codes, scales)).
 
-    x, residual: bf16 or fp16 [tokens, hidden], rows by any stride that is a multiple of 8; weight [hidden] of their type
-    or float32; all 16-byte aligned.  y is
-    there with `plain` (x's type; None without), s with a residual (x's type), the pair with `mx`: y in MXFP8, codes
-    uint8 e4m3 [tokens, hidden] and scales uint8 e8m0 [tokens, hidden / 32], as forward and MoeLayer take them in place
-    of bf16 tokens (rounded once, from the fp32 y).  hidden: a multiple of 8 (of 32 with mx) up to 32768.
+    x, residual: bf16 or fp16 [tokens, hidden], rows by any stride that is a multiple of 8; weight [hidden] of their
+    type or float32; all 16-byte aligned.  y is there with `plain` (x's type; None without), s with a residual (x's
+    type), the pair with `mx`: y in MXFP8, codes uint8 e4m3 [tokens, hidden] and scales uint8 e8m0 [tokens,
+    hidden / 32], as forward and MoeLayer take them in place of bf16 tokens (rounded once, from the fp32 y).  hidden: a
+    multiple of 8 (of 32 with mx) up to 32768.  Squares are summed in fp32: where their sum passes 3.4e38, y is zeros.
 
     out and residual_out may be x or residual; they share no memory otherwise."""
     if not isinstance(x, torch.Tensor) or x.dtype not in _a.DTYPE_CODES or x.dim() != 2:
