@@ -196,9 +196,10 @@ kt_status kt_paged_attention(const kt_paged_kv* cache, const kt_paged_batch* bat
  * them; the same workspace and arguments.  Where a call has few query rows
  * (max_q_len x group up to 32) queries and softmax weights go into fp16 products:
  * bf16 queries relative to their row's largest element (exact down to 2^-31 of
- * it), the weights rounded to 11 bits relative to the largest, its value's power
- * included, of 32 to 64 neighbouring keys (in two parts for fp16 outputs).  Chunks
- * of more round the weights to the element type, once.
+ * it), the weights relative to the largest, its value's power included, of 32 to 64
+ * neighbouring keys: rounded to 11 bits down to 2^-24 of it, off by at most 2^-35 of
+ * it below (in two parts for fp16 outputs).  Chunks of more round the weights to the
+ * element type, once.
  */
 kt_status kt_paged_attention8(const kt_paged_kv8* cache, const kt_paged_batch* batch, const kt_heads* q,
                               const kt_heads* out, int max_q_len, float scale, int window, const float* sinks,

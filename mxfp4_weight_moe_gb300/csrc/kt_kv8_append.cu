@@ -9,8 +9,7 @@
 // from the loads to the codes.  Bound by memory (large steps) or by the chain of
 // look-ups, cu_q -> block table -> old scale (decode steps).
 //
-// The step's queries go through the head-row kernel's code: in the same launch where
-// there are few of them, whose time is that of launches.
+// The step's queries go through the head-row kernel's code, in the same launch.
 #include <algorithm>
 
 #include "kt_head_rows_dev.cuh"
@@ -237,33 +236,44 @@ __global__ void __launch_bounds__(kAppendThreads, 5) kv8_append_kernel(const Kv8
     griddep_launch_dependents();
     kv8_append_block<T, NORM>(p, blockIdx.x);
 }
-// The same and the queries: blocks from `blocks` on are the head rows'.
-template <typename T, int NORM>
-__global__ void __launch_bounds__(kAppendThreads)
+// The same and the queries, R rows a group: blocks from `blocks` on are the head rows'.  Keys and values come first:
+// their chains are the longer ones (three prompts, below: 40.3 us; last, 41.6; among the queries' blocks, 41.1).
+template <typename T, int NORM, int R, bool STREAM>
+__global__ void __launch_bounds__(kAppendThreads, R > 1 ? 5 : 1)
     kv8_append_queries_kernel(const Kv8AppendParams p, const HeadRowsParams q, unsigned blocks) {
     static_assert(kAppendThreads == kRowThreads, "one launch");
     griddep_wait();
     griddep_launch_dependents();
     if (blockIdx.x < blocks) kv8_append_block<T, NORM>(p, blockIdx.x);
-    else head_rows_block<T, 8, 1, NORM, false>(q, blockIdx.x - blocks);
+    else head_rows_block<T, 8, R, NORM, STREAM>(q, blockIdx.x - blocks);
+}
+
+template <typename T, int R, bool STREAM>
+static cudaError_t launch_kv8_queries(const Kv8AppendParams& p, HeadRowsParams& q, unsigned blocks, cudaStream_t s) {
+    const unsigned rows = plan_head_rows<8, R>(q);
+    const bool normed = p.weight != nullptr || q.seg[0].weight != nullptr;
+    count_launches(1);
+    return launch_chained(!normed          ? kv8_append_queries_kernel<T, kNoNorm, R, STREAM>
+                          : p.weight_f32   ? kv8_append_queries_kernel<T, kWeightsF32, R, STREAM>
+                                           : kv8_append_queries_kernel<T, kWeightsTyped, R, STREAM>,
+                          dim3(blocks + rows), dim3(kAppendThreads), 0, s, p, static_cast<const HeadRowsParams&>(q),
+                          blocks);
 }
 
 template <typename T>
 static cudaError_t launch_kv8_typed(const Kv8AppendParams& p, HeadRowsParams* q, bool wide, int dtype, cudaStream_t s) {
     const unsigned blocks = static_cast<unsigned>(first_block(p.tokens, p.seqs)) *
                             static_cast<unsigned>((2 * p.heads + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
-    const bool normed = p.weight != nullptr || (q != nullptr && q->seg[0].weight != nullptr);
-    // Few query rows: one launch (48 single tokens of 64 + 8 heads of 128: 4.9 us in two, 3.3 in one).  Many: two, for
-    // one row at a time and this kernel's registers leave too few loads under way (three prompts of up to 3500 tokens:
-    // 43 us in two, 11 of them this kernel's, and 83 in one).
-    if (q != nullptr && wide && static_cast<long long>(q->tokens) * q->seg[0].heads < 16384) {
-        const unsigned rows = plan_head_rows<8, 1>(*q);
-        count_launches(1);
-        return launch_chained(!normed          ? kv8_append_queries_kernel<T, kNoNorm>
-                              : p.weight_f32   ? kv8_append_queries_kernel<T, kWeightsF32>
-                                               : kv8_append_queries_kernel<T, kWeightsTyped>,
-                              dim3(blocks + rows), dim3(kAppendThreads), 0, s, p, static_cast<const HeadRowsParams&>(*q),
-                              blocks);
+    if (q != nullptr && wide) {
+        // One row at a time where there are few, four for the loads under way where there are many (128 tokens of
+        // 64 + 8 heads of 128: 4.16 us one at a time, 3.66 four, with norms 4.2 and 4.6; 250 tokens: 4.2 and 3.9, with
+        // norms 5.5 and 4.9; three prompts of up to 3500 with norms: 83 and 40.3).  Many are marked to leave L2 first,
+        // as in the head-row kernel's launcher.  In a launch of their own the prompts' take 43.5 us, those of 48 single
+        // tokens 4.9, 3.3 here.
+        const long long rows = static_cast<long long>(q->tokens) * q->seg[0].heads;
+        if (rows < 12288) return launch_kv8_queries<T, 1, false>(p, *q, blocks, s);
+        if (rows * q->head_dim * 4 > (128ll << 20)) return launch_kv8_queries<T, 4, true>(p, *q, blocks, s);
+        return launch_kv8_queries<T, 4, false>(p, *q, blocks, s);
     }
     count_launches(1);
     const cudaError_t e = launch_chained(!p.weight        ? kv8_append_kernel<T, kNoNorm>

@@ -254,6 +254,31 @@ def test_streams_and_graph():
     assert cache.append(*args, q=q_in, q_weight=w, k_weight=w, q_out=q_in) is q_in and torch.equal(q_in, want_q)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_many_queries(dtype):
+    _run(dtype, [150, 0, 181], [5, 3, 40], 40, 2, 96, 64, "interleaved", 48, True)
+    _run(dtype, [320], [0], 64, 1, 48, 48, "halves", 16, False)
+
+
+@pytest.mark.parametrize("norm", [None, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,hq,d", [(9, 8, 64), (400, 40, 80), (4200, 64, 128)])
+def test_queries_beside_keys_and_values(norm, n, hq, d):
+    """One launch for all writes what a launch for the queries and one for the rest do, at every number of queries."""
+    hk, page, past, dt = 2, 16, 21, torch.bfloat16
+    kp, vp, ks, vs, table, _, _ = M.paged8([n + past], page, hk, d, dt, DEV, 3)
+    made = [kp, vp, ks, vs]
+    twice = [t.clone() for t in made]
+    q, k, v = _rand(n, hq + 2 * hk, d, dtype=dt, seed=1).split((hq, hk, hk), dim=1)
+    wq, wk = (None if norm is None else _rand(d, dtype=norm, seed=i) for i in (2, 3))
+    cs = kt.rope_table(n + past, d)
+    step = table, R.starts([n], DEV), _i32([n + past]), cs
+    got = kt.PagedKV8(*made, dt).append(k, v, *step, q=q, q_weight=wq, k_weight=wk)
+    kt.PagedKV8(*twice, dt).append(k, v, *step, k_weight=wk)
+    want, _ = kt.qk_norm_rope(q, None, torch.arange(past, past + n, dtype=torch.int32, device=DEV), cs, q_weight=wq)
+    assert torch.equal(got, want)
+    assert all(torch.equal(a, b) for a, b in zip(made, twice))
+
+
 def test_empty_step():
     kp, vp, ks, vs, table, _, _ = M.paged8([5], 16, 1, 32, torch.bfloat16, DEV, 3)
     before = _state(kp, ks)

@@ -144,6 +144,31 @@ def test_every_code_and_power(dtype, q_lens, past):
         _near(out, want, bound + 2.0 ** -126 * (dtype == torch.bfloat16))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("new", [1, 20])
+def test_weights_far_below_the_largest(dtype, new):
+    """One key outweighs its neighbours by up to 2^190, and half its value's elements are zeros.
+
+    A weight, relative to the largest of its block, is an fp16 number times 2^-10 (times 2^-24 of rounding below fp16's
+    smallest normal one): off by at most 2^-35 of the largest, which is at most 1, times its value."""
+    hk, d, page, n = 1, 64, 16, 60
+
+    def rows(b):
+        k, v = torch.zeros(n, hk, d, dtype=torch.float64), torch.ones(n, hk, d, dtype=torch.float64)
+        k[:, 0, 0] = -torch.arange(n).double() / 4                # e4m3 keeps four bits of these
+        k[0] = 0
+        k[1:, 0, 0] -= 1.75
+        v[0, 0, ::2] = 0
+        return k, v
+
+    kp, vp, ks, vs, table, k, v = M.paged8([n], page, hk, d, dtype, DEV, 1, rows=rows)
+    q = torch.zeros(new, 4, d, dtype=dtype, device=DEV)
+    q[:, :, 0] = torch.tensor([1.0, 2.0, 4.0, 8.0])
+    out = kt.PagedKV8(kp, vp, ks, vs, dtype).attend(q, table, R.starts([new], DEV), _i32([n]), new, scale=1.0)
+    want, bound = R.attend(q, k, v, table, [new], [n], 1.0)
+    _near(out, want, bound + 2.0 ** -35 * n)
+
+
 @pytest.mark.parametrize("q_lens,lens", [([3, 1, 2], [1, 0, 2]), ([150, 2], [140, 0])])
 def test_tokens_that_see_nothing(q_lens, lens):
     d, page = 64, 16
