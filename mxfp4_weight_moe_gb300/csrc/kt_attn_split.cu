@@ -238,7 +238,8 @@ __device__ __forceinline__ uint32_t piece8(uint32_t base, int row, int piece) {
 // exact down to 2^-31 of the row's largest element and off by at most 2^-39 of that below; softmax weights, their
 // value's power included, relative to the largest of the row in the block's 32 or 64 keys, times 2^10: rounded to 11
 // bits down to 2^-24 of that largest and off by at most 2^-35 of it below.  For fp16 results, which have as many bits,
-// the weights go in in two parts.
+// the weights go in in two parts (error 1.00 times that of rounding the result once; in one part up to 1.40, for 5 of
+// 67 us of 4 tokens after up to 131071 under heads of 64).
 constexpr float kWeightLog2 = 10.0f;   // the largest weight of a block, log2; O stays multiplied by that to the end
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 // Codes 0 and 1 (in `lo`), 2 and 3 as pairs of fp16.
