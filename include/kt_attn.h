@@ -199,7 +199,8 @@ kt_status kt_paged_attention(const kt_paged_kv* cache, const kt_paged_batch* bat
  * it), the weights relative to the largest, its value's power included, of 32 to 64
  * neighbouring keys: rounded to 11 bits down to 2^-24 of it, off by at most 2^-35 of
  * it below (in two parts for fp16 outputs).  Chunks of more round the weights to the
- * element type, once.
+ * element type, once.  A block of scale 255 makes what sees one of its keys NaN, and,
+ * if it holds values, in chunks of more also tokens that share a tile with those.
  */
 kt_status kt_paged_attention8(const kt_paged_kv8* cache, const kt_paged_batch* batch, const kt_heads* q,
                               const kt_heads* out, int max_q_len, float scale, int window, const float* sinks,

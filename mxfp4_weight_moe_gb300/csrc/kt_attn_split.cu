@@ -651,13 +651,17 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
                 last_all = min(last_all, last_key[c / 2][c % 2]);
             }
             const bool masked = __any_sync(0xffffffffu, last_all < key0 + Cfg::kBlockKeys - 1 || first_all > key0);
+            // Values of scale 255 are NaN to the rows that see a key of their 16, by those rows' sums of weights; in the
+            // products they are zeros under the least power, so that no other row meets them.
             uint32_t scales[kSub];
             float v_exp[kSub];   // the values' exponents
+            bool nan_values = false;
 #pragma unroll
             for (int sub = 0; sub < kSub; ++sub) {
                 scales[sub] = s_scales[warp][st][sub];
                 const int byte = static_cast<int>(scales[sub] >> 8);
-                v_exp[sub] = byte == 255 ? __uint_as_float(0x7fc00000u) : static_cast<float>(byte - 127);
+                nan_values = nan_values || byte == 255;
+                v_exp[sub] = static_cast<float>((byte == 255 ? 0 : byte) - 127);
             }
             uint32_t pw[kTiles][kSub][kParts][2];   // [16 keys][part][keys 0-7, 8-15]
             float share[kTiles][2];   // what a row's sums over this block are to be multiplied by
@@ -690,14 +694,11 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
                     const float scale = ex2(m[n][e] - base_m);
                     m[n][e] = mn;
                     // The largest weight times its value's power: the block's weights, powers included, are taken as
-                    // multiples of it, so that they use fp16's range whatever the blocks' powers are.  (A sum, not
-                    // fmaxf: NaN stays.)
+                    // multiples of it, so that they use fp16's range whatever the blocks' powers are.  (Scores that are
+                    // NaN, which fmaxf passes over, are in the row's sum of weights.)
                     float ref = top[0] + v_exp[0];
 #pragma unroll
-                    for (int sub = 1; sub < kSub; ++sub) {
-                        const float r = top[sub] + v_exp[sub];
-                        ref = ref >= r || ref != ref ? ref : r;
-                    }
+                    for (int sub = 1; sub < kSub; ++sub) ref = fmaxf(ref, top[sub] + v_exp[sub]);
                     const float base_r = ref == -INFINITY ? 0.0f : ref;
                     share[n][e] = ex2(ref - base_m);
                     float sum = 0.0f;
@@ -708,6 +709,11 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
                             sum += ex2(x[sub][f] - base_m);
                             x[sub][f] = ex2(x[sub][f] + (v_exp[sub] - base_r + kWeightLog2));
                         }
+                    if (nan_values) {
+#pragma unroll
+                        for (int sub = 0; sub < kSub; ++sub)
+                            if (scales[sub] >> 8 == 255 && top[sub] != -INFINITY) sum = __uint_as_float(0x7fc00000u);
+                    }
                     l[n][e] = l[n][e] * scale + sum;
                     if (__any_sync(0xffffffffu, scale != 1.0f)) {
 #pragma unroll
@@ -729,9 +735,9 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
                                 transpose_8x8(pack2<__half>(lo - low_of<__half>(w), hi - high_of<__half>(w)));
                     }
             }
-            // ---- O^T += V^T P^T; value rows that no token sees are not multiplied (0 x NaN)
+            // ---- O^T += V^T P^T; value rows that no token sees, or that are NaN, are not multiplied (0 x NaN)
             const int vrow = (lane & 7) + (((lane >> 3) & 1) << 3);
-            const bool ragged = key0 + Cfg::kBlockKeys > it.hi || key0 < it.lo;
+            const bool ragged = nan_values || key0 + Cfg::kBlockKeys > it.hi || key0 < it.lo;
 #pragma unroll
             for (int c = 0; c < DP / 16; c += 2) {
                 uint32_t a[kSub][2][4];   // [16 keys][16 elements]
@@ -745,6 +751,7 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
                             const int key = key0 + sub * kSplitKeys + t4 * 2 + (f & 1) * 8;
                             if (key >= it.hi || key < it.lo) vf[f] &= 0xffff0000u;
                             if (key + 1 >= it.hi || key + 1 < it.lo) vf[f] &= 0x0000ffffu;
+                            if (scales[sub] >> 8 == 255) vf[f] = 0;
                         }
                     }
                     // keys 2t and 2t + 1 of element 2g, of element 2g + 1
