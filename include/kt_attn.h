@@ -197,8 +197,8 @@ kt_status kt_paged_attention(const kt_paged_kv* cache, const kt_paged_batch* bat
  * (max_q_len x group up to 32) queries and softmax weights go into fp16 products:
  * bf16 queries relative to their row's largest element (exact down to 2^-31 of
  * it), the weights relative to the largest, its value's power included, of 32 to 64
- * neighbouring keys: rounded to 11 bits down to 2^-24 of it, off by at most 2^-35 of
- * it below (in two parts for fp16 outputs).  Chunks of more round the weights to the
+ * neighbouring keys, or to 2^-125 if that is more: rounded to 11 bits down to 2^-24 of
+ * it, off by at most 2^-35 of it below (in two parts for fp16 outputs).  Chunks of more round the weights to the
  * element type, once.  A block of scale 255 makes what sees one of its keys NaN, and,
  * if it holds values, in chunks of more also tokens that share a tile with those.
  */

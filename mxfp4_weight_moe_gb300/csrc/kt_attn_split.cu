@@ -241,6 +241,7 @@ __device__ __forceinline__ uint32_t piece8(uint32_t base, int row, int piece) {
 // the weights go in in two parts (error 1.00 times that of rounding the result once; in one part up to 1.40, for 5 of
 // 67 us of 4 tokens after up to 131071 under heads of 64).
 constexpr float kWeightLog2 = 10.0f;   // the largest weight of a block, log2; O stays multiplied by that to the end
+constexpr float kLeastShareLog2 = -125.0f;   // (a unit above what ex2 flushes)
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 // Codes 0 and 1 (in `lo`), 2 and 3 as pairs of fp16.
 __device__ __forceinline__ void widen_e4m3(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -693,21 +694,23 @@ __global__ void __launch_bounds__(kSplitThreads, SplitCfg<DP, KV8, ROWS>::kCtasP
                     const float base_m = mn == -INFINITY ? 0.0f : mn;
                     const float scale = ex2(m[n][e] - base_m);
                     m[n][e] = mn;
-                    // The largest weight times its value's power: the block's weights, powers included, are taken as
-                    // multiples of it, so that they use fp16's range whatever the blocks' powers are.  (Scores that are
+                    // The largest weight times its value's power, relative to the maximum: the block's weights, powers
+                    // included, are taken as multiples of it, so that they use fp16's range whatever the blocks' powers
+                    // are.  What ex2 would flush (below 2^-126) stays with the weights, which have room for it: at the
+                    // least power, 2^-117, a block's largest weight keeps its 11 bits down to 2^-32.  (Scores that are
                     // NaN, which fmaxf passes over, are in the row's sum of weights.)
-                    float ref = top[0] + v_exp[0];
+                    float ref = kLeastShareLog2;
 #pragma unroll
-                    for (int sub = 1; sub < kSub; ++sub) ref = fmaxf(ref, top[sub] + v_exp[sub]);
-                    const float base_r = ref == -INFINITY ? 0.0f : ref;
-                    share[n][e] = ex2(ref - base_m);
+                    for (int sub = 0; sub < kSub; ++sub) ref = fmaxf(ref, top[sub] - base_m + v_exp[sub]);
+                    share[n][e] = ex2(ref);
                     float sum = 0.0f;
 #pragma unroll
                     for (int sub = 0; sub < kSub; ++sub)
 #pragma unroll
                         for (int f = e; f < 4; f += 2) {
-                            sum += ex2(x[sub][f] - base_m);
-                            x[sub][f] = ex2(x[sub][f] + (v_exp[sub] - base_r + kWeightLog2));
+                            const float d = x[sub][f] - base_m;
+                            sum += ex2(d);
+                            x[sub][f] = ex2(d + (v_exp[sub] - ref + kWeightLog2));
                         }
                     if (nan_values) {
 #pragma unroll
