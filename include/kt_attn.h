@@ -151,10 +151,11 @@ kt_status kt_kv_append(const kt_paged_kv* cache, const kt_paged_batch* batch, co
  * each head, keys and values by themselves, the exponent X is the least with
  * amax <= 448 * 2^X over the new tokens (fp32 keys after norm and rotation), within
  * the cache dtype's range; codes are x * 2^-X rounded once to nearest even,
- * saturating.  A block that has older tokens keeps its exponent if that is larger;
- * if X is, its older codes are rescaled (exact but for numbers that become e4m3
- * subnormals, which round).  An element that is not finite makes its block NaN (scale
- * 255), until the block is begun anew.  No two sequences of a step append to one block.
+ * saturating.  A block that has older tokens keeps its exponent if that is larger (one
+ * past the dtype's range as well, where another program wrote it); if X is, its older
+ * codes are rescaled (exact but for numbers that become e4m3 subnormals, which round).
+ * An element that is not finite makes its block NaN (scale 255), until the block is
+ * begun anew.  No two sequences of a step append to one block.
  * rotary_dim is a multiple of 16; k, v: 16-byte aligned, strides multiples of 8
  * elements; otherwise as kt_kv_append.
  */

@@ -43,7 +43,10 @@ __device__ __forceinline__ int sequence_of_block(const Kv8AppendParams& p, long 
     return lo;
 }
 
-__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+// e from -127 (a subnormal number) to 127.
+__device__ __forceinline__ float power_of_two(int e) {
+    return __uint_as_float(e < -126 ? 1u << 22 : static_cast<uint32_t>(e + 127) << 23);
+}
 
 // Four codes times 2^-shift, rounded again.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float factor) {
@@ -192,8 +195,10 @@ __device__ __forceinline__ void kv8_append_block(const Kv8AppendParams& p, unsig
     odd = __any_sync(0xffffffffu, odd);
     // least X with top <= 448 * 2^X = 1.75 * 2^(X + 8): a mantissa past 1.75 carries into the exponent
     if (top > 0) exponent = static_cast<int>((top + 0x1fffffu) >> 23) - 127 - 8;
+    // A larger power that older tokens have is kept, one past p.most (another program's) as well: their codes mean it.
     const int old_exponent = old_byte - 127;
-    exponent = min(max(max(exponent, old_exponent), p.least), p.most);
+    if (old_byte == 255) exponent = p.most;
+    else exponent = max(min(max(exponent, p.least), p.most), old_exponent);
     // a block with an element that is not finite is NaN as a whole, and stays so while it fills
     const int byte = odd || old_byte == 255 ? 255 : exponent + 127;
     if (lane == 0 && (older == 0 || byte != old_byte)) *scale_at = static_cast<uint8_t>(byte);
