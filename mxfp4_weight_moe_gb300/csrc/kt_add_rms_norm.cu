@@ -49,9 +49,13 @@ __device__ __forceinline__ uint4 narrow8(const float (&v)[8]) {
 constexpr int kSmallRows = 4;   // rows a block where a row is one warp's
 
 // CHUNKS chunks of 8 elements a thread; a row is a block's (as many warps as it takes), or a warp's (SMALL).
+//
+// A row's squares are summed in an order that its length alone decides, so that a token's bits do not depend on how
+// many others are in the step.  Of a block's row: the eight of a chunk; the chunks of each group of 32 neighbouring
+// ones, which a warp holds in both forms, by a butterfly; the groups i, i + 32, .. by lane i; the lanes by a butterfly.
 template <typename T, int CHUNKS, bool SMALL>
 __global__ void __launch_bounds__(SMALL ? kSmallRows * 32 : 1024) add_rms_norm_kernel(const NormParams p) {
-    __shared__ float s_sum[32];
+    __shared__ float s_sum[32 * CHUNKS];   // of the groups of chunks
     griddep_wait();
     griddep_launch_dependents();
     const int kThreads = SMALL ? 32 : static_cast<int>(blockDim.x);   // of a row
@@ -73,24 +77,36 @@ __global__ void __launch_bounds__(SMALL ? kSmallRows * 32 : 1024) add_rms_norm_k
         }
     }
     float s[CHUNKS][8];
-    float sum = 0.0f;
+    constexpr int kSums = SMALL ? 1 : CHUNKS;
+    float sums[kSums] = {};
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
         float b[8];
         widen8<T>(rx[c], s[c]);
         widen8<T>(rr[c], b);
+        float& q = sums[c % kSums];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             s[c][i] += b[i];
-            sum = fmaf(s[c][i], s[c][i], sum);
+            q = fmaf(s[c][i], s[c][i], q);
         }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int c = 0; c < kSums; ++c) sums[c] += __shfl_xor_sync(0xffffffffu, sums[c], o);
+    float sum = sums[0];
     if (!SMALL) {
-        if ((tid & 31) == 0) s_sum[tid >> 5] = sum;
+        const int warps = kThreads / 32, groups = warps * CHUNKS;
+        if ((tid & 31) == 0) {
+#pragma unroll
+            for (int c = 0; c < kSums; ++c) s_sum[(tid >> 5) + c * warps] = sums[c];
+        }
         __syncthreads();
-        sum = (tid & 31) < kThreads / 32 ? s_sum[tid & 31] : 0.0f;
+        sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+            if ((tid & 31) + 32 * c < groups) sum += s_sum[(tid & 31) + 32 * c];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
