@@ -110,10 +110,11 @@ __global__ void __launch_bounds__(SMALL ? kSmallRows * 32 : 1024) add_rms_norm_k
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
-    // the root to half a unit: its error would move every rounding of the row the same way
+    // The root to half a unit, by a Newton-Raphson step on 1 / r^2 - v (r + r (1 - v r^2) / 2): its error would move every
+    // rounding of the row the same way.  Roots of 0 and of infinity are as they are: the step would make them NaN.
     const float v = sum / static_cast<float>(p.hidden) + p.eps;
     const float near = rsqrtf(v);
-    const float inv = v > 1e-30f && v < 1e30f ? fmaf(0.5f * near, fmaf(-v * near, near, 1.0f), near) : near;
+    const float inv = v > 0.0f && v < INFINITY ? fmaf(0.5f * near, fmaf(-v * near, near, 1.0f), near) : near;
     if (!row) return;   // a whole warp
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
