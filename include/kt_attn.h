@@ -155,9 +155,11 @@ kt_status kt_kv_append(const kt_paged_kv* cache, const kt_paged_batch* batch, co
  * past the dtype's range as well, where another program wrote it); if X is, its older
  * codes are rescaled (exact but for numbers that become e4m3 subnormals, which round).
  * An element that is not finite makes its block NaN (scale 255), until the block is
- * begun anew.  No two sequences of a step append to one block.
+ * begun anew: a caller that takes such a token back (a rejected draft) appends the
+ * block's older tokens again.  No two sequences of a step append to one block.
  * rotary_dim is a multiple of 16; k, v: 16-byte aligned, strides multiples of 8
- * elements; otherwise as kt_kv_append.
+ * elements; otherwise as kt_kv_append.  One launch, or two where q or q_out is not
+ * 16-byte aligned or has a stride that is no multiple of 8.
  */
 kt_status kt_kv8_append(const kt_paged_kv8* cache, const kt_paged_batch* batch, const kt_heads* k, const kt_heads* v,
                         const kt_heads* q, const kt_heads* q_out, const kt_head_transform* transform, int* err,

@@ -35,7 +35,8 @@ typedef struct kt_token_rows {
  *                 rounded to nearest even, saturating), from the fp32 y
  * Any output may be NULL, but not all.  A token's bits do not depend on the call's
  * other tokens.  The sums are fp32, of the unrounded s: a token whose squares' sum
- * passes fp32's range (3.4e38) has zeros for y.
+ * passes fp32's range (3.4e38) has zeros for y, and with eps 0 one whose squares
+ * vanish below that range has no finite y.
  * dtype KT_DTYPE_BF16 or KT_DTYPE_FP16; weight [hidden] of dtype or KT_DTYPE_F32.
  * hidden: a multiple of 8 (of 32 for codes) up to KT_NORM_MAX_HIDDEN.  Pointers of
  * rows, weight and codes are 16-byte aligned, strides multiples of 8 elements.

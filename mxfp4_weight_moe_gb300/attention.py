@@ -458,9 +458,10 @@ class PagedKV8(PagedKV):
     2^87 for bf16 and from 2^-14 to 2^7 for fp16, past which values saturate at 448 times that; a block that has older
     tokens keeps its power or rescales their codes to a larger one), and `attend` computes with the numbers that the
     cache stands for.  A rotation table's width is a multiple of 16, k and v are 16-byte aligned with strides that are
-    multiples of 8.  A key or value element that is not finite makes its 16 positions of that head NaN: what sees one of
-    them is NaN.  Values that are NaN reach other tokens of the sequence (attend) only in calls of more than 32 query
-    rows, max_q_len times the query heads of a cache head."""
+    multiples of 8 (queries that are not so have a launch of their own).  A key or value element that is not finite
+    makes its 16 positions of that head NaN, until the first of them is appended anew (taking the token back does not
+    bring the older ones back): what sees one of them is NaN.  Values that are NaN reach other tokens of the sequence
+    (attend) only in calls of more than 32 query rows, max_q_len times the query heads of a cache head."""
 
     BLOCK = 16   # KT_KV8_BLOCK
     _append, _attend = "kt_kv8_append", "kt_paged_attention8"

@@ -412,10 +412,13 @@ static kt_status attention_impl(const kt_paged_kv* cache, const uint8_t* k_scale
                       kt_paged_attention_workspace_bytes());
     AttnArgs a{*cache, k_scales, v_scales, *batch, *q, *out, scale, window, sinks, err, static_cast<unsigned*>(ws),
                static_cast<uint8_t*>(ws) + KT_PAGED_ATTENTION_ZEROED};
-    // The split kernel's tiles hold 16 query rows: it reads the keys once for chunks of up to so many.  Over an 8-bit
-    // cache, which the tile kernel has to widen, reading them twice is no slower (64 x 4 tokens after up to 8191 under 8
-    // heads a cache head, 32 rows: 433 us and 449; 16 x 4 after 3000: 53 and 57; one sequence after 16000: 28.7 and 30.3;
-    // three times: 640 and 453).  The tile kernel loads its queries by TMA, which needs strides.
+    // The split kernel's tiles hold 16 query rows: it reads the keys once for chunks of up to so many. Over an 8-bit
+    // cache it takes up to 32, which reads them twice, for what it keeps: weights in 11 bits or more (the tile kernel
+    // rounds them to the element type) and NaN values with the tokens that see them. Its times at 32 rows (4 tokens of
+    // 8 heads a cache head) and the tile kernel's, us: 64 sequences after 8191, heads of 128: 445 and 355, of 64: 290
+    // and 296; 16 after 3000: 54.7 and 47.0; one after 16000: 29.0 and 28.5. At 16 rows: 231 and 355, 153 and 296, 37.2
+    // and 47.1, 25.7 and 30.0; at 48, heads of 128: 657 and 358. The tile kernel loads its queries by TMA, which needs
+    // strides.
     const long long rows = static_cast<long long>(max_q_len) * (q->heads / cache->heads);
     if (rows <= (k_scales != nullptr ? 32 : 16) || q->token_stride == 0 || q->head_stride == 0)
         return launch_attn_split(a, static_cast<int>(std::min(rows, 1024ll)), static_cast<cudaStream_t>(stream));

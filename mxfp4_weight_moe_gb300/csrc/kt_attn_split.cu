@@ -31,9 +31,11 @@
 // after 60 (no join) 6.1 us.  L2 promotion past a head's row (256 bytes for rows of
 // 128) read 1.39 times the cache.
 // Over 8-bit caches: 64 single tokens after up to 16383, bf16, 64 / 8 heads of 128
-// (1.45 GB), 222 us, 6.6 TB/s (97 %); 4 after up to 131071, fp16, heads of 64 (0.29
-// GB), 67 us, 4.4 TB/s (bound by the arithmetic of 64 elements a key: conversions,
-// and a key's share of the softmax); one after 700 keys, 10.9 us.
+// (1.45 GB), 222 to 232 us on different machines, 6.3 to 6.6 TB/s (93 to 97 %); 4
+// after up to 131071, fp16, heads of 64 (0.29 GB), 68 us, 4.3 TB/s; one after 700
+// keys, 10.9 us.  The heads of 64 are bound by latency: issue slots 51 %, ALU 47 %,
+// DRAM 53 %, tensor pipe 19 %, no unit full; a warp waits 1.4 cycles an instruction
+// for its own last one, 0.6 for loads, 0.4 for a busy unit.
 #include <algorithm>
 #include <type_traits>
 
@@ -56,8 +58,9 @@ struct SplitCfg {
     static constexpr int kUnit = kSplitWarps * kBlockKeys;           // keys of one unit
     static constexpr int kRowBytes = DP * (KV8 ? 1 : 2);             // of a key in a block
     static constexpr int kBlockBytes = kBlockKeys * kRowBytes;       // one of K, V
-    // KV8 heads of 64 wait for the arithmetic (4 x 131k keys: 67 us with three CTAs an SM, 71 with two), of 128 for the
-    // loads (64 single tokens: 222 us with two CTAs, 234 with three, whose rings are smaller)
+    // KV8 heads of 64 wait for the chain of a block's instructions, which more warps hide (4 x 131k keys: 67 us with
+    // three CTAs an SM, 71 with two), of 128 for the loads (64 single tokens: 222 us with two CTAs, 234 with three,
+    // whose rings are smaller)
     static constexpr int kCtasPerSm = ROWS == 8 && DP == 64 ? 3 : 2;
     static constexpr int kStages = kCtasPerSm == 3 ? 2 : 3;          // 24 KB a warp, or 16
     static constexpr int kRing = kStages * 2 * kBlockBytes;          // per warp
@@ -238,8 +241,8 @@ __device__ __forceinline__ uint32_t piece8(uint32_t base, int row, int piece) {
 // exact down to 2^-31 of the row's largest element and off by at most 2^-39 of that below; softmax weights, their
 // value's power included, relative to the largest of the row in the block's 32 or 64 keys, times 2^10: rounded to 11
 // bits down to 2^-24 of that largest and off by at most 2^-35 of it below.  For fp16 results, which have as many bits,
-// the weights go in in two parts (error 1.00 times that of rounding the result once; in one part up to 1.40, for 5 of
-// 67 us of 4 tokens after up to 131071 under heads of 64).
+// the weights go in in two parts (error 1.00 times that of rounding the result once; in one part up to 1.40, for 5 us
+// less of 4 tokens after up to 131071 under heads of 64).
 constexpr float kWeightLog2 = 10.0f;   // the largest weight of a block, log2; O stays multiplied by that to the end
 constexpr float kLeastShareLog2 = -125.0f;   // (a unit above what ex2 flushes)
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }

@@ -56,7 +56,7 @@
 // eight widening warps instead of four (1020 to 1060, the softmax spills), two for
 // keys and two for values (1088 against 1054), the codes of 16 rows loaded ahead
 // (1024), two copies of the loop's body (1230: it and the softmax then do not fit the
-// instruction cache together; 1065 now); more tiles of codes and fewer wide ones in
+// instruction cache together; 1065 with one); more tiles of codes and fewer wide ones in
 // the rings (882 against 863).
 #include <algorithm>
 #include <type_traits>

@@ -270,11 +270,12 @@ static cudaError_t launch_kv8_typed(const Kv8AppendParams& p, HeadRowsParams* q,
     const unsigned blocks = static_cast<unsigned>(first_block(p.tokens, p.seqs)) *
                             static_cast<unsigned>((2 * p.heads + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
     if (q != nullptr && wide) {
-        // One row at a time where there are few, four for the loads under way where there are many (128 tokens of
-        // 64 + 8 heads of 128: 4.16 us one at a time, 3.66 four, with norms 4.2 and 4.6; 250 tokens: 4.2 and 3.9, with
-        // norms 5.5 and 4.9; three prompts of up to 3500 with norms: 83 and 40.3).  Many are marked to leave L2 first,
-        // as in the head-row kernel's launcher.  In a launch of their own the prompts' take 43.5 us, those of 48 single
-        // tokens 4.9, 3.3 here.
+        // One row at a time where there are few, four for the loads under way where there are many (128 tokens of 64 +
+        // 8 heads of 128: 4.16 us one at a time, 3.66 four, with norms 4.2 and 4.6; 250 tokens: 4.2 and 3.9, with norms
+        // 5.5 and 4.9; three prompts of up to 3500 with norms: 83 and 40.3). One border for both, by which 128 tokens
+        // lose 0.5 us without norms and win 0.4 with them. Many rows are marked to leave L2 first, as in the head-row
+        // kernel's launcher. In a launch of their own the prompts' take 43.5 us, those of 48 single tokens 4.9, 3.3
+        // here. (Queries that 16-byte loads do not fit have one.)
         const long long rows = static_cast<long long>(q->tokens) * q->seg[0].heads;
         if (rows < 12288) return launch_kv8_queries<T, 1, false>(p, *q, blocks, s);
         if (rows * q->head_dim * 4 > (128ll << 20)) return launch_kv8_queries<T, 4, true>(p, *q, blocks, s);

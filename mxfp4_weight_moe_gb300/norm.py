@@ -98,7 +98,8 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor |
     type or float32; all 16-byte aligned.  y is there with `plain` (x's type; None without), s with a residual (x's
     type), the pair with `mx`: y in MXFP8, codes uint8 e4m3 [tokens, hidden] and scales uint8 e8m0 [tokens,
     hidden / 32], as forward and MoeLayer take them in place of bf16 tokens (rounded once, from the fp32 y).  hidden: a
-    multiple of 8 (of 32 with mx) up to 32768.  Squares are summed in fp32: where their sum passes 3.4e38, y is zeros.
+    multiple of 8 (of 32 with mx) up to 32768.  Squares are summed in fp32: where their sum passes 3.4e38, y is zeros
+    (with eps 0, where it vanishes, not finite).  A token's bits do not depend on the call's other tokens.
 
     out and residual_out may be x or residual; they share no memory otherwise."""
     if not isinstance(x, torch.Tensor) or x.dtype not in _a.DTYPE_CODES or x.dim() != 2:
