@@ -5,7 +5,7 @@
 // registers as fp32 between its sum of squares and its outputs, so that x and the
 // residual are read once.  A chunk of 8 elements (16 bytes) belongs to one thread;
 // the 32 elements of an MXFP8 scale to four neighbouring lanes.  Bound by memory
-// for many rows (8192 tokens of 7168 in 77.8 us, the measured copy rate), by latency
+// for many rows (8192 tokens of 7168 in 78.0 us, the measured copy rate), by latency
 // for few.
 #include <climits>
 #include <cmath>
@@ -178,7 +178,7 @@ static cudaError_t launch_norm_typed(const NormParams& p, cudaStream_t s) {
     if (chunks <= 32) return launch_norm<T, 1, true>(p, s);
     if (chunks <= 128) return launch_norm<T, 4, true>(p, s);
     // Small steps: a chunk a thread (1 token of 7168: 2.3 us, 2.9 with four; 600 tokens of 2048: 2.4 and 3.3).  Large
-    // ones: four, for the loads under way (8192 tokens of 7168, all outputs, 531 MB: 77.8 us, 6.8 TB/s, and 89.9 with
+    // ones: four, for the loads under way (8192 tokens of 7168, all outputs, 531 MB: 78.0 us, 6.8 TB/s, and 89.9 with
     // one).  They meet at 2 to 4 million elements (450 tokens of 7168: 5.0 and 5.2; 600: 5.8 and 5.0; 2000 of 2048: 5.0
     // and 5.4).
     if (static_cast<long long>(p.tokens) * chunks <= (1 << 19) && chunks <= 1024) return launch_norm<T, 1, false>(p, s);
